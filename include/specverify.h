@@ -25,6 +25,9 @@
  *     FR-Spec / VocabTrim baselines of the DynaSpec summary).
  *   - KV-cache commit of the accepted drafts after a verify step.
  *     Speculative Decoding lesson, "KV-cache management".
+ *   - The same head and commit in an 8-bit block format (rows quantised, the
+ *     head on quantised weights, the cache quantised as it is written and
+ *     read back), and the log-probabilities of the emitted tokens.
  *
  * Conventions shared by every entry point:
  *   - All array arguments are device pointers (hipMalloc / torch CUDA tensors),
@@ -49,6 +52,8 @@ extern "C" {
 
 #define SPEC_ABI_VERSION 2
 #define SPEC_MAX_K 64
+#define SPEC_MAX_TOP 32      /* alternatives per row of spec_token_logprobs */
+#define SPEC_QUANT_BLOCK 128 /* values that share a scale in the 8-bit format */
 
 /*
  * The dtype, mode and status arguments are fixed-width integers with named
@@ -364,6 +369,157 @@ size_t spec_draft_head_static_workspace_bytes(int32_t M, int32_t d, int32_t V, i
 spec_status_t spec_kv_commit(void* cache, const void* staging, const int32_t* accepted_len,
                              int32_t* cache_len, int32_t* status, int32_t P, int32_t B, int32_t K,
                              int32_t L_max, int32_t E, spec_dtype_t dtype, void* stream);
+
+/*
+ * Log-probabilities of given tokens, with the entropy of each row and its
+ * likeliest alternatives: what a server reports for the tokens that a verify
+ * step emitted, from the target rows that the step read.
+ *
+ *   logits         [N, V] of dtype (spec_verify's target_logits with N = B *
+ *                  (K + 1)): finite or -inf.
+ *   tokens         [N] int32 (spec_verify's out_tokens): row i's token.  A row
+ *                  whose token is outside [0, V), such as the -1 after a
+ *                  sequence's last token, is not read.
+ *   temperature    finite, at least the smallest normal float: the law is
+ *                  softmax(logits / T).
+ *   top_n          alternatives per row, 0 .. SPEC_MAX_TOP.
+ *   logprobs       [N] float out: ln P(token); -inf where its logit is -inf.
+ *   entropy        NULL or [N] float out: -sum P ln P, in nats.
+ *   top_ids        [N, top_n] int32 out: the tokens with the largest logits in
+ *                  descending order, equal logits by lower id first.  Tokens
+ *                  at -inf are no alternatives: entries past the others are -1.
+ *   top_logprobs   [N, top_n] float out: their ln P, -inf for an entry of -1.
+ *                  Both may be NULL when top_n == 0.
+ *   workspace      spec_token_logprobs_workspace_bytes(), 256-byte aligned; its
+ *                  contents need no initialisation.
+ * A row that is not read, and one whose largest logit is not finite or that
+ * holds a NaN, gets NaN in its float outputs and -1 in top_ids.
+ * Two launches.  Sums are held in fp32 over 4096 (bf16) or 2048 (fp32) logits
+ * and in fp64 beyond; results do not depend on the launch and are the same on
+ * every call.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, sizes below
+ * zero, V < 1, a temperature outside its range, an unknown dtype;
+ * SPEC_ERR_UNSUPPORTED for top_n > SPEC_MAX_TOP, V > 2^30 or a grid too large
+ * for one launch; SPEC_ERR_WORKSPACE.
+ */
+spec_status_t spec_token_logprobs(const void* logits, const int32_t* tokens, int32_t N, int32_t V,
+                                  spec_dtype_t dtype, float temperature, int32_t top_n, float* logprobs,
+                                  float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of spec_token_logprobs (0 for an empty or invalid shape). */
+size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top_n);
+
+/*
+ * The 8-bit block format.  A row is cut into blocks of SPEC_QUANT_BLOCK = 128
+ * values (the last one may be shorter).  Each block has a scale 2^e, stored as
+ * the e8m0 byte e + 127: e is the smallest integer >= -126 for which the
+ * block's largest finite magnitude is at most 448 * 2^e.  A code is the e4m3
+ * value (8 bits, largest 448, no infinities) nearest to x * 2^-e, ties to
+ * even; x * 2^-e is exact, so codes and scales are fully determined.  Values
+ * that are not finite get a NaN code and do not count for e.  A code c of
+ * the block stands for c * 2^e; read back to bf16 or fp32 this is exact where
+ * it is a normal number of that type.
+ *
+ * spec_quantize_rows: rows of bf16 or fp32 into the format of the drafter
+ * head's operands.
+ *   x       [R, d] of dtype.
+ *   codes   [R, D] bytes out, D = 128 * ceil(d / 128), 16-byte aligned; codes
+ *           past d are zeros.
+ *   scales  [R, ceil(d / 128)] bytes out.
+ * One launch.  16-byte vector loads when d * size is a multiple of 16 and x is
+ * 16-byte aligned (d % 8 == 0 in fp32 too), element loads otherwise.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, R < 0, d < 1
+ * or an unknown dtype; SPEC_ERR_UNSUPPORTED for more than 2^30 - 1 blocks.
+ */
+spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype_t dtype, void* codes,
+                                 void* scales, void* stream);
+
+/*
+ * Drafter head over a static shortlist (spec_draft_head_static) on a weight in
+ * the 8-bit block format, for half the bytes of the bf16 head:
+ *   logits[m, s] = sum_j hq[m, j] * Wq[tok(s), j],  tok(s) = cluster_ids[s / cs] * cs + s % cs,
+ * with Wq the values that the weight's codes stand for and hq those of h's,
+ * quantised by the call's first launch as spec_quantize_rows does; products
+ * are exact and accumulated in fp32 by the matrix cores.  With every cluster
+ * selected it is the head over the whole vocabulary.
+ *
+ *   h            bf16 [M, d].
+ *   W_codes      [V, D] bytes, D = 128 * ceil(d / 128), 16-byte aligned, and
+ *   W_scales     [V, ceil(d / 128)] bytes: spec_quantize_rows of W [V, d].
+ *   cluster_ids  int32 [n_sel] (device), ids in [0, V / cluster_size) in any
+ *                order (the output columns follow it); an id outside that
+ *                range contributes zero columns (not checked on the host).
+ *   logits       [M, N] of out_dtype out, N = n_sel * cluster_size (bf16
+ *                rounds to nearest even).
+ *   workspace    spec_draft_head_quantized_workspace_bytes(), 256-byte
+ *                aligned: h's codes and, where the grid would leave compute
+ *                units idle and d is split over several blocks per output
+ *                tile, their fp32 partial tiles, added in a fixed order by a
+ *                last launch.  The contents need no initialisation.
+ * Results are the same on every call.  Errors: SPEC_ERR_INVALID_ARG for NULL
+ * or misaligned buffers or bad sizes; SPEC_ERR_WORKSPACE; SPEC_ERR_UNSUPPORTED
+ * if V % cluster_size != 0, or for buffers or grids too large.
+ */
+spec_status_t spec_draft_head_quantized(const void* h, const void* W_codes, const void* W_scales,
+                                        const int32_t* cluster_ids, int32_t M, int32_t d, int32_t V,
+                                        int32_t cluster_size, int32_t n_sel, void* logits, spec_dtype_t out_dtype,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of spec_draft_head_quantized (0 for an empty or invalid shape). */
+size_t spec_draft_head_quantized_workspace_bytes(int32_t M, int32_t d, int32_t V, int32_t cluster_size,
+                                                 int32_t n_sel);
+
+/*
+ * KV-cache commit (spec_kv_commit) into a cache in the 8-bit block format:
+ * the accepted drafts' entries are quantised as they are written, for half
+ * the bytes of a bf16 cache.
+ *
+ *   codes        [P, B, L_max, E] bytes and
+ *   scales       [P, B, L_max, ceil(E / 128)] bytes: the cache, updated in
+ *                place.  Each entry of E values is a row of the format; codes
+ *                are not padded.  Entries outside the committed range are
+ *                left as they were.
+ *   staging      [P, B, K, E] of dtype: entries for positions 0..K-1.
+ *   accepted_len [B] int32: entries 0..n-1 go to cache positions
+ *                cache_len[b] .. cache_len[b]+n-1.
+ *   cache_len    [B] int32, and
+ *   new_len      [B] int32 out: cache_len + n where the commit happens, else
+ *                cache_len.  Either cache_len itself (advanced in place, by a
+ *                second launch) or a buffer apart from it (one launch).
+ *   status       [B] int32 out, or NULL: 0 committed; 1 no room (cache_len < 0
+ *                or cache_len + n > L_max); 2 n outside [0, K].  Nothing is
+ *                committed unless 0.
+ * K may be any length: a prompt's entries are committed by the same call.
+ * 8-value vectors when E % 8 == 0, staging is 16-byte and codes 8-byte
+ * aligned; element accesses otherwise.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, negative sizes,
+ * an unknown dtype, sizes that overflow, or lengths and status that overlap;
+ * SPEC_ERR_UNSUPPORTED for a grid too large for one launch.
+ */
+spec_status_t spec_kv_commit_quantized(void* codes, void* scales, const void* staging, const int32_t* accepted_len,
+                                       const int32_t* cache_len, int32_t* new_len, int32_t* status, int32_t P,
+                                       int32_t B, int32_t K, int32_t L_max, int32_t E, spec_dtype_t dtype,
+                                       void* stream);
+
+/*
+ * Reads a cache in the 8-bit block format back as values, for attention over
+ * P of its planes (a layer's keys and values).
+ *
+ *   codes, scales as in spec_kv_commit_quantized, from the first plane read.
+ *   cache_len    [B] int32: entries per sequence.
+ *   out          [P, B, L_out, E] of dtype out: entry j < cache_len[b] of each
+ *                plane and sequence at [p, b, j]; entries from cache_len[b] on
+ *                are left as they were.
+ *   status       [B] int32 out, or NULL: 0 read; 1 length outside [0, min(L_max,
+ *                L_out)], nothing is written for the sequence.
+ * One launch.  8-value vectors when E % 8 == 0, out is 16-byte and codes
+ * 8-byte aligned; element accesses otherwise.  Errors as
+ * spec_kv_commit_quantized's.
+ */
+spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len, void* out,
+                                     int32_t* status, int32_t P, int32_t B, int32_t L_max, int32_t L_out,
+                                     int32_t E, spec_dtype_t dtype, void* stream);
 
 /*
  * Measurement aid, not part of the method: reads `bytes` (a multiple of

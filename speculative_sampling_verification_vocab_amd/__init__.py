@@ -20,7 +20,8 @@ from ._native import SpecVerifyError  # noqa: F401
 
 __all__ = ["spec_verify", "VerifyPlan", "spec_verify_noalloc", "spec_verify_workspace_bytes", "spec_verify_launch_count", "spec_draft_head_shortlist",
            "spec_kv_commit", "spec_verify_sparse_draft", "position_budget", "spec_draft_head_positions",
-           "spec_draft_head_static",
+           "spec_draft_head_static", "spec_quantize_rows", "spec_draft_head_quantized",
+           "spec_kv_commit_quantized", "spec_kv_read_quantized", "spec_token_logprobs",
            "Workspace", "SpecVerifyError", "abi_version"]
 
 _DTYPES = {torch.bfloat16: _native.SPEC_BF16, torch.float32: _native.SPEC_F32}
@@ -481,3 +482,210 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
                                     _stream_handle(h.device, stream))
     _native.check(st, "spec_draft_head_static")
     return out
+
+
+# ---- the 8-bit block format: e4m3 codes, a power-of-two scale per 128 values -----
+
+_BLOCK = 128
+_CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _blocks(n: int) -> int:
+    return -(-int(n) // _BLOCK)
+
+
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    _need_gpu(t, name, device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+
+
+def spec_quantize_rows(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None, stream=None):
+    """Rows into the 8-bit block format (see spec_quantize_rows in specverify.h).
+
+    x [..., d], bf16 or float32.  Returns (codes, scales): float8_e4m3fn
+    [..., D] with D = 128 * ceil(d / 128), zeros past d, and float8_e8m0fnu
+    [..., ceil(d / 128)], or fills the two tensors of `out`.  Value j of a row
+    is codes[..., j].float() * scales[..., j // 128].float()."""
+    _need_gpu(x, "x")
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be bfloat16 or float32 [..., d] with d >= 1")
+    d = x.shape[-1]
+    nb = _blocks(d)
+    lead = tuple(x.shape[:-1])
+    if out is None:
+        codes = torch.empty(lead + (nb * _BLOCK,), dtype=_CODES, device=x.device)
+        scales = torch.empty(lead + (nb,), dtype=_SCALES, device=x.device)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must hold codes and scales")
+        codes, scales = out
+        _need(codes, "codes", _CODES, lead + (nb * _BLOCK,), x.device)
+        _need(scales, "scales", _SCALES, lead + (nb,), x.device)
+    st = _native.load().spec_quantize_rows(_ptr(x), x.numel() // d, d, dt, _ptr(codes), _ptr(scales),
+                                           _stream_handle(x.device, stream))
+    _native.check(st, "spec_quantize_rows")
+    return codes, scales
+
+
+def spec_draft_head_quantized(h: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tensor,
+                              cluster_ids: torch.Tensor, cluster_size: int, dtype: torch.dtype = torch.float32,
+                              out: Optional[torch.Tensor] = None, stream=None,
+                              workspace: Optional[Workspace] = None) -> torch.Tensor:
+    """Drafter head on a weight in the 8-bit block format (see
+    spec_draft_head_quantized in specverify.h).  h bf16 [..., d] (all leading
+    dims are rows; quantised within the call), W_codes and W_scales from
+    spec_quantize_rows of W [V, d], cluster_ids int32 [n_sel].  Returns logits
+    [..., n_sel * cluster_size] of dtype."""
+    for t, name in ((h, "h"), (W_codes, "W_codes"), (W_scales, "W_scales"), (cluster_ids, "cluster_ids")):
+        _need_gpu(t, name, h.device)
+    if h.dtype != torch.bfloat16 or h.dim() < 1 or h.shape[-1] < 1:
+        raise ValueError("h must be bfloat16 [..., d] with d >= 1")
+    d = h.shape[-1]
+    nb = _blocks(d)
+    if W_codes.dim() != 2:
+        raise ValueError("W_codes must be [V, 128 * ceil(d / 128)]")
+    V = W_codes.shape[0]
+    _need(W_codes, "W_codes", _CODES, (V, nb * _BLOCK), h.device)
+    _need(W_scales, "W_scales", _SCALES, (V, nb), h.device)
+    if cluster_ids.dtype != torch.int32 or cluster_ids.dim() != 1:
+        raise ValueError("cluster_ids must be int32 [n_sel]")
+    cluster_size = int(cluster_size)
+    n_sel = cluster_ids.numel()
+    M = h.numel() // d
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("dtype must be bfloat16 or float32")
+    shape = tuple(h.shape[:-1]) + (n_sel * cluster_size,)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=h.device)
+    else:
+        _need(out, "out", dtype, shape, h.device)
+    lib = _native.load()
+    need = lib.spec_draft_head_quantized_workspace_bytes(M, d, V, cluster_size, n_sel)
+    ws, wsb = None, 0
+    if need:
+        buf = (workspace or _workspace_for(h.device, stream)).get(need, stream, h.device)
+        ws, wsb = _ptr(buf), buf.numel()
+    st = lib.spec_draft_head_quantized(_ptr(h), _ptr(W_codes), _ptr(W_scales), _ptr(cluster_ids), M, d, V,
+                                       cluster_size, n_sel, _ptr(out), dt, ws, wsb, _stream_handle(h.device, stream))
+    _native.check(st, "spec_draft_head_quantized")
+    return out
+
+
+def _kv_shape(codes: torch.Tensor, scales: torch.Tensor):
+    """(P, B, L_max, E) of a quantised cache, after its checks."""
+    _need_gpu(codes, "codes")
+    if codes.dtype != _CODES or codes.dim() < 3:
+        raise ValueError(f"codes must be {_CODES} [P, B, L_max, ...]")
+    P, B, Lmax = codes.shape[:3]
+    E = 1
+    for x in codes.shape[3:]:
+        E *= int(x)
+    _need(scales, "scales", _SCALES, (P, B, Lmax, _blocks(E)), codes.device)
+    return P, B, Lmax, E
+
+
+def _kv_ints(t: Optional[torch.Tensor], name: str, B: int, device: torch.device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(B, dtype=torch.int32, device=device)
+    _need(t, name, torch.int32, (B,), device)
+    return t
+
+
+def spec_kv_commit_quantized(codes: torch.Tensor, scales: torch.Tensor, staging: torch.Tensor,
+                             accepted_len: torch.Tensor, cache_len: torch.Tensor,
+                             new_len: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """Commit the accepted drafts' KV entries into a cache in the 8-bit block
+    format (see spec_kv_commit_quantized in specverify.h).
+
+    codes float8_e4m3fn [P, B, L_max, ...] (E values per entry), scales
+    float8_e8m0fnu [P, B, L_max, ceil(E / 128)], staging [P, B, K, ...] bf16 or
+    float32 with the same trailing shape, accepted_len and cache_len int32
+    [B].  cache_len is advanced in place, or left alone when new_len (int32
+    [B]) takes the new lengths, which saves a launch.  Returns the status tensor
+    (int32 [B]: 0 committed, 1 no room, 2 accepted_len outside [0, K])."""
+    P, B, Lmax, E = _kv_shape(codes, scales)
+    dev = codes.device
+    _need_gpu(staging, "staging", dev)
+    dt = _DTYPES.get(staging.dtype)
+    if dt is None:
+        raise ValueError("staging must be bfloat16 or float32")
+    if staging.dim() != codes.dim() or staging.shape[:2] != codes.shape[:2] or staging.shape[3:] != codes.shape[3:]:
+        raise ValueError("staging must be [P, B, K, ...] with the trailing shape of codes")
+    K = staging.shape[2]
+    _need(accepted_len, "accepted_len", torch.int32, (B,), dev)
+    _need(cache_len, "cache_len", torch.int32, (B,), dev)
+    new_len = cache_len if new_len is None else _kv_ints(new_len, "new_len", B, dev)
+    status = _kv_ints(status, "status", B, dev)
+    st = _native.load().spec_kv_commit_quantized(_ptr(codes), _ptr(scales), _ptr(staging), _ptr(accepted_len),
+                                                 _ptr(cache_len), _ptr(new_len), _ptr(status), P, B, K, Lmax, E, dt,
+                                                 _stream_handle(dev, stream))
+    _native.check(st, "spec_kv_commit_quantized")
+    return status
+
+
+def spec_kv_read_quantized(codes: torch.Tensor, scales: torch.Tensor, cache_len: torch.Tensor, out: torch.Tensor,
+                           status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Read a cache in the 8-bit block format back (see spec_kv_read_quantized in specverify.h).
+
+    codes and scales as in spec_kv_commit_quantized (or a contiguous run of its
+    planes), cache_len int32 [B], out [P, B, L_out, ...] bf16 or float32 with
+    the trailing shape of codes: entries 0 .. cache_len[b] - 1 of every plane
+    are written, the others left as they were.  Returns the status tensor
+    (int32 [B]: 0 read, 1 length outside [0, min(L_max, L_out)])."""
+    P, B, Lmax, E = _kv_shape(codes, scales)
+    dev = codes.device
+    _need_gpu(out, "out", dev)
+    dt = _DTYPES.get(out.dtype)
+    if dt is None:
+        raise ValueError("out must be bfloat16 or float32")
+    if out.dim() != codes.dim() or out.shape[:2] != codes.shape[:2] or out.shape[3:] != codes.shape[3:]:
+        raise ValueError("out must be [P, B, L_out, ...] with the trailing shape of codes")
+    _need(cache_len, "cache_len", torch.int32, (B,), dev)
+    status = _kv_ints(status, "status", B, dev)
+    st = _native.load().spec_kv_read_quantized(_ptr(codes), _ptr(scales), _ptr(cache_len), _ptr(out), _ptr(status),
+                                               P, B, Lmax, out.shape[2], E, dt, _stream_handle(dev, stream))
+    _native.check(st, "spec_kv_read_quantized")
+    return status
+
+
+# ---- log-probabilities of the emitted tokens --------------------------------------
+
+def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, temperature: float = 1.0, *,
+                        workspace: Optional[Workspace] = None, stream=None):
+    """Log-probabilities of given tokens (see spec_token_logprobs in specverify.h).
+
+    logits [..., V] (bf16 or float32), tokens int32 [...]: spec_verify's target
+    and out_tokens.  Returns (logprobs float32 [...], entropy float32 [...],
+    top_ids int32 [..., top_n], top_logprobs float32 [..., top_n]) under
+    softmax(logits / temperature).  A row whose token is outside [0, V) (the -1
+    after a sequence's last token) is not read: NaN, and -1 in top_ids."""
+    _need_gpu(logits, "logits")
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None or logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError("logits must be bfloat16 or float32 [..., V] with V >= 1")
+    V = logits.shape[-1]
+    lead = tuple(logits.shape[:-1])
+    dev = logits.device
+    _need(tokens, "tokens", torch.int32, lead, dev)
+    top_n = int(top_n)
+    if top_n < 0:
+        raise ValueError("top_n must be >= 0")
+    N = tokens.numel()
+    lp = torch.empty(lead, dtype=torch.float32, device=dev)
+    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+    ids = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev)
+    top = torch.empty(lead + (top_n,), dtype=torch.float32, device=dev)
+    lib = _native.load()
+    need = lib.spec_token_logprobs_workspace_bytes(N, V, dt, top_n)
+    ws, wsb = None, 0
+    if need:
+        buf = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
+        ws, wsb = _ptr(buf), buf.numel()
+    st = lib.spec_token_logprobs(_ptr(logits), _ptr(tokens), N, V, dt, ctypes.c_float(temperature), top_n, _ptr(lp),
+                                 _ptr(entropy), _ptr(ids), _ptr(top), ws, wsb, _stream_handle(dev, stream))
+    _native.check(st, "spec_token_logprobs")
+    return lp, entropy, ids, top

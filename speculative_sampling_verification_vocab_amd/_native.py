@@ -75,6 +75,20 @@ def load() -> ctypes.CDLL:
         lib.spec_position_budget.restype = i32
         lib.spec_kv_commit.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, ctypes.c_int, P]
         lib.spec_kv_commit.restype = ctypes.c_int
+        lib.spec_quantize_rows.argtypes = [P, i32, i32, ctypes.c_int, P, P, P]
+        lib.spec_quantize_rows.restype = ctypes.c_int
+        lib.spec_draft_head_quantized.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, ctypes.c_int, P, sz, P]
+        lib.spec_draft_head_quantized.restype = ctypes.c_int
+        lib.spec_draft_head_quantized_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.spec_draft_head_quantized_workspace_bytes.restype = sz
+        lib.spec_kv_commit_quantized.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, ctypes.c_int, P]
+        lib.spec_kv_commit_quantized.restype = ctypes.c_int
+        lib.spec_kv_read_quantized.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, ctypes.c_int, P]
+        lib.spec_kv_read_quantized.restype = ctypes.c_int
+        lib.spec_token_logprobs.argtypes = [P, P, i32, i32, ctypes.c_int, ctypes.c_float, i32, P, P, P, P, P, sz, P]
+        lib.spec_token_logprobs.restype = ctypes.c_int
+        lib.spec_token_logprobs_workspace_bytes.argtypes = [i32, i32, ctypes.c_int, i32]
+        lib.spec_token_logprobs_workspace_bytes.restype = sz
         _lib = lib
         return lib
 

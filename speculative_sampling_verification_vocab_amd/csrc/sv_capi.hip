@@ -277,6 +277,98 @@ spec_status_t spec_kv_commit(void* cache, const void* staging, const int32_t* ac
   return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
+spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype_t dtype, void* codes, void* scales,
+                                 void* stream) {
+  bool empty = false;
+  const spec_status_t sc = sv::validate_quantize_rows(x, R, d, dtype, codes, scales, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_quantize_rows(x, R, d, dtype == SPEC_BF16 ? 1 : 0, codes, scales,
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+size_t spec_draft_head_quantized_workspace_bytes(int32_t M, int32_t d, int32_t V, int32_t cluster_size,
+                                                 int32_t n_sel) {
+  sv::HeadQPlan plan{};
+  sv::HeadQWorkspace w{};
+  bool empty = false;
+  const spec_status_t sc = sv::check_head_quantized(M, d, V, cluster_size, n_sel, &plan, &w, &empty);
+  return sc != SPEC_OK || empty ? 0 : w.total;
+}
+
+spec_status_t spec_draft_head_quantized(const void* h, const void* W_codes, const void* W_scales,
+                                        const int32_t* cluster_ids, int32_t M, int32_t d, int32_t V,
+                                        int32_t cluster_size, int32_t n_sel, void* logits, spec_dtype_t out_dtype,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  sv::HeadQPlan plan{};
+  sv::HeadQWorkspace w{};
+  bool empty = false;
+  const spec_status_t sc =
+      sv::validate_head_quantized(h, W_codes, W_scales, cluster_ids, M, d, V, cluster_size, n_sel, logits, out_dtype,
+                                  workspace, workspace_bytes, &plan, &w, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_head_quantized(h, W_codes, W_scales, cluster_ids, M, d, V, cluster_size, n_sel,
+                                                 logits, out_dtype == SPEC_BF16 ? 1 : 0, plan, w, workspace,
+                                                 static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+spec_status_t spec_kv_commit_quantized(void* codes, void* scales, const void* staging, const int32_t* accepted_len,
+                                       const int32_t* cache_len, int32_t* new_len, int32_t* status, int32_t P,
+                                       int32_t B, int32_t K, int32_t L_max, int32_t E, spec_dtype_t dtype,
+                                       void* stream) {
+  sv::KvQPlan plan{};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_kv_commit_quantized(codes, scales, staging, accepted_len, cache_len, new_len,
+                                                            status, P, B, K, L_max, E, dtype, &plan, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_kv_commit_quantized(codes, scales, staging, accepted_len, cache_len, new_len, status,
+                                                      P, B, K, L_max, E, dtype == SPEC_BF16 ? 1 : 0, plan,
+                                                      static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len, void* out,
+                                     int32_t* status, int32_t P, int32_t B, int32_t L_max, int32_t L_out, int32_t E,
+                                     spec_dtype_t dtype, void* stream) {
+  sv::KvQPlan plan{};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_kv_read_quantized(codes, scales, cache_len, out, status, P, B, L_max, L_out, E,
+                                                          dtype, &plan, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_kv_read_quantized(codes, scales, cache_len, out, status, P, B, L_max, L_out, E,
+                                                    dtype == SPEC_BF16 ? 1 : 0, plan,
+                                                    static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top_n) {
+  sv::LogprobsShape s{};
+  sv::LogprobsWorkspace w{};
+  return sv::check_logprobs(N, V, dtype, top_n, &s, &w) == SPEC_OK && N > 0 ? w.total : 0;
+}
+
+spec_status_t spec_token_logprobs(const void* logits, const int32_t* tokens, int32_t N, int32_t V,
+                                  spec_dtype_t dtype, float temperature, int32_t top_n, float* logprobs,
+                                  float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  sv::LogprobsShape s{};
+  sv::LogprobsWorkspace w{};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_logprobs(logits, tokens, N, V, dtype, temperature, top_n, logprobs, entropy,
+                                                 top_ids, top_logprobs, workspace, workspace_bytes, &s, &w, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_logprobs(s, w, logits, tokens, dtype == SPEC_BF16 ? 1 : 0, temperature, logprobs,
+                                           entropy, top_ids, top_logprobs, workspace,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
 spec_status_t spec_read_stream_probe(const void* src, size_t bytes, void* sink, void* stream) {
   if (!src || !sink || bytes == 0 || bytes % 32768 != 0 || (uintptr_t)src % 16 != 0 || (uintptr_t)sink % 4 != 0)
     return SPEC_ERR_INVALID_ARG;

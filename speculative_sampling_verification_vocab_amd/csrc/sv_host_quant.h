@@ -1,0 +1,284 @@
+// Host half of the 8-bit operators and the token log-probabilities: geometry
+// and argument checks.  Plain C++ with no HIP types, like sv_host.h.
+#pragma once
+
+#include "sv_host.h"
+
+namespace sv {
+
+constexpr int kQuantBlock = SPEC_QUANT_BLOCK;  // values that share a scale
+
+inline int32_t quant_blocks(int32_t d) { return d / kQuantBlock + (d % kQuantBlock != 0); }
+
+// a * b and a + b in size_t with a flag for overflow (byte counts of buffers).
+inline bool mul_fits(size_t a, size_t b, size_t limit, size_t* out) {
+  if (b != 0 && a > limit / b) return false;
+  *out = a * b;
+  return true;
+}
+
+constexpr size_t kMaxBytes = SIZE_MAX / 4;  // byte counts of one buffer; offsets then fit 63 bits
+
+// Blocks of `threads` threads that one launch can have: the grid's threads
+// are counted in 32 bits.
+constexpr size_t max_blocks(int threads) { return 0xffffffffu / (unsigned)threads; }
+
+// [p, p + bytes) and [q, q + q_bytes) share a byte.
+inline bool overlap(const void* p, size_t bytes, const void* q, size_t q_bytes) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return bytes != 0 && q_bytes != 0 && a < b + q_bytes && b < a + bytes;
+}
+
+// ---- rows -----------------------------------------------------------------------
+
+// spec_quantize_rows; *empty when there is nothing to launch.
+inline spec_status_t validate_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype_t dtype,
+                                            const void* codes, const void* scales, bool* empty) {
+  if (!valid_dtype(dtype) || R < 0 || d < 1) return SPEC_ERR_INVALID_ARG;
+  *empty = R == 0;
+  if (*empty) return SPEC_OK;
+  if (!x || !codes || !scales) return SPEC_ERR_INVALID_ARG;
+  if ((uintptr_t)x % elem_size(dtype) || (uintptr_t)codes % 16) return SPEC_ERR_INVALID_ARG;
+  const size_t blocks = (size_t)R * (size_t)quant_blocks(d);
+  // Block numbers stay in int32 with the grid's round-up, 16 lanes each in its threads (four per lane in long grids).
+  if (blocks > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+// ---- drafter head ---------------------------------------------------------------
+
+// Launch plan of spec_draft_head_quantized: the tile that a block computes and
+// the number of blocks that share a tile's sum.
+struct HeadQPlan {
+  int tile;    // index of the compiled tile (see launch_head_quantized)
+  int mt, nt;  // its rows and columns
+  int split;   // blocks per tile, each over a slice of the blocks of 128
+};
+
+constexpr int kHeadQCUs = 256;     // compute units that a grid should reach
+constexpr int kHeadQMaxSplit = 8;
+
+inline HeadQPlan head_quantized_plan(int32_t M, int32_t d, int32_t N) {
+  HeadQPlan p{};
+  const long long nb = quant_blocks(d);
+  auto tiles = [&](int mt, int nt) {
+    return ((long long)M + mt - 1) / mt * (((long long)N + nt - 1) / nt);
+  };
+  if (M <= 16) p.tile = 0, p.mt = 16, p.nt = 32;
+  else if (M <= 32) p.tile = 1, p.mt = 32, p.nt = 32;
+  else if (M <= 64) p.tile = 2, p.mt = 64, p.nt = 64;
+  else p.tile = 3, p.mt = 128, p.nt = 128;
+  long long s = kHeadQCUs / (tiles(p.mt, p.nt) > 0 ? tiles(p.mt, p.nt) : 1);
+  if (s > kHeadQMaxSplit) s = kHeadQMaxSplit;
+  if (s > nb / 4) s = nb / 4;  // at least four blocks of 128 per slice
+  p.split = s < 1 ? 1 : (int)s;
+  return p;
+}
+
+// Workspace of spec_draft_head_quantized: h's codes and scales, then the
+// slices' fp32 partial tiles (split > 1).
+struct HeadQWorkspace {
+  size_t codes, scales, partial, total;  // byte offsets
+};
+
+inline bool head_quantized_layout(int32_t M, int32_t d, int32_t N, const HeadQPlan& p, HeadQWorkspace* w) {
+  const size_t nb = (size_t)quant_blocks(d);
+  size_t a = 0, b = 0, c = 0;
+  if (!mul_fits((size_t)M, nb * kQuantBlock, kMaxBytes, &a) || !mul_fits((size_t)M, nb, kMaxBytes, &b)) return false;
+  if (p.split > 1 && !mul_fits((size_t)M * (size_t)N, (size_t)p.split * sizeof(float), kMaxBytes, &c)) return false;
+  w->codes = 0;
+  w->scales = align256(a);
+  w->partial = w->scales + align256(b);
+  w->total = w->partial + align256(c);
+  return true;
+}
+
+// The sizes of spec_draft_head_quantized (workspace sizing and the call).
+inline spec_status_t check_head_quantized(int32_t M, int32_t d, int32_t V, int32_t cluster_size, int32_t n_sel,
+                                          HeadQPlan* plan, HeadQWorkspace* w, bool* empty) {
+  if (M < 0 || d < 1 || V < 1 || cluster_size < 1 || n_sel < 0) return SPEC_ERR_INVALID_ARG;
+  if (V % cluster_size != 0) return SPEC_ERR_UNSUPPORTED;
+  if (n_sel > V / cluster_size) return SPEC_ERR_INVALID_ARG;
+  *empty = M == 0 || n_sel == 0;
+  if (*empty) return SPEC_OK;
+  const int32_t N = n_sel * cluster_size;  // at most V
+  if (d > 0x7fffffff - kQuantBlock) return SPEC_ERR_UNSUPPORTED;
+  *plan = head_quantized_plan(M, d, N);
+  if (!head_quantized_layout(M, d, N, *plan, w)) return SPEC_ERR_UNSUPPORTED;
+  size_t out = 0, wb = 0;
+  if (!mul_fits((size_t)M * (size_t)N, 4, kMaxBytes, &out)) return SPEC_ERR_UNSUPPORTED;
+  if (!mul_fits((size_t)V, (size_t)quant_blocks(d) * kQuantBlock, kMaxBytes, &wb)) return SPEC_ERR_UNSUPPORTED;
+  const unsigned long long tiles = (((unsigned long long)M + plan->mt - 1) / plan->mt) *
+                                   (((unsigned long long)N + plan->nt - 1) / plan->nt) * plan->split;
+  if (tiles > max_blocks(512) || (size_t)M * (size_t)quant_blocks(d) > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;
+  if (((size_t)M * (size_t)N + 1023) / 1024 > max_blocks(256)) return SPEC_ERR_UNSUPPORTED;  // the sum of partials
+  return SPEC_OK;
+}
+
+// spec_draft_head_quantized.
+inline spec_status_t validate_head_quantized(const void* h, const void* W_codes, const void* W_scales,
+                                             const int32_t* cluster_ids, int32_t M, int32_t d, int32_t V,
+                                             int32_t cluster_size, int32_t n_sel, const void* logits,
+                                             spec_dtype_t out_dtype, const void* workspace, size_t workspace_bytes,
+                                             HeadQPlan* plan, HeadQWorkspace* w, bool* empty) {
+  if (!valid_dtype(out_dtype)) return SPEC_ERR_INVALID_ARG;
+  const spec_status_t sc = check_head_quantized(M, d, V, cluster_size, n_sel, plan, w, empty);
+  if (sc != SPEC_OK || *empty) return sc;
+  if (!h || !W_codes || !W_scales || !cluster_ids || !logits) return SPEC_ERR_INVALID_ARG;
+  if ((uintptr_t)h % 2 || (uintptr_t)W_codes % 16 || (uintptr_t)cluster_ids % 4 ||
+      (uintptr_t)logits % elem_size(out_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < w->total) return SPEC_ERR_WORKSPACE;
+  return SPEC_OK;
+}
+
+// ---- KV cache -------------------------------------------------------------------
+
+// What both cache calls launch: 8-value units of a row, whole blocks of 16.
+struct KvQPlan {
+  bool copies;      // there is something to move
+  bool vec;         // whole 8-value units at aligned addresses
+  int32_t nb;       // blocks of 128 per row
+  uint32_t chunks;  // blocks of threads per (plane, sequence)
+  int32_t unroll;   // units per thread
+};
+
+// Sizes shared by the cache calls: rows is the longer row count of the two
+// buffers, row_units the units that one (plane, sequence) can have.
+inline spec_status_t check_kv_quantized(int32_t P, int32_t B, int32_t rows_move, int32_t rows_a, int32_t rows_b,
+                                        int32_t E, spec_dtype_t dtype, KvQPlan* plan) {
+  const size_t planes = (size_t)P * (size_t)B;
+  if (planes > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
+  size_t rows = 0, bytes = 0;
+  if (!mul_fits(planes, (size_t)(rows_a > rows_b ? rows_a : rows_b), kMaxBytes, &rows) ||
+      !mul_fits(rows, (size_t)E * elem_size(dtype), kMaxBytes, &bytes))
+    return SPEC_ERR_INVALID_ARG;
+  plan->copies = P > 0 && rows_move > 0 && E > 0;
+  plan->vec = false;
+  plan->nb = quant_blocks(E);
+  plan->chunks = 0;
+  plan->unroll = 1;
+  if (!plan->copies) return SPEC_OK;
+  const size_t units = (size_t)rows_move * (size_t)plan->nb * 16;
+  if (units > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;  // unit numbers stay in int32
+  // Four units per thread where that still gives every CU several blocks.
+  plan->unroll = planes * ((units + 4 * kBlock - 1) / (4 * kBlock)) >= 4 * 256 ? 4 : 1;
+  plan->chunks = (uint32_t)((units + (size_t)plan->unroll * kBlock - 1) / ((size_t)plan->unroll * kBlock));
+  if (plan->chunks * planes > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+// spec_kv_commit_quantized; *empty when there is nothing to launch.
+inline spec_status_t validate_kv_commit_quantized(const void* codes, const void* scales, const void* staging,
+                                                  const int32_t* accepted_len, const int32_t* cache_len,
+                                                  const int32_t* new_len, const int32_t* status, int32_t P,
+                                                  int32_t B, int32_t K, int32_t L_max, int32_t E,
+                                                  spec_dtype_t dtype, KvQPlan* plan, bool* empty) {
+  if (!valid_dtype(dtype)) return SPEC_ERR_INVALID_ARG;
+  if (P < 0 || B < 0 || K < 0 || L_max < 0 || E < 0) return SPEC_ERR_INVALID_ARG;
+  *empty = B == 0;
+  if (*empty) return SPEC_OK;
+  if (!accepted_len || !cache_len || !new_len) return SPEC_ERR_INVALID_ARG;
+  if ((uintptr_t)accepted_len % 4 || (uintptr_t)cache_len % 4 || (uintptr_t)new_len % 4 || (uintptr_t)status % 4)
+    return SPEC_ERR_INVALID_ARG;
+  // Blocks read accepted_len and cache_len while others write the outputs:
+  // new_len is cache_len itself (the lengths then follow in a launch of their
+  // own) or apart from every input.
+  const size_t lens = (size_t)B * 4;
+  if (new_len != cache_len && overlap(new_len, lens, cache_len, lens)) return SPEC_ERR_INVALID_ARG;
+  if (overlap(new_len, lens, accepted_len, lens)) return SPEC_ERR_INVALID_ARG;
+  if (status && (overlap(status, lens, accepted_len, lens) || overlap(status, lens, cache_len, lens) ||
+                 overlap(status, lens, new_len, lens)))
+    return SPEC_ERR_INVALID_ARG;
+  const spec_status_t sc = check_kv_quantized(P, B, K, K, L_max, E, dtype, plan);
+  if (sc != SPEC_OK || !plan->copies) return sc;
+  if (!codes || !scales || !staging || (uintptr_t)staging % elem_size(dtype)) return SPEC_ERR_INVALID_ARG;
+  plan->vec = E % 8 == 0 && (uintptr_t)staging % 16 == 0 && (uintptr_t)codes % 8 == 0;
+  return SPEC_OK;
+}
+
+// spec_kv_read_quantized; *empty when there is nothing to launch.
+inline spec_status_t validate_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len,
+                                                const void* out, const int32_t* status, int32_t P, int32_t B,
+                                                int32_t L_max, int32_t L_out, int32_t E, spec_dtype_t dtype,
+                                                KvQPlan* plan, bool* empty) {
+  if (!valid_dtype(dtype)) return SPEC_ERR_INVALID_ARG;
+  if (P < 0 || B < 0 || L_max < 0 || L_out < 0 || E < 0) return SPEC_ERR_INVALID_ARG;
+  *empty = B == 0;
+  if (*empty) return SPEC_OK;
+  if (!cache_len || (uintptr_t)cache_len % 4 || (uintptr_t)status % 4) return SPEC_ERR_INVALID_ARG;
+  if (status && overlap(status, (size_t)B * 4, cache_len, (size_t)B * 4)) return SPEC_ERR_INVALID_ARG;
+  const int32_t rows = L_max < L_out ? L_max : L_out;
+  const spec_status_t sc = check_kv_quantized(P, B, rows, L_max, L_out, E, dtype, plan);
+  if (sc != SPEC_OK || !plan->copies) return sc;
+  if (!codes || !scales || !out || (uintptr_t)out % elem_size(dtype)) return SPEC_ERR_INVALID_ARG;
+  plan->vec = E % 8 == 0 && (uintptr_t)out % 16 == 0 && (uintptr_t)codes % 8 == 0;
+  return SPEC_OK;
+}
+
+// ---- token log-probabilities ----------------------------------------------------
+
+// One tile of the statistics pass: one wave, 8 chunks of 64 16-byte vectors.
+// Tiles and chunks lie on a row's 16-byte grid: a row that does not begin on
+// a 16-byte boundary begins inside its first vector.
+struct LogprobsShape {
+  int N, V;
+  int vec;     // values per 16 bytes
+  int tile;    // values per tile
+  int NT;      // tiles per row (enough for any alignment)
+  int groups;  // blocks of four tiles per row
+  int top;
+};
+
+constexpr int kMaxTop = SPEC_MAX_TOP;
+constexpr int kChunksPerTile = 8;
+
+struct LogprobsTile {
+  double ref;  // the tile's reference, in units of log 2: sums are of 2^(x * s - ref)
+  float z;     // sum of e = 2^(x * s - ref)
+  float h;     // sum of e * (x * s - ref)
+};
+
+struct LogprobsWorkspace {
+  size_t tiles, chunks, total;  // byte offsets
+};
+
+inline spec_status_t check_logprobs(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top, LogprobsShape* s,
+                                    LogprobsWorkspace* w) {
+  if (!valid_dtype(dtype) || N < 0 || V < 1 || top < 0) return SPEC_ERR_INVALID_ARG;
+  if (V > (1 << 30) || top > kMaxTop) return SPEC_ERR_UNSUPPORTED;
+  s->N = N;
+  s->V = V;
+  s->vec = 16 / (int)elem_size(dtype);
+  s->tile = kWave * s->vec * kChunksPerTile;
+  s->NT = (V + s->vec - 1 + s->tile - 1) / s->tile;
+  s->groups = (s->NT + kWavesPerBlock - 1) / kWavesPerBlock;
+  s->top = top;
+  if ((size_t)N * (size_t)s->groups > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
+  w->tiles = 0;
+  w->chunks = align256((size_t)N * s->NT * sizeof(LogprobsTile));
+  w->total = w->chunks + (top > 0 ? align256((size_t)N * s->NT * kChunksPerTile * sizeof(float)) : 0);
+  return SPEC_OK;
+}
+
+// spec_token_logprobs; *empty when there is nothing to launch.
+inline spec_status_t validate_logprobs(const void* logits, const int32_t* tokens, int32_t N, int32_t V,
+                                       spec_dtype_t dtype, float temperature, int32_t top, const float* logprobs,
+                                       const float* entropy, const int32_t* top_ids, const float* top_logprobs,
+                                       const void* workspace, size_t workspace_bytes, LogprobsShape* s,
+                                       LogprobsWorkspace* w, bool* empty) {
+  const spec_status_t sc = check_logprobs(N, V, dtype, top, s, w);
+  if (sc != SPEC_OK) return sc;
+  // log2(e) / T must be a finite float: T at or above the least normal one.
+  if (!(temperature >= 1.17549435e-38f && isfinite(temperature))) return SPEC_ERR_INVALID_ARG;
+  *empty = N == 0;
+  if (*empty) return SPEC_OK;
+  if (!logits || !tokens || !logprobs || (top > 0 && (!top_ids || !top_logprobs))) return SPEC_ERR_INVALID_ARG;
+  if ((uintptr_t)logits % elem_size(dtype) || (uintptr_t)tokens % 4 || (uintptr_t)logprobs % 4 ||
+      (uintptr_t)entropy % 4 || (uintptr_t)top_ids % 4 || (uintptr_t)top_logprobs % 4)
+    return SPEC_ERR_INVALID_ARG;
+  if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < w->total) return SPEC_ERR_WORKSPACE;
+  return SPEC_OK;
+}
+
+}  // namespace sv

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "sv_host.h"
+#include "sv_host_quant.h"
 
 namespace sv {
 
@@ -46,5 +47,28 @@ hipError_t launch_read_stream(const void* src, size_t bytes, void* sink, hipStre
 hipError_t launch_kv_commit(void* cache, const void* staging, const int32_t* accepted_len, int32_t* cache_len,
                             int32_t* status, int P, int B, int K, int Lmax, int64_t row_bytes, int elem_bytes,
                             bool vec_ok, hipStream_t st);
+
+// Rows into the 8-bit block format (one launch).
+hipError_t launch_quantize_rows(const void* x, int R, int d, int dtype, void* codes, void* scales, hipStream_t st);
+
+// Head on a quantised weight: h's rows quantised into the workspace, the
+// product, and with plan.split > 1 the sum of the slices.
+hipError_t launch_head_quantized(const void* h, const void* W_codes, const void* W_scales, const int32_t* cluster_ids,
+                                 int M, int d, int V, int cluster_size, int n_sel, void* out, int out_dtype,
+                                 const HeadQPlan& plan, const HeadQWorkspace& w, void* workspace, hipStream_t st);
+
+// Quantised KV cache: commit (one launch, or two when new_len is cache_len)
+// and read (one launch).
+hipError_t launch_kv_commit_quantized(void* codes, void* scales, const void* staging, const int32_t* accepted_len,
+                                      const int32_t* cache_len, int32_t* new_len, int32_t* status, int P, int B, int K,
+                                      int Lmax, int E, int dtype, const KvQPlan& plan, hipStream_t st);
+hipError_t launch_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len, void* out,
+                                    int32_t* status, int P, int B, int Lmax, int Lout, int E, int dtype,
+                                    const KvQPlan& plan, hipStream_t st);
+
+// Token log-probabilities: tiles, then pick (two launches).
+hipError_t launch_logprobs(const LogprobsShape& s, const LogprobsWorkspace& w, const void* logits,
+                           const int32_t* tokens, int dtype, float temperature, float* logprobs, float* entropy,
+                           int32_t* top_ids, float* top_logprobs, void* workspace, hipStream_t st);
 
 }  // namespace sv
