@@ -390,13 +390,13 @@ spec_status_t spec_kv_commit(void* cache, const void* staging, const int32_t* ac
  *                  at -inf are no alternatives: entries past the others are -1.
  *   top_logprobs   [N, top_n] float out: their ln P, -inf for an entry of -1.
  *                  Both may be NULL when top_n == 0.
- *   workspace      spec_token_logprobs_workspace_bytes(), 256-byte aligned; its
- *                  contents need no initialisation.
+ *   workspace      spec_token_logprobs_workspace_bytes(), 256-byte aligned (may
+ *                  be NULL where that is 0); its contents need no initialisation.
  * A row that is not read, and one whose largest logit is not finite or that
  * holds a NaN, gets NaN in its float outputs and -1 in top_ids.
- * Two launches.  Sums are held in fp32 over 4096 (bf16) or 2048 (fp32) logits
- * and in fp64 beyond; results do not depend on the launch and are the same on
- * every call.
+ * One launch for short rows and small batches, two for the others.  Sums are
+ * held in fp32 over a lane's 64 (bf16) or 32 (fp32) logits of a tile and in
+ * fp64 beyond; results are the same on every call.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, sizes below
  * zero, V < 1, a temperature outside its range, an unknown dtype;
  * SPEC_ERR_UNSUPPORTED for top_n > SPEC_MAX_TOP, V > 2^30 or a grid too large
@@ -407,7 +407,7 @@ spec_status_t spec_token_logprobs(const void* logits, const int32_t* tokens, int
                                   float* entropy, int32_t* top_ids, float* top_logprobs, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of spec_token_logprobs (0 for an empty or invalid shape). */
+/* Workspace bytes of spec_token_logprobs (0: none is needed, or the shape is invalid). */
 size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top_n);
 
 /*

@@ -11,6 +11,7 @@ same device.  See include/specverify.h for the full contract.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -485,19 +486,58 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
 
 
 # ---- the 8-bit block format: e4m3 codes, a power-of-two scale per 128 values -----
+#
+# The smallest calls take a few microseconds on the GPU, about what a call
+# costs on the host, so these functions check each tensor in one expression,
+# ask torch for the raw stream handle (0.1 us against 1.9 us for the Stream
+# object) and keep the default workspace at hand.
 
 _BLOCK = 128
 _CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
-
-
-def _blocks(n: int) -> int:
-    return -(-int(n) // _BLOCK)
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
-    _need_gpu(t, name, device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _need_gpu(t, name, device)
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
+
+
+def _raw_stream(device: torch.device, stream=None) -> int:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}, the device of the call's tensors")
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Workspace], stream) -> torch.Tensor:
+    """At least `need` bytes of workspace: the caller's, or the default one of (device, stream)."""
+    if workspace is not None:
+        return workspace.get(need, stream, device)
+    ws = _default_ws.get((device, raw))
+    if ws is not None and ws.buf.numel() >= need:
+        return ws.buf  # allocated on this stream: calls on others have workspaces of their own
+    return _workspace_for(device, stream).get(need, stream, device)
+
+
+def _fits(*sizes):
+    """The C ABI's sizes are 32-bit; ctypes would cut a larger one off without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
+
+
+def _call(fn, what: str, device: torch.device, *args):
+    """One C call with `device` current, as a launch on one of its streams needs."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _native.check(st, what)
 
 
 def spec_quantize_rows(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None, stream=None):
@@ -509,23 +549,26 @@ def spec_quantize_rows(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = 
     is codes[..., j].float() * scales[..., j // 128].float()."""
     _need_gpu(x, "x")
     dt = _DTYPES.get(x.dtype)
-    if dt is None or x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if dt is None or not shape or shape[-1] < 1:
         raise ValueError("x must be bfloat16 or float32 [..., d] with d >= 1")
-    d = x.shape[-1]
-    nb = _blocks(d)
-    lead = tuple(x.shape[:-1])
+    dev = x.device
+    d = shape[-1]
+    nb = (d + 127) // 128
+    lead = shape[:-1]
+    rows = x.numel() // d
+    _fits(rows, d)
     if out is None:
-        codes = torch.empty(lead + (nb * _BLOCK,), dtype=_CODES, device=x.device)
-        scales = torch.empty(lead + (nb,), dtype=_SCALES, device=x.device)
+        codes = torch.empty(lead + (nb * _BLOCK,), dtype=_CODES, device=dev)
+        scales = torch.empty(lead + (nb,), dtype=_SCALES, device=dev)
     else:
         if len(out) != 2:
             raise ValueError("out must hold codes and scales")
         codes, scales = out
-        _need(codes, "codes", _CODES, lead + (nb * _BLOCK,), x.device)
-        _need(scales, "scales", _SCALES, lead + (nb,), x.device)
-    st = _native.load().spec_quantize_rows(_ptr(x), x.numel() // d, d, dt, _ptr(codes), _ptr(scales),
-                                           _stream_handle(x.device, stream))
-    _native.check(st, "spec_quantize_rows")
+        _need(codes, "codes", _CODES, lead + (nb * _BLOCK,), dev)
+        _need(scales, "scales", _SCALES, lead + (nb,), dev)
+    _call(_native.load().spec_quantize_rows, "spec_quantize_rows", dev, x.data_ptr(), rows, d, dt,
+          codes.data_ptr(), scales.data_ptr(), _raw_stream(dev, stream))
     return codes, scales
 
 
@@ -538,60 +581,68 @@ def spec_draft_head_quantized(h: torch.Tensor, W_codes: torch.Tensor, W_scales: 
     dims are rows; quantised within the call), W_codes and W_scales from
     spec_quantize_rows of W [V, d], cluster_ids int32 [n_sel].  Returns logits
     [..., n_sel * cluster_size] of dtype."""
-    for t, name in ((h, "h"), (W_codes, "W_codes"), (W_scales, "W_scales"), (cluster_ids, "cluster_ids")):
-        _need_gpu(t, name, h.device)
-    if h.dtype != torch.bfloat16 or h.dim() < 1 or h.shape[-1] < 1:
+    _need_gpu(h, "h")
+    dev, shape = h.device, h.shape
+    if h.dtype is not torch.bfloat16 or not shape or shape[-1] < 1:
         raise ValueError("h must be bfloat16 [..., d] with d >= 1")
-    d = h.shape[-1]
-    nb = _blocks(d)
+    d = shape[-1]
+    nb = (d + 127) // 128
     if W_codes.dim() != 2:
         raise ValueError("W_codes must be [V, 128 * ceil(d / 128)]")
     V = W_codes.shape[0]
-    _need(W_codes, "W_codes", _CODES, (V, nb * _BLOCK), h.device)
-    _need(W_scales, "W_scales", _SCALES, (V, nb), h.device)
-    if cluster_ids.dtype != torch.int32 or cluster_ids.dim() != 1:
-        raise ValueError("cluster_ids must be int32 [n_sel]")
-    cluster_size = int(cluster_size)
+    _need(W_codes, "W_codes", _CODES, (V, nb * _BLOCK), dev)
+    _need(W_scales, "W_scales", _SCALES, (V, nb), dev)
     n_sel = cluster_ids.numel()
+    _need(cluster_ids, "cluster_ids", torch.int32, (n_sel,), dev)
+    cluster_size = int(cluster_size)
+    if cluster_size < 1:
+        raise ValueError("cluster_size must be >= 1")
     M = h.numel() // d
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise ValueError("dtype must be bfloat16 or float32")
-    shape = tuple(h.shape[:-1]) + (n_sel * cluster_size,)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=h.device)
-    else:
-        _need(out, "out", dtype, shape, h.device)
+    _fits(M, d, V, cluster_size, n_sel)
     lib = _native.load()
     need = lib.spec_draft_head_quantized_workspace_bytes(M, d, V, cluster_size, n_sel)
+    shape = shape[:-1] + (n_sel * cluster_size,)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, shape, dev)
+    raw = _raw_stream(dev, stream)
     ws, wsb = None, 0
     if need:
-        buf = (workspace or _workspace_for(h.device, stream)).get(need, stream, h.device)
-        ws, wsb = _ptr(buf), buf.numel()
-    st = lib.spec_draft_head_quantized(_ptr(h), _ptr(W_codes), _ptr(W_scales), _ptr(cluster_ids), M, d, V,
-                                       cluster_size, n_sel, _ptr(out), dt, ws, wsb, _stream_handle(h.device, stream))
-    _native.check(st, "spec_draft_head_quantized")
+        buf = _scratch(dev, need, raw, workspace, stream)
+        ws, wsb = buf.data_ptr(), buf.numel()
+    _call(lib.spec_draft_head_quantized, "spec_draft_head_quantized", dev, h.data_ptr(), W_codes.data_ptr(),
+          W_scales.data_ptr(), cluster_ids.data_ptr(), M, d, V, cluster_size, n_sel, out.data_ptr(), dt, ws, wsb, raw)
     return out
 
 
 def _kv_shape(codes: torch.Tensor, scales: torch.Tensor):
     """(P, B, L_max, E) of a quantised cache, after its checks."""
     _need_gpu(codes, "codes")
-    if codes.dtype != _CODES or codes.dim() < 3:
+    shape = codes.shape
+    if codes.dtype is not _CODES or len(shape) < 3:
         raise ValueError(f"codes must be {_CODES} [P, B, L_max, ...]")
-    P, B, Lmax = codes.shape[:3]
-    E = 1
-    for x in codes.shape[3:]:
-        E *= int(x)
-    _need(scales, "scales", _SCALES, (P, B, Lmax, _blocks(E)), codes.device)
+    P, B, Lmax = shape[:3]
+    E = shape[3] if len(shape) == 4 else math.prod(shape[3:])
+    _fits(P, B, Lmax, E)
+    _need(scales, "scales", _SCALES, (P, B, Lmax, (E + 127) // 128), codes.device)
     return P, B, Lmax, E
 
 
-def _kv_ints(t: Optional[torch.Tensor], name: str, B: int, device: torch.device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(B, dtype=torch.int32, device=device)
-    _need(t, name, torch.int32, (B,), device)
-    return t
+def _kv_other(t: torch.Tensor, name: str, codes: torch.Tensor):
+    """dtype code of a [P, B, K, ...] tensor of values that goes with codes."""
+    _need_gpu(t, name, codes.device)
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    a, b = t.shape, codes.shape
+    if len(a) != len(b) or a[:2] != b[:2] or a[3:] != b[3:]:
+        raise ValueError(f"{name} must be [P, B, K, ...] with the trailing shape of codes")
+    _fits(a[2])
+    return dt
 
 
 def spec_kv_commit_quantized(codes: torch.Tensor, scales: torch.Tensor, staging: torch.Tensor,
@@ -609,21 +660,20 @@ def spec_kv_commit_quantized(codes: torch.Tensor, scales: torch.Tensor, staging:
     (int32 [B]: 0 committed, 1 no room, 2 accepted_len outside [0, K])."""
     P, B, Lmax, E = _kv_shape(codes, scales)
     dev = codes.device
-    _need_gpu(staging, "staging", dev)
-    dt = _DTYPES.get(staging.dtype)
-    if dt is None:
-        raise ValueError("staging must be bfloat16 or float32")
-    if staging.dim() != codes.dim() or staging.shape[:2] != codes.shape[:2] or staging.shape[3:] != codes.shape[3:]:
-        raise ValueError("staging must be [P, B, K, ...] with the trailing shape of codes")
-    K = staging.shape[2]
+    dt = _kv_other(staging, "staging", codes)
     _need(accepted_len, "accepted_len", torch.int32, (B,), dev)
     _need(cache_len, "cache_len", torch.int32, (B,), dev)
-    new_len = cache_len if new_len is None else _kv_ints(new_len, "new_len", B, dev)
-    status = _kv_ints(status, "status", B, dev)
-    st = _native.load().spec_kv_commit_quantized(_ptr(codes), _ptr(scales), _ptr(staging), _ptr(accepted_len),
-                                                 _ptr(cache_len), _ptr(new_len), _ptr(status), P, B, K, Lmax, E, dt,
-                                                 _stream_handle(dev, stream))
-    _native.check(st, "spec_kv_commit_quantized")
+    if new_len is None:
+        new_len = cache_len
+    else:
+        _need(new_len, "new_len", torch.int32, (B,), dev)
+    if status is None:
+        status = torch.empty_like(cache_len)
+    else:
+        _need(status, "status", torch.int32, (B,), dev)
+    _call(_native.load().spec_kv_commit_quantized, "spec_kv_commit_quantized", dev, codes.data_ptr(),
+          scales.data_ptr(), staging.data_ptr(), accepted_len.data_ptr(), cache_len.data_ptr(), new_len.data_ptr(),
+          status.data_ptr(), P, B, staging.shape[2], Lmax, E, dt, _raw_stream(dev, stream))
     return status
 
 
@@ -638,17 +688,15 @@ def spec_kv_read_quantized(codes: torch.Tensor, scales: torch.Tensor, cache_len:
     (int32 [B]: 0 read, 1 length outside [0, min(L_max, L_out)])."""
     P, B, Lmax, E = _kv_shape(codes, scales)
     dev = codes.device
-    _need_gpu(out, "out", dev)
-    dt = _DTYPES.get(out.dtype)
-    if dt is None:
-        raise ValueError("out must be bfloat16 or float32")
-    if out.dim() != codes.dim() or out.shape[:2] != codes.shape[:2] or out.shape[3:] != codes.shape[3:]:
-        raise ValueError("out must be [P, B, L_out, ...] with the trailing shape of codes")
+    dt = _kv_other(out, "out", codes)
     _need(cache_len, "cache_len", torch.int32, (B,), dev)
-    status = _kv_ints(status, "status", B, dev)
-    st = _native.load().spec_kv_read_quantized(_ptr(codes), _ptr(scales), _ptr(cache_len), _ptr(out), _ptr(status),
-                                               P, B, Lmax, out.shape[2], E, dt, _stream_handle(dev, stream))
-    _native.check(st, "spec_kv_read_quantized")
+    if status is None:
+        status = torch.empty_like(cache_len)
+    else:
+        _need(status, "status", torch.int32, (B,), dev)
+    _call(_native.load().spec_kv_read_quantized, "spec_kv_read_quantized", dev, codes.data_ptr(), scales.data_ptr(),
+          cache_len.data_ptr(), out.data_ptr(), status.data_ptr(), P, B, Lmax, out.shape[2], E, dt,
+          _raw_stream(dev, stream))
     return status
 
 
@@ -665,27 +713,29 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int =
     after a sequence's last token) is not read: NaN, and -1 in top_ids."""
     _need_gpu(logits, "logits")
     dt = _DTYPES.get(logits.dtype)
-    if dt is None or logits.dim() < 1 or logits.shape[-1] < 1:
+    shape = logits.shape
+    if dt is None or not shape or shape[-1] < 1:
         raise ValueError("logits must be bfloat16 or float32 [..., V] with V >= 1")
-    V = logits.shape[-1]
-    lead = tuple(logits.shape[:-1])
+    V = shape[-1]
+    lead = shape[:-1]
     dev = logits.device
     _need(tokens, "tokens", torch.int32, lead, dev)
     top_n = int(top_n)
     if top_n < 0:
         raise ValueError("top_n must be >= 0")
     N = tokens.numel()
-    lp = torch.empty(lead, dtype=torch.float32, device=dev)
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    ids = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev)
-    top = torch.empty(lead + (top_n,), dtype=torch.float32, device=dev)
+    _fits(N, V, top_n)
     lib = _native.load()
     need = lib.spec_token_logprobs_workspace_bytes(N, V, dt, top_n)
+    lp = torch.empty_like(tokens, dtype=torch.float32)
+    entropy = torch.empty_like(lp)
+    ids = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev)
+    top = torch.empty_like(ids, dtype=torch.float32)
+    raw = _raw_stream(dev, stream)
     ws, wsb = None, 0
     if need:
-        buf = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
-        ws, wsb = _ptr(buf), buf.numel()
-    st = lib.spec_token_logprobs(_ptr(logits), _ptr(tokens), N, V, dt, ctypes.c_float(temperature), top_n, _ptr(lp),
-                                 _ptr(entropy), _ptr(ids), _ptr(top), ws, wsb, _stream_handle(dev, stream))
-    _native.check(st, "spec_token_logprobs")
+        buf = _scratch(dev, need, raw, workspace, stream)
+        ws, wsb = buf.data_ptr(), buf.numel()
+    _call(lib.spec_token_logprobs, "spec_token_logprobs", dev, logits.data_ptr(), tokens.data_ptr(), N, V, dt,
+          temperature, top_n, lp.data_ptr(), entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), ws, wsb, raw)
     return lp, entropy, ids, top

@@ -349,7 +349,7 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
 size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top_n) {
   sv::LogprobsShape s{};
   sv::LogprobsWorkspace w{};
-  return sv::check_logprobs(N, V, dtype, top_n, &s, &w) == SPEC_OK && N > 0 ? w.total : 0;
+  return sv::check_logprobs(N, V, dtype, top_n, false, &s, &w) == SPEC_OK && N > 0 ? w.total : 0;
 }
 
 spec_status_t spec_token_logprobs(const void* logits, const int32_t* tokens, int32_t N, int32_t V,

@@ -218,46 +218,63 @@ inline spec_status_t validate_kv_read_quantized(const void* codes, const void* s
 
 // ---- token log-probabilities ----------------------------------------------------
 
-// One tile of the statistics pass: one wave, 8 chunks of 64 16-byte vectors.
-// Tiles and chunks lie on a row's 16-byte grid: a row that does not begin on
-// a 16-byte boundary begins inside its first vector.
+// A row is cut into tiles, one wave's 8 chunks of 64 16-byte vectors.  Tiles
+// and chunks lie on a row's 16-byte grid: a row that does not begin on a
+// 16-byte boundary begins inside its first vector.
 struct LogprobsShape {
   int N, V;
-  int vec;     // values per 16 bytes
-  int tile;    // values per tile
-  int NT;      // tiles per row (enough for any alignment)
-  int groups;  // blocks of four tiles per row
+  int vec;         // values per 16 bytes
+  int tile;        // values per tile
+  int NT;          // tiles per row (enough for any alignment)
+  int part_tiles;  // tiles per block of four waves, and
+  int NP;          // parts per row; 0: a block does a whole row
   int top;
 };
 
 constexpr int kMaxTop = SPEC_MAX_TOP;
 constexpr int kChunksPerTile = 8;
+constexpr int kLpShortRow = 8;    // tiles of a row that always is one block's
+constexpr int kLpRowTiles = 16;   // tiles of a row that is one block's in small batches: one per wave
+constexpr int kLpWideRows = 256;  // the small batches; their blocks have 16 waves
+constexpr int kLpManyRows = 768;  // rows joined by blocks of four waves from here
+constexpr int kLpPartsWanted = 8192;
+constexpr int kLpPartTiles = 16;  // most tiles per part
 
-struct LogprobsTile {
-  double ref;  // the tile's reference, in units of log 2: sums are of 2^(x * s - ref)
-  float z;     // sum of e = 2^(x * s - ref)
-  float h;     // sum of e * (x * s - ref)
+struct LogprobsPart {
+  double R;  // reference, in units of log 2: sums are of 2^(x * s - R)
+  double z;  // sum of e = 2^(x * s - R)
+  double h;  // sum of e * (x * s - R)
 };
 
 struct LogprobsWorkspace {
-  size_t tiles, chunks, total;  // byte offsets
+  size_t parts, chunks, lanes, total;  // byte offsets
 };
 
-inline spec_status_t check_logprobs(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top, LogprobsShape* s,
-                                    LogprobsWorkspace* w) {
+// aligned: every row begins on a 16-byte boundary (false: any may begin anywhere).
+inline spec_status_t check_logprobs(int32_t N, int32_t V, spec_dtype_t dtype, int32_t top, bool aligned,
+                                    LogprobsShape* s, LogprobsWorkspace* w) {
   if (!valid_dtype(dtype) || N < 0 || V < 1 || top < 0) return SPEC_ERR_INVALID_ARG;
   if (V > (1 << 30) || top > kMaxTop) return SPEC_ERR_UNSUPPORTED;
   s->N = N;
   s->V = V;
   s->vec = 16 / (int)elem_size(dtype);
   s->tile = kWave * s->vec * kChunksPerTile;
-  s->NT = (V + s->vec - 1 + s->tile - 1) / s->tile;
-  s->groups = (s->NT + kWavesPerBlock - 1) / kWavesPerBlock;
+  s->NT = (V + (aligned ? 0 : s->vec - 1) + s->tile - 1) / s->tile;
   s->top = top;
-  if ((size_t)N * (size_t)s->groups > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
-  w->tiles = 0;
-  w->chunks = align256((size_t)N * s->NT * sizeof(LogprobsTile));
-  w->total = w->chunks + (top > 0 ? align256((size_t)N * s->NT * kChunksPerTile * sizeof(float)) : 0);
+  // The plan goes by the tiles that an aligned row has, so that the alignment
+  // decides nothing but NT.
+  const int full = (V + s->tile - 1) / s->tile;
+  const bool one = full <= kLpShortRow || (N <= kLpWideRows && full <= kLpRowTiles);
+  long long tiles = (long long)N * full / kLpPartsWanted / kWavesPerBlock * kWavesPerBlock;
+  tiles = tiles < kWavesPerBlock ? kWavesPerBlock : tiles > kLpPartTiles ? kLpPartTiles : tiles;
+  s->part_tiles = (int)tiles;
+  s->NP = one ? 0 : (s->NT + s->part_tiles - 1) / s->part_tiles;
+  if ((size_t)N * (size_t)(one ? 1 : s->NP) > max_blocks(one && N <= kLpWideRows ? 1024 : kBlock))
+    return SPEC_ERR_UNSUPPORTED;
+  w->parts = 0;
+  w->chunks = align256((size_t)N * s->NP * sizeof(LogprobsPart));
+  w->lanes = w->chunks + (top > 0 && !one ? align256((size_t)N * s->NT * kChunksPerTile * sizeof(float)) : 0);
+  w->total = w->lanes + (top > 0 && !one ? align256((size_t)N * s->NP * kWave * sizeof(float)) : 0);
   return SPEC_OK;
 }
 
@@ -267,7 +284,12 @@ inline spec_status_t validate_logprobs(const void* logits, const int32_t* tokens
                                        const float* entropy, const int32_t* top_ids, const float* top_logprobs,
                                        const void* workspace, size_t workspace_bytes, LogprobsShape* s,
                                        LogprobsWorkspace* w, bool* empty) {
-  const spec_status_t sc = check_logprobs(N, V, dtype, top, s, w);
+  LogprobsShape any{};
+  spec_status_t sc = check_logprobs(N, V, dtype, top, false, &any, w);
+  if (sc != SPEC_OK) return sc;
+  const size_t need = w->total;  // what the sizing function says
+  const bool aligned = (uintptr_t)logits % 16 == 0 && ((size_t)V * elem_size(dtype)) % 16 == 0;
+  sc = check_logprobs(N, V, dtype, top, aligned, s, w);
   if (sc != SPEC_OK) return sc;
   // log2(e) / T must be a finite float: T at or above the least normal one.
   if (!(temperature >= 1.17549435e-38f && isfinite(temperature))) return SPEC_ERR_INVALID_ARG;
@@ -277,7 +299,7 @@ inline spec_status_t validate_logprobs(const void* logits, const int32_t* tokens
   if ((uintptr_t)logits % elem_size(dtype) || (uintptr_t)tokens % 4 || (uintptr_t)logprobs % 4 ||
       (uintptr_t)entropy % 4 || (uintptr_t)top_ids % 4 || (uintptr_t)top_logprobs % 4)
     return SPEC_ERR_INVALID_ARG;
-  if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < w->total) return SPEC_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < need)) return SPEC_ERR_WORKSPACE;
   return SPEC_OK;
 }
 

@@ -133,6 +133,38 @@ def test_masked_rows(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,V", [(3, 40000), (3, 300001), (300, 40003)])
+def test_masked_before_a_fault(N, V, dtype):
+    """-inf in the first tiles and a NaN or +inf in a later one, in each form of the launch."""
+    x = normal(3, V, dtype, 21)
+    x[:, :9000] = -INF
+    x[0, V - 5], x[1, V - 3] = NAN, INF
+    x = x.repeat(N // 3, 1)
+    t = torch.full((N,), V - 1, dtype=torch.int32)
+    got = [g.cpu().numpy() for g in sv().spec_token_logprobs(x.to(DEV), t.to(DEV), 7)]
+    compare(x[:3], t[:3], 7, 1.0, [g[:3] for g in got])
+    # the others hold the same rows, at other alignments where V is odd: sums are then grouped otherwise
+    for i in range(3, N, 31):
+        compare(x[i:i + 1], t[i:i + 1], 7, 1.0, [g[i:i + 1] for g in got])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,V,dtype", [(257, 40003, BF), (257, 66000, F32), (40, 140000, BF), (700, 20000, BF),
+                                       (2050, 3001, F32)])
+def test_batches(N, V, dtype):
+    """Each form of the launch, odd and even rows, dead ones among them."""
+    g = torch.Generator().manual_seed(N)
+    x = normal(7, V, dtype, V).repeat(N // 7 + 1, 1)[:N].contiguous()
+    t = torch.randint(-1, V + 1, (N,), generator=g).to(torch.int32)
+    t[::3] = -1
+    got = [v.cpu().numpy() for v in sv().spec_token_logprobs(x.to(DEV), t.to(DEV), 12)]
+    some = torch.randperm(N, generator=g)[:25]
+    compare(x[some], t[some], 12, 1.0, [v[some.numpy()] for v in got])
+    assert np.array_equal(np.isnan(got[0]), ((t < 0) | (t >= V)).numpy())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T", [1.2e-38, 1e-30, 1e-8, 1e-3, 0.3, 2.0, 1e4, 1e30, 3e38])
 def test_temperatures(T, dtype):
     check(normal(4, 5001, dtype, 13), [0, 5000, 17, 300], 8, T)
@@ -225,9 +257,11 @@ def test_refusals():
         assert call(T=T) == INVALID, T
     assert call(top=33) == UNSUP and call(V=(1 << 30) + 1) == UNSUP
     assert call(N=0x7fffffff, V=1 << 20) == UNSUP
-    need = size(4, 1000, 1, 5)
-    assert need > size(4, 1000, 1, 0) > 0
-    assert call(ws=None) == WS and call(ws=0x100080) == WS and call(wb=need - 1) == WS
+    need = size(4, 200000, 1, 5)
+    assert need > size(4, 200000, 1, 0) > 0
+    for o in (dict(ws=None), dict(ws=0x100080), dict(wb=need - 1)):
+        assert call(V=200000, **o) == WS
+    assert size(4, 1000, 1, 5) == 0                       # short rows need none
     assert call(N=0, x=None, ws=None) == OK
     assert size(0, 1000, 1, 5) == 0 and size(4, 0, 1, 5) == 0 and size(4, 1000, 1, 33) == 0
 
