@@ -49,7 +49,8 @@ struct HeadQArgs {
   const int32_t* cids;    // [n_sel], any order
   int M, N, cs, nclusters;
   int nb;                 // blocks of 128 in a row; D = 128 * nb
-  int m_tiles, remap;
+  int m_tiles;
+  int total, per_xcd;     // tiles (times slices), and how many each XCD takes in turn
   int split, split_nb;    // blocks of threads per tile; blocks of 128 per slice
   int dword_scales;       // scale rows begin on 4-byte boundaries
   void* out;              // [M][N] fp32 or bf16
@@ -88,7 +89,6 @@ __device__ __forceinline__ void store1(void* dst, bool bf16, size_t o, float v) 
   else static_cast<float*>(dst)[o] = v;
 }
 
-constexpr int kSeg = 64;  // blocks of 128 whose scales are in LDS at a time
 
 template <int WM, int WN, int WK, int TM, int TN, int NBUF>
 struct HeadQTile {
@@ -97,11 +97,12 @@ struct HeadQTile {
   static constexpr int kGroup = kRows / 8;             // DMA instructions per block of 128
   static constexpr int kIW = WK * kGroup / NW;         // per wave and stage of WK blocks
   static constexpr int kStage = WK * kRows * 128;      // bytes
+  static constexpr int kSeg = kRows > 256 ? 32 : 64;   // blocks of 128 whose scales are in LDS at a time
   static_assert(kRows % 8 == 0 && WK * kGroup % NW == 0, "DMA split");
-  static_assert(NBUF >= 3 && (NBUF - 2) * kIW < 64, "pipeline depth");
+  static_assert(NBUF >= 2 && (NBUF - 2) * kIW < 64, "pipeline depth");
   static_assert(kSeg % WK == 0 && WK <= 4, "scale groups");
   static_assert((WK - 1) * WM * WN * kWave * TN * 4 * 4 <= NBUF * kStage, "reduction space");
-  static_assert(kMt * (kNt + 4) * 4 <= NBUF * kStage, "epilogue space");
+  static_assert(16 * WM * (kNt + 4) * 4 <= NBUF * kStage, "epilogue space");
   static_assert(kThreads % (kNt / 4) == 0, "epilogue rows per pass");
 };
 
@@ -123,7 +124,7 @@ __device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_f
 template <int WM, int WN, int WK, int TM, int TN, int NBUF, bool kF32>
 __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a) {
   using C = HeadQTile<WM, WN, WK, TM, TN, NBUF>;
-  constexpr int kMt = C::kMt, kNt = C::kNt, kRows = C::kRows, NW = C::NW, kIW = C::kIW;
+  constexpr int kMt = C::kMt, kNt = C::kNt, kRows = C::kRows, NW = C::NW, kIW = C::kIW, kSeg = C::kSeg;
   // One LDS object: beside a second one the compiler waits for every DMA in
   // flight before each read of this one.
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * C::kStage + kSeg * kRows + 4 * kRows];
@@ -134,9 +135,12 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const int wk = wave / (WM * WN), wmn = wave % (WM * WN);
   const int wm = wmn / WN, wn = wmn % WN;
-  int v = blockIdx.x;
-  if (a.remap) v = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-  const int tiles = (int)(gridDim.x / (unsigned)a.split);
+  // Blocks go to the eight XCDs in turn: each takes a run of tiles, row tiles
+  // first, so that the row tiles of a column tile read its W rows from one L2.
+  const int v0 = (int)(blockIdx.x & 7) * a.per_xcd + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= a.per_xcd || v0 >= a.total) return;
+  int v = v0;
+  const int tiles = a.total / a.split;
   const int slice = v / tiles;
   v -= slice * tiles;
   const int n0 = (v / a.m_tiles) * kNt, m0 = (v % a.m_tiles) * kMt;
@@ -202,12 +206,21 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
   // with no other memory loads between the DMAs that the waits count.
   for (int first = b0; first < b0 + blocks; first += kSeg) {
     const int seg = min(b0 + blocks - first, kSeg), stages = (seg + WK - 1) / WK;
+    // Rows lie a multiple of 128 bytes apart, mostly of 4096, and the memory's
+    // channels take turns every 256: the pieces that a stage reads of its rows
+    // are all on one channel or two.  So that not all blocks wait for the same
+    // ones, each begins at another stage and goes round (M = 128, N = 128256, d =
+    // 4096: 157 -> 142 us).  Where several row tiles read the same W rows they
+    // stay in step instead, for their L2's sake (M = 1792: 880 against 950 us).
+    const int rot = kMt < 256 && a.m_tiles == 1 ? (int)((unsigned)(v0 % a.per_xcd) % (unsigned)stages) : 0;
+    auto stage_of = [&](int s) { return s + rot < stages ? s + rot : s + rot - stages; };
     auto issue = [&](int s) {
       uint8_t* dst = lds + s % NBUF * C::kStage;
+      const int sk = stage_of(s);
 #pragma unroll
       for (int j = 0; j < kIW; ++j) {
         const int sub = (j * NW + wave) / C::kGroup;
-        const int b = first + min(s * WK + sub, seg - 1);  // past the segment: its last block again, not used
+        const int b = first + min(sk * WK + sub, seg - 1);  // past the segment: its last block again, not used
         dma16(src[j] + (size_t)b * kQuantBlock, dst + 1024 * (j * NW + wave));
       }
     };
@@ -226,8 +239,8 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
       block_barrier();
       // Every wave has finished stage s - 1, whose buffer the next DMA refills.
       if (s + NBUF - 1 < stages) issue(s + NBUF - 1);
-      const int kb = s * WK + wk;  // this wave's block of the segment
-      if ((kb & 3) < WK) {
+      const int kb = stage_of(s) * WK + wk;  // this wave's block of the segment
+      if ((kb & 3) < WK || s == 0) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = sc[kb / 4 * kRows + arow0 + 16 * i] >> (8 * (kb & 3));
 #pragma unroll
@@ -245,20 +258,20 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
       for (int j = 0; j < TN; ++j) bf[j] = fragment(buf, brow0 + 16 * j);
 #if defined(__HIP_DEVICE_COMPILE__)
       if constexpr (kF32) {
-        i32x8 af[TM];
+        bf16x8 bv[TN][4];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) af[i] = fragment(buf, arow0 + 16 * i);
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int p = 0; p < 8; p += 2) {
-          bf16x8 bv[TN];
+          for (int p = 0; p < 4; ++p) bv[j][p] = codes_to_bf16(bf[j][2 * p], bf[j][2 * p + 1], scale_float(sb[j]));
 #pragma unroll
-          for (int j = 0; j < TN; ++j) bv[j] = codes_to_bf16(bf[j][p], bf[j][p + 1], scale_float(sb[j]));
+        for (int i = 0; i < TM; ++i) {
+          const i32x8 af = fragment(buf, arow0 + 16 * i);
 #pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const bf16x8 av = codes_to_bf16(af[i][p], af[i][p + 1], scale_float(sa[i]));
+          for (int p = 0; p < 4; ++p) {
+            const bf16x8 av = codes_to_bf16(af[2 * p], af[2 * p + 1], scale_float(sa[i]));
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[j], acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[j][p], acc[i][j], 0, 0, 0);
           }
         }
       } else {
@@ -305,37 +318,42 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
     }
   }
 
-  // Through LDS to whole rows: lane l holds D[4 * (l / 16) + r][l % 16] of
-  // each 16 x 16 chunk; then every thread stores 4 consecutive columns.
-  constexpr int kLd = kNt + 4;
-  if (wk == 0) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          stage[(wm * 16 * TM + 16 * i + 4 * fc + r) * kLd + wn * 16 * TN + 16 * j + frow] = acc[i][j][r];
-  }
-  __syncthreads();
-  constexpr int kTpr = kNt / 4;
+  // Through LDS to whole rows, one chunk of 16 rows per wave row at a time:
+  // lane l holds D[4 * (l / 16) + r][l % 16] of each 16 x 16 chunk; then every
+  // thread stores 4 consecutive columns.
+  constexpr int kLd = kNt + 4, kTpr = kNt / 4;
   const int c4 = (int)(threadIdx.x % kTpr) * 4;
   void* dst = a.split == 1 ? a.out : static_cast<void*>(a.partial + (size_t)slice * a.M * a.N);
   const bool bf16 = a.split == 1 && a.out_bf16;
   const bool vec = a.N % 4 == 0 && (uintptr_t)dst % (bf16 ? 8 : 16) == 0;
-  for (int r = threadIdx.x / kTpr; r < kMt; r += C::kThreads / kTpr) {
-    const int m = m0 + r;
-    if (m >= a.M) break;
-    float w[4];
+  bool none[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = token[kMt + c4 + e] < 0 ? 0.0f : stage[r * kLd + c4 + e];
-    const size_t o = (size_t)m * a.N + n0 + c4;
-    if (vec) {
-      if (n0 + c4 < a.N) store4(dst, bf16, o, w);
-    } else {
+  for (int e = 0; e < 4; ++e) none[e] = token[kMt + c4 + e] < 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n0 + c4 + e < a.N) store1(dst, bf16, o + e, w[e]);
+  for (int i = 0; i < TM; ++i) {
+    if (i > 0) __syncthreads();
+    if (wk == 0) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          stage[(wm * 16 + 4 * fc + r) * kLd + wn * 16 * TN + 16 * j + frow] = acc[i][j][r];
+    }
+    __syncthreads();
+    for (int r = threadIdx.x / kTpr; r < 16 * WM; r += C::kThreads / kTpr) {
+      const int m = m0 + (r / 16) * 16 * TM + 16 * i + r % 16;
+      if (m >= a.M) continue;
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = none[e] ? 0.0f : stage[r * kLd + c4 + e];
+      const size_t o = (size_t)m * a.N + n0 + c4;
+      if (vec) {
+        if (n0 + c4 < a.N) store4(dst, bf16, o, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n0 + c4 + e < a.N) store1(dst, bf16, o + e, w[e]);
+      }
     }
   }
 }
@@ -376,9 +394,10 @@ hipError_t launch_tile(HeadQArgs a, const HeadQPlan& plan, hipStream_t st) {
   a.split_nb = (a.nb + plan.split - 1) / plan.split;
   a.split = (a.nb + a.split_nb - 1) / a.split_nb;  // no empty slice
   const long long total = tiles * a.split;
-  a.remap = (a.m_tiles > 1 || a.split > 1) && total % 8 == 0;
+  a.total = (int)total;
+  a.per_xcd = (int)((total + 7) / 8);
   a.dword_scales = a.nb % 4 == 0 && a.split_nb % 4 == 0 && (uintptr_t)a.hs % 4 == 0 && (uintptr_t)a.ws % 4 == 0;
-  const dim3 grid((unsigned)total), block(C::kThreads);
+  const dim3 grid((unsigned)a.per_xcd * 8), block(C::kThreads);
   if (a.out_bf16) hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, false>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, true>), grid, block, 0, st, a);
   const hipError_t e = hipGetLastError();
@@ -411,10 +430,12 @@ hipError_t launch_head_quantized(const void* h, const void* W_codes, const void*
   const hipError_t e = launch_quantize_rows(h, M, d, 1, base + w.codes, base + w.scales, st);
   if (e != hipSuccess) return e;
   switch (plan.tile) {
-    case 0: return launch_tile<1, 2, 2, 1, 1, 5>(a, plan, st);
-    case 1: return launch_tile<1, 2, 2, 2, 1, 4>(a, plan, st);
-    case 2: return launch_tile<1, 4, 2, 4, 1, 4>(a, plan, st);
-    default: return launch_tile<2, 4, 1, 4, 2, 4>(a, plan, st);
+    case 0: return launch_tile<1, 2, 4, 1, 1, 3>(a, plan, st);
+    case 1: return launch_tile<1, 4, 1, 2, 1, 3>(a, plan, st);
+    case 2: return launch_tile<2, 4, 1, 2, 2, 3>(a, plan, st);
+    case 3: return launch_tile<2, 4, 1, 4, 2, 3>(a, plan, st);
+    case 4: return launch_tile<2, 4, 1, 4, 4, 3>(a, plan, st);
+    default: return launch_tile<2, 4, 1, 8, 4, 2>(a, plan, st);
   }
 }
 

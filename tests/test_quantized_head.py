@@ -83,7 +83,8 @@ def test_ids_out_of_range_and_repeated(M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,d,V", [(5, 4096, 24000), (40, 2048, 17000), (200, 1024, 36000)])
+@pytest.mark.parametrize("M,d,V", [(5, 4096, 24000), (40, 2048, 17000), (200, 1024, 36000), (100, 384, 66000),
+                                   (300, 640, 26000), (513, 1024, 17410), (129, 4224, 52000)])
 def test_wide_shortlists(M, d, V):
     """Grids of many tiles, without a split."""
     check(M, d, V, 1, np.arange(V - 3), BF)
