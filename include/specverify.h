@@ -427,8 +427,8 @@ size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dt
  *   codes   [R, D] bytes out, D = 128 * ceil(d / 128), 16-byte aligned; codes
  *           past d are zeros.
  *   scales  [R, ceil(d / 128)] bytes out.
- * One launch.  16-byte vector loads when d * size is a multiple of 16 and x is
- * 16-byte aligned (d % 8 == 0 in fp32 too), element loads otherwise.
+ * One launch.  Any alignment of whole elements works; rows of d % 8 == 0
+ * from a 16-byte boundary take aligned vector loads.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, R < 0, d < 1
  * or an unknown dtype; SPEC_ERR_UNSUPPORTED for more than 2^30 - 1 blocks.
  */
@@ -491,8 +491,8 @@ size_t spec_draft_head_quantized_workspace_bytes(int32_t M, int32_t d, int32_t V
  *                or cache_len + n > L_max); 2 n outside [0, K].  Nothing is
  *                committed unless 0.
  * K may be any length: a prompt's entries are committed by the same call.
- * 8-value vectors when E % 8 == 0, staging is 16-byte and codes 8-byte
- * aligned; element accesses otherwise.
+ * Any alignment of whole elements works; E % 8 == 0 with staging on a 16-byte
+ * and codes on an 8-byte boundary takes aligned vectors.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, negative sizes,
  * an unknown dtype, sizes that overflow, or lengths and status that overlap;
  * SPEC_ERR_UNSUPPORTED for a grid too large for one launch.
@@ -513,8 +513,8 @@ spec_status_t spec_kv_commit_quantized(void* codes, void* scales, const void* st
  *                are left as they were.
  *   status       [B] int32 out, or NULL: 0 read; 1 length outside [0, min(L_max,
  *                L_out)], nothing is written for the sequence.
- * One launch.  8-value vectors when E % 8 == 0, out is 16-byte and codes
- * 8-byte aligned; element accesses otherwise.  Errors as
+ * One launch.  Any alignment of whole elements works; E % 8 == 0 with out on a
+ * 16-byte and codes on an 8-byte boundary takes aligned vectors.  Errors as
  * spec_kv_commit_quantized's.
  */
 spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len, void* out,

@@ -154,7 +154,7 @@ struct KvQPlan {
 // Sizes shared by the cache calls: rows is the longer row count of the two
 // buffers, row_units the units that one (plane, sequence) can have.
 inline spec_status_t check_kv_quantized(int32_t P, int32_t B, int32_t rows_move, int32_t rows_a, int32_t rows_b,
-                                        int32_t E, spec_dtype_t dtype, KvQPlan* plan) {
+                                        int32_t E, spec_dtype_t dtype, bool single, KvQPlan* plan) {
   const size_t planes = (size_t)P * (size_t)B;
   if (planes > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
   size_t rows = 0, bytes = 0;
@@ -169,8 +169,11 @@ inline spec_status_t check_kv_quantized(int32_t P, int32_t B, int32_t rows_move,
   if (!plan->copies) return SPEC_OK;
   const size_t units = (size_t)rows_move * (size_t)plan->nb * 16;
   if (units > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;  // unit numbers stay in int32
-  // Four units per thread where that still gives every CU several blocks.
-  plan->unroll = planes * ((units + 4 * kBlock - 1) / (4 * kBlock)) >= 4 * 256 ? 4 : 1;
+  // Four units per thread where that still gives every CU several blocks (64 x
+  // 8192 entries read as bf16: 418 us, 472 with one); fp32 values are read back
+  // by one (98 us for 16 x 4096 entries, 136 with four, whose stores then cut
+  // lines in two).
+  plan->unroll = single ? 1 : planes * ((units + 4 * kBlock - 1) / (4 * kBlock)) >= 4 * 256 ? 4 : 1;
   plan->chunks = (uint32_t)((units + (size_t)plan->unroll * kBlock - 1) / ((size_t)plan->unroll * kBlock));
   if (plan->chunks * planes > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
@@ -198,7 +201,7 @@ inline spec_status_t validate_kv_commit_quantized(const void* codes, const void*
   if (status && (overlap(status, lens, accepted_len, lens) || overlap(status, lens, cache_len, lens) ||
                  overlap(status, lens, new_len, lens)))
     return SPEC_ERR_INVALID_ARG;
-  const spec_status_t sc = check_kv_quantized(P, B, K, K, L_max, E, dtype, plan);
+  const spec_status_t sc = check_kv_quantized(P, B, K, K, L_max, E, dtype, false, plan);
   if (sc != SPEC_OK || !plan->copies) return sc;
   if (!codes || !scales || !staging || (uintptr_t)staging % elem_size(dtype)) return SPEC_ERR_INVALID_ARG;
   plan->vec = E % 8 == 0 && (uintptr_t)staging % 16 == 0 && (uintptr_t)codes % 8 == 0;
@@ -217,7 +220,7 @@ inline spec_status_t validate_kv_read_quantized(const void* codes, const void* s
   if (!cache_len || (uintptr_t)cache_len % 4 || (uintptr_t)status % 4) return SPEC_ERR_INVALID_ARG;
   if (status && overlap(status, (size_t)B * 4, cache_len, (size_t)B * 4)) return SPEC_ERR_INVALID_ARG;
   const int32_t rows = L_max < L_out ? L_max : L_out;
-  const spec_status_t sc = check_kv_quantized(P, B, rows, L_max, L_out, E, dtype, plan);
+  const spec_status_t sc = check_kv_quantized(P, B, rows, L_max, L_out, E, dtype, dtype == SPEC_F32, plan);
   if (sc != SPEC_OK || !plan->copies) return sc;
   if (!codes || !scales || !out || (uintptr_t)out % elem_size(dtype)) return SPEC_ERR_INVALID_ARG;
   plan->vec = E % 8 == 0 && (uintptr_t)out % 16 == 0 && (uintptr_t)codes % 8 == 0;

@@ -80,36 +80,55 @@ __device__ __forceinline__ uint2 quantize8(float (&x)[kPerLaneQ], int* byte) {
   return uint2{(uint32_t)lo, (uint32_t)hi};
 }
 
-// Eight consecutive values p[0 .. 7] as float.  kVec: p is 16-byte aligned
-// and all eight exist; otherwise only the first n (possibly <= 0) are read and
-// the rest are zeros.
-template <typename T, bool kVec>
+// Vectors at any address of whole elements: the hardware takes unaligned ones,
+// and the compiler makes one access of each of these.
+typedef uint32_t u32x4_any2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_any4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+template <typename T> struct AnyVector;
+template <> struct AnyVector<uint16_t> { typedef u32x4_any2 type; };
+template <> struct AnyVector<float> { typedef u32x4_any4 type; };
+
+// 16 bytes at p.  kVec: p is 16-byte aligned.  kStream: nontemporal.
+template <typename T, bool kVec, bool kStream>
+__device__ __forceinline__ u32x4 load16(const T* p) {
+  if constexpr (kVec) return kStream ? stream16(p) : *reinterpret_cast<const u32x4*>(p);
+  else return *reinterpret_cast<const typename AnyVector<T>::type*>(p);
+}
+
+// Eight consecutive values p[0 .. 7] as float, of which n (possibly <= 0)
+// exist: the others are zeros and not read.  kVec: p is 16-byte aligned and n is
+// at least 8 or at most 0.
+template <typename T, bool kVec, bool kStream = true>
 __device__ __forceinline__ void load8(const T* p, int n, float (&x)[kPerLaneQ]) {
-  if constexpr (kVec) {
-    if (n <= 0) {
-#pragma unroll
-      for (int i = 0; i < kPerLaneQ; ++i) x[i] = 0.0f;
-    } else if constexpr (sizeof(T) == 2) {
-      const u32x4 w = stream16(p);
+  if (n >= kPerLaneQ) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 w = load16<T, kVec, kStream>(p);
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[2 * q] = bf16_lo(w[q]), x[2 * q + 1] = bf16_hi(w[q]);
     } else {
-      const u32x4 w0 = stream16(p), w1 = stream16(p + 4);
+      const u32x4 w0 = load16<T, kVec, kStream>(p), w1 = load16<T, kVec, kStream>(p + 4);
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[q] = __uint_as_float(w0[q]), x[4 + q] = __uint_as_float(w1[q]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPerLaneQ; ++i) x[i] = i < n ? to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < kPerLaneQ; ++i) x[i] = !kVec && i < n ? to_f32(p[i]) : 0.0f;
   }
 }
 
-// bf16 of a float, to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint16_t bf16_rne(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & kInfBits) == kInfBits) return (uint16_t)((u >> 16) | ((u & 0xffffu) ? 0x40u : 0u));
-  u += 0x7fffu + ((u >> 16) & 1u);
-  return (uint16_t)(u >> 16);
+// Eight codes at q.  kVec: 8-byte aligned.
+template <bool kVec>
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint2 q) {
+  if (n >= kPerLaneQ) {
+    // Nontemporal: nothing reads them soon, and the lines leave whole (a weight of 128256 x 4096: 265 -> 254 us).
+    if (kVec) __builtin_nontemporal_store((uint64_t)q.x | ((uint64_t)q.y << 32), reinterpret_cast<uint64_t*>(p));
+    else *reinterpret_cast<u32x2_any*>(p) = u32x2_any{q.x, q.y};
+  } else if (!kVec) {
+#pragma unroll
+    for (int e = 0; e < kPerLaneQ; ++e)
+      if (e < n) p[e] = (uint8_t)(e < 4 ? q.x >> (8 * e) : q.y >> (8 * (e - 4)));
+  }
 }
 
 }  // namespace sv

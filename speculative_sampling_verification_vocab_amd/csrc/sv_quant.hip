@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kBlock) quantize_rows_kernel(const T* __restri
     int sb;
     const uint2 q = quantize8(v[k], &sb);
     if (i >= blocks) continue;
-    *reinterpret_cast<uint2*>(codes + (size_t)i * kQuantBlock + sub * kPerLaneQ) = q;
+    store_codes<true>(codes + (size_t)i * kQuantBlock + sub * kPerLaneQ, kPerLaneQ, q);
     if (sub == 0) scales[i] = (uint8_t)sb;
   }
 }
@@ -88,7 +88,7 @@ __device__ __forceinline__ int commit_status(const KvQArgs& a, int b, int& n, in
 // blocks are numbered through.  lens: the first block of each sequence also
 // writes its new length and status (new_len is not cache_len, so no block
 // reads what another writes).
-template <typename T, bool kVec, int U>
+template <typename T, bool kVec, int U, bool kStream>
 __global__ void __launch_bounds__(kBlock) kvq_commit_kernel(KvQArgs a, int lens) {
   const uint32_t pb = blockIdx.x / a.chunks, chunk = blockIdx.x - pb * a.chunks;
   const int b = (int)(pb % (uint32_t)a.B);
@@ -101,35 +101,30 @@ __global__ void __launch_bounds__(kBlock) kvq_commit_kernel(KvQArgs a, int lens)
   if (st != 0) return;
   constexpr int kPer = kBlock / kLanesPerBlock;
   const int total = n * a.nb;
-  const int first = (int)chunk * (kPer * U) + threadIdx.x / kLanesPerBlock;
-  if ((int)chunk * (kPer * U) >= total) return;
+  const int base = (int)chunk * (kPer * U), first = base + threadIdx.x / kLanesPerBlock;
+  if (base >= total) return;
   const int sub = threadIdx.x % kLanesPerBlock;
   const T* src = static_cast<const T*>(a.in) + (size_t)pb * (size_t)a.K * (size_t)a.E;
   const size_t row0 = (size_t)pb * (size_t)a.Lmax + (size_t)len;
   float v[U][kPerLaneQ];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
+    if (base + k * kPer >= total) break;  // few drafts fill a part of the block: 60 us without, 48 with
     const int i = min(first + k * kPer, total - 1);
     const int r = i / a.nb;
     const int at = (i - r * a.nb) * kQuantBlock + sub * kPerLaneQ;
-    load8<T, kVec>(src + (size_t)r * (size_t)a.E + at, a.E - at, v[k]);
+    load8<T, kVec, kStream>(src + (size_t)r * (size_t)a.E + at, a.E - at, v[k]);
   }
 #pragma unroll
   for (int k = 0; k < U; ++k) {
+    if (base + k * kPer >= total) break;
     const int i = first + k * kPer;
     int sb;
     const uint2 q = quantize8(v[k], &sb);
     if (i >= total) continue;
     const int r = i / a.nb, blk = i - r * a.nb;
     const int at = blk * kQuantBlock + sub * kPerLaneQ;
-    uint8_t* dst = a.codes + (row0 + (size_t)r) * (size_t)a.E + at;
-    if (kVec) {
-      if (at < a.E) *reinterpret_cast<uint2*>(dst) = q;
-    } else {
-#pragma unroll
-      for (int e = 0; e < kPerLaneQ; ++e)
-        if (at + e < a.E) dst[e] = (uint8_t)((e < 4 ? q.x >> (8 * e) : q.y >> (8 * (e - 4))));
-    }
+    store_codes<kVec>(a.codes + (row0 + (size_t)r) * (size_t)a.E + at, a.E - at, q);
     if (sub == 0) a.scales[(row0 + (size_t)r) * (size_t)a.nb + blk] = (uint8_t)sb;
   }
 }
@@ -163,13 +158,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
 }
 
+template <bool kVec>
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[kPerLaneQ]) {
-  *reinterpret_cast<u32x4*>(p) =
-      u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+  const u32x4 w{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+  if (kVec) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));  // 64 x 8192 entries: 420 -> 403 us
+  else *reinterpret_cast<u32x4_any2*>(p) = w;
 }
+template <bool kVec>
 __device__ __forceinline__ void store8(float* p, const float (&x)[kPerLaneQ]) {
-  *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
-  *reinterpret_cast<float4*>(p + 4) = float4{x[4], x[5], x[6], x[7]};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const u32x4 w{__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 2]),
+                  __float_as_uint(x[4 * q + 3])};
+    if (kVec) *reinterpret_cast<u32x4*>(p + 4 * q) = w;
+    else *reinterpret_cast<u32x4_any4*>(p + 4 * q) = w;
+  }
 }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = __builtin_bit_cast(uint16_t, (__bf16)x); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
@@ -184,8 +187,8 @@ __global__ void __launch_bounds__(kBlock) kvq_read_kernel(KvQArgs a) {
   if (st != 0) return;
   constexpr int kPer = kBlock / kLanesPerBlock;
   const int total = n * a.nb;
-  if ((int)chunk * (kPer * U) >= total) return;
-  const int first = (int)chunk * (kPer * U) + threadIdx.x / kLanesPerBlock;
+  const int base = (int)chunk * (kPer * U), first = base + threadIdx.x / kLanesPerBlock;
+  if (base >= total) return;
   const int sub = threadIdx.x % kLanesPerBlock;
   const size_t row0 = (size_t)pb * (size_t)a.Lmax;
   const uint8_t* src = a.codes + row0 * (size_t)a.E;
@@ -195,15 +198,20 @@ __global__ void __launch_bounds__(kBlock) kvq_read_kernel(KvQArgs a) {
   uint32_t sb[U];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    const int i = min(first + k * kPer, total - 1);
+    const int i = min(first + k * kPer, total - 1);  // nearly all are there: no branch
     const int r = i / a.nb;
     const int at = (i - r * a.nb) * kQuantBlock + sub * kPerLaneQ;
     const uint8_t* p = src + (size_t)r * (size_t)a.E + at;
     q[k] = uint2{0u, 0u};
     sb[k] = sc[i];
-    if (kVec) {
-      if (at < a.E) q[k] = *reinterpret_cast<const uint2*>(p);
-    } else {
+    if (at + kPerLaneQ <= a.E) {
+      if (kVec) {
+        q[k] = *reinterpret_cast<const uint2*>(p);
+      } else {
+        const u32x2_any w = *reinterpret_cast<const u32x2_any*>(p);
+        q[k] = uint2{w[0], w[1]};
+      }
+    } else if (!kVec) {
 #pragma unroll
       for (int e = 0; e < kPerLaneQ; ++e) {
         const uint32_t c = at + e < a.E ? (uint32_t)p[e] : 0u;
@@ -221,9 +229,9 @@ __global__ void __launch_bounds__(kBlock) kvq_read_kernel(KvQArgs a) {
     T* p = dst + (size_t)r * (size_t)a.E + at;
     float x[kPerLaneQ];
     decode8(q[k], scale_value(sb[k]), x);
-    if (kVec) {
-      if (at < a.E) store8(p, x);
-    } else {
+    if (at + kPerLaneQ <= a.E) {
+      store8<kVec>(p, x);
+    } else if (!kVec) {
 #pragma unroll
       for (int e = 0; e < kPerLaneQ; ++e)
         if (at + e < a.E) store1(p + e, x[e]);
@@ -237,8 +245,9 @@ __global__ void __launch_bounds__(kBlock) kvq_read_status_kernel(KvQArgs a) {
 }
 
 template <typename T, bool kVec, int U>
-void start_commit(const KvQArgs& a, unsigned grid, int lens, hipStream_t st) {
-  hipLaunchKernelGGL((kvq_commit_kernel<T, kVec, U>), dim3(grid), dim3(kBlock), 0, st, a, lens);
+void start_commit(const KvQArgs& a, unsigned grid, int lens, bool stream, hipStream_t st) {
+  if (stream) hipLaunchKernelGGL((kvq_commit_kernel<T, kVec, U, true>), dim3(grid), dim3(kBlock), 0, st, a, lens);
+  else hipLaunchKernelGGL((kvq_commit_kernel<T, kVec, U, false>), dim3(grid), dim3(kBlock), 0, st, a, lens);
 }
 template <typename T, bool kVec, int U>
 void start_read(const KvQArgs& a, unsigned grid, hipStream_t st) {
@@ -279,15 +288,19 @@ hipError_t launch_kv_commit_quantized(void* codes, void* scales, const void* sta
   if (plan.copies) {
     const unsigned grid = (unsigned)((size_t)P * (size_t)B * plan.chunks);
     const int pick = (dtype == 1 ? 4 : 0) + (plan.vec ? 2 : 0) + (plan.unroll == 4 ? 1 : 0);
+    // Staging that fits in the memory-side cache is likely still there (64
+    // planes x 64 x 7 entries of 1024 fp32: 26 us nontemporal, 17 plain); more
+    // than that streams (2 x 2000 bf16 entries: 42 and 48 us).
+    const bool stream = (size_t)P * B * K * E * (dtype == 1 ? 2 : 4) > ((size_t)256 << 20);
     switch (pick) {
-      case 0: start_commit<float, false, 1>(a, grid, lens, st); break;
-      case 1: start_commit<float, false, 4>(a, grid, lens, st); break;
-      case 2: start_commit<float, true, 1>(a, grid, lens, st); break;
-      case 3: start_commit<float, true, 4>(a, grid, lens, st); break;
-      case 4: start_commit<uint16_t, false, 1>(a, grid, lens, st); break;
-      case 5: start_commit<uint16_t, false, 4>(a, grid, lens, st); break;
-      case 6: start_commit<uint16_t, true, 1>(a, grid, lens, st); break;
-      default: start_commit<uint16_t, true, 4>(a, grid, lens, st); break;
+      case 0: start_commit<float, false, 1>(a, grid, lens, stream, st); break;
+      case 1: start_commit<float, false, 4>(a, grid, lens, stream, st); break;
+      case 2: start_commit<float, true, 1>(a, grid, lens, stream, st); break;
+      case 3: start_commit<float, true, 4>(a, grid, lens, stream, st); break;
+      case 4: start_commit<uint16_t, false, 1>(a, grid, lens, stream, st); break;
+      case 5: start_commit<uint16_t, false, 4>(a, grid, lens, stream, st); break;
+      case 6: start_commit<uint16_t, true, 1>(a, grid, lens, stream, st); break;
+      default: start_commit<uint16_t, true, 4>(a, grid, lens, stream, st); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || lens) return e;
@@ -317,16 +330,15 @@ hipError_t launch_kv_read_quantized(const void* codes, const void* scales, const
     return hipGetLastError();
   }
   const unsigned grid = (unsigned)((size_t)P * (size_t)B * plan.chunks);
-  const int pick = (dtype == 1 ? 4 : 0) + (plan.vec ? 2 : 0) + (plan.unroll == 4 ? 1 : 0);
-  switch (pick) {
-    case 0: start_read<float, false, 1>(a, grid, st); break;
-    case 1: start_read<float, false, 4>(a, grid, st); break;
-    case 2: start_read<float, true, 1>(a, grid, st); break;
-    case 3: start_read<float, true, 4>(a, grid, st); break;
-    case 4: start_read<uint16_t, false, 1>(a, grid, st); break;
-    case 5: start_read<uint16_t, false, 4>(a, grid, st); break;
-    case 6: start_read<uint16_t, true, 1>(a, grid, st); break;
-    default: start_read<uint16_t, true, 4>(a, grid, st); break;
+  if (dtype != 1) {  // one unit per thread (see check_kv_quantized)
+    if (plan.vec) start_read<float, true, 1>(a, grid, st);
+    else start_read<float, false, 1>(a, grid, st);
+  } else if (plan.unroll == 4) {
+    if (plan.vec) start_read<uint16_t, true, 4>(a, grid, st);
+    else start_read<uint16_t, false, 4>(a, grid, st);
+  } else {
+    if (plan.vec) start_read<uint16_t, true, 1>(a, grid, st);
+    else start_read<uint16_t, false, 1>(a, grid, st);
   }
   return hipGetLastError();
 }
