@@ -440,8 +440,10 @@ spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype
  * the 8-bit block format, for half the bytes of the bf16 head:
  *   logits[m, s] = sum_j hq[m, j] * Wq[tok(s), j],  tok(s) = cluster_ids[s / cs] * cs + s % cs,
  * with Wq the values that the weight's codes stand for and hq those of h's,
- * quantised by the call's first launch as spec_quantize_rows does; products
- * are exact and accumulated in fp32 by the matrix cores.  With every cluster
+ * quantised by the call as spec_quantize_rows does; products are exact and
+ * accumulated in fp32 by the matrix cores (bf16 outputs: by their 8-bit form,
+ * which cuts the low bits of products beside far larger ones, about 1.5e-5 of
+ * the result, a hundredth of the output's own rounding).  With every cluster
  * selected it is the head over the whole vocabulary.
  *
  *   h            bf16 [M, d].
@@ -453,7 +455,7 @@ spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype
  *   logits       [M, N] of out_dtype out, N = n_sel * cluster_size (bf16
  *                rounds to nearest even).
  *   workspace    spec_draft_head_quantized_workspace_bytes(), 256-byte
- *                aligned: h's codes and, where the grid would leave compute
+ *                aligned (may be NULL where that is 0): h's codes and, where the grid would leave compute
  *                units idle and d is split over several blocks per output
  *                tile, their fp32 partial tiles, added in a fixed order by a
  *                last launch.  The contents need no initialisation.
@@ -466,7 +468,7 @@ spec_status_t spec_draft_head_quantized(const void* h, const void* W_codes, cons
                                         int32_t cluster_size, int32_t n_sel, void* logits, spec_dtype_t out_dtype,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of spec_draft_head_quantized (0 for an empty or invalid shape). */
+/* Workspace bytes of spec_draft_head_quantized (0: none is needed, or the shape is empty or invalid). */
 size_t spec_draft_head_quantized_workspace_bytes(int32_t M, int32_t d, int32_t V, int32_t cluster_size,
                                                  int32_t n_sel);
 

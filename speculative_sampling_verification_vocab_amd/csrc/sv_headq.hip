@@ -31,6 +31,7 @@
 #include "sv_common.h"
 #include "sv_host_quant.h"
 #include "sv_internal.h"
+#include "sv_quant.h"
 
 namespace sv {
 
@@ -42,6 +43,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct HeadQArgs {
+  const uint16_t* h;      // bf16 [M][d], where the blocks quantise it themselves
+  int d, vec_h;           // vec_h: d % 8 == 0 and 16-byte aligned rows
   const uint8_t* hq;      // [M][D]
   const uint8_t* hs;      // [M][nb]
   const uint8_t* wq;      // [V][D]
@@ -90,14 +93,19 @@ __device__ __forceinline__ void store1(void* dst, bool bf16, size_t o, float v) 
 }
 
 
-template <int WM, int WN, int WK, int TM, int TN, int NBUF>
+// kOwnH: few enough values of h that every block quantises its slice of them
+// into LDS (kHeadQOwn bytes), with no launch before it; only W rows are staged.
+template <int WM, int WN, int WK, int TM, int TN, int NBUF, bool kOwnH>
 struct HeadQTile {
-  static constexpr int kMt = 16 * WM * TM, kNt = 16 * WN * TN, kRows = kMt + kNt;
+  static constexpr int kMt = 16 * WM * TM, kNt = 16 * WN * TN, kRows = kOwnH ? kNt : kMt + kNt;  // rows staged
+  static constexpr int kH = kOwnH ? 0 : kMt;           // of those, rows of h
   static constexpr int NW = WM * WN * WK, kThreads = kWave * NW;
+  static constexpr int kOwn = kOwnH ? kHeadQOwn + kHeadQOwn / kQuantBlock : 0;  // codes and scale bytes of h
   static constexpr int kGroup = kRows / 8;             // DMA instructions per block of 128
   static constexpr int kIW = WK * kGroup / NW;         // per wave and stage of WK blocks
   static constexpr int kStage = WK * kRows * 128;      // bytes
   static constexpr int kSeg = kRows > 256 ? 32 : 64;   // blocks of 128 whose scales are in LDS at a time
+  static_assert(!kOwnH || (kMt == 16 && kHeadQOwn / kQuantBlock * kLanesPerBlock <= 6 * kThreads), "own h");
   static_assert(kRows % 8 == 0 && WK * kGroup % NW == 0, "DMA split");
   static_assert(NBUF >= 2 && (NBUF - 2) * kIW < 64, "pipeline depth");
   static_assert(kSeg % WK == 0 && WK <= 4, "scale groups");
@@ -121,16 +129,18 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi, float scale) {
 __device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float((byte << 23) & 0x7f800000u); }
 
 // kF32: the products of fp32 outputs (see above).
-template <int WM, int WN, int WK, int TM, int TN, int NBUF, bool kF32>
+template <int WM, int WN, int WK, int TM, int TN, int NBUF, bool kOwnH, bool kF32>
 __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a) {
-  using C = HeadQTile<WM, WN, WK, TM, TN, NBUF>;
+  using C = HeadQTile<WM, WN, WK, TM, TN, NBUF, kOwnH>;
+  constexpr int kH = C::kH;
   constexpr int kMt = C::kMt, kNt = C::kNt, kRows = C::kRows, NW = C::NW, kIW = C::kIW, kSeg = C::kSeg;
   // One LDS object: beside a second one the compiler waits for every DMA in
   // flight before each read of this one.
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * C::kStage + kSeg * kRows + 4 * kRows];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * C::kStage + kSeg * kRows + 4 * kRows + C::kOwn];
   uint32_t* const sc = reinterpret_cast<uint32_t*>(lds + NBUF * C::kStage);  // [kSeg / 4][kRows]: four scale bytes
   int* const token = reinterpret_cast<int*>(lds + NBUF * C::kStage + kSeg * kRows);  // W or h row of a tile row, or -1
 
+  uint8_t* const own = lds + NBUF * C::kStage + kSeg * kRows + 4 * kRows;  // h's codes, then its scale bytes
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const int wk = wave / (WM * WN), wmn = wave % (WM * WN);
@@ -146,12 +156,28 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
   const int n0 = (v / a.m_tiles) * kNt, m0 = (v % a.m_tiles) * kMt;
   const int b0 = slice * a.split_nb, blocks = min(a.nb - b0, a.split_nb);
 
+  constexpr int kOwnUnits = kOwnH ? 6 : 1;
+  float ox[kOwnUnits][kPerLaneQ];
+  int om[kOwnUnits], ob[kOwnUnits];  // row and block of this slice
+  if constexpr (kOwnH) {
+    // h's values, on their way while the tile's rows are looked up.
+#pragma unroll
+    for (int k = 0; k < kOwnUnits; ++k) {
+      const int i = min((int)threadIdx.x / kLanesPerBlock + k * (C::kThreads / kLanesPerBlock), a.M * blocks - 1);
+      om[k] = i / blocks, ob[k] = i - om[k] * blocks;
+      const int at = (b0 + ob[k]) * kQuantBlock + (int)(threadIdx.x % kLanesPerBlock) * kPerLaneQ;
+      const uint16_t* p = a.h + (size_t)om[k] * (size_t)a.d + at;
+      if (a.vec_h) load8<uint16_t, true, false>(p, a.d - at, ox[k]);
+      else load8<uint16_t, false, false>(p, a.d - at, ox[k]);
+    }
+  }
+
   for (int r = threadIdx.x; r < kRows; r += C::kThreads) {
     int t = -1;
-    if (r < kMt) {
+    if (r < kH) {
       if (m0 + r < a.M) t = m0 + r;
-    } else if (n0 + r - kMt < a.N) {
-      const int n = n0 + r - kMt, c = n / a.cs, cl = a.cids[c];
+    } else if (n0 + r - kH < a.N) {
+      const int n = n0 + r - kH, c = n / a.cs, cl = a.cids[c];
       if (cl >= 0 && cl < a.nclusters) t = cl * a.cs + (n - c * a.cs);
     }
     token[r] = t;
@@ -159,33 +185,26 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
   __syncthreads();
 
   // DMA instruction j of this wave: block `sub` of the stage, tile rows 8 * g ..
-  // Rows that are none load h's first row; their outputs are not stored, or
-  // stored as zeros.
+  // Rows that are none load the first one of h or W; their outputs are not
+  // stored, or stored as zeros.
   const size_t D = (size_t)a.nb * kQuantBlock;
   const uint8_t* src[kIW];
 #pragma unroll
   for (int j = 0; j < kIW; ++j) {
     const int g = (j * NW + wave) % C::kGroup, r = 8 * g + (lane >> 3);
     const int t = token[r];
-    src[j] = (t < 0 ? a.hq : (r < kMt ? a.hq : a.wq) + (size_t)t * D) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    src[j] = (r < kH ? a.hq : a.wq) + (size_t)max(t, 0) * D + 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
-  // Scales of blocks first .. first + seg - 1 of the rows.
-  auto load_scales = [&](int first, int seg) {
-    const int groups = (seg + 3) / 4;
-    for (int i = threadIdx.x; i < groups * kRows; i += C::kThreads) {
-      const int g = i / kRows, r = i - g * kRows, t = token[r];
-      const int b = first + 4 * g;
-      const uint8_t* p = (r < kMt ? a.hs : a.ws) + (t < 0 ? 0 : (size_t)t * a.nb) + b;
-      uint32_t w = 0;
-      if (a.dword_scales) {
-        w = *reinterpret_cast<const uint32_t*>(p);
-      } else {
+  // Scales of blocks first .. first + seg - 1 of the rows, word i of [group][row].
+  auto scale_word = [&](int i, int first) {
+    const int g = i / kRows, r = i - g * kRows, b = first + 4 * g;
+    const uint8_t* p = (r < kH ? a.hs : a.ws) + (size_t)max(token[r], 0) * a.nb + b;
+    if (a.dword_scales) return *reinterpret_cast<const uint32_t*>(p);
+    uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (b + e < a.nb) w |= (uint32_t)p[e] << (8 * e);
-      }
-      sc[g * kRows + r] = w;
-    }
+    for (int e = 0; e < 4; ++e)
+      if (b + e < a.nb) w |= (uint32_t)p[e] << (8 * e);
+    return w;
   };
 
   f32x4 acc[TM][TN];
@@ -195,13 +214,38 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int frow = lane & 15, fc = lane >> 4;
-  const int arow0 = wm * 16 * TM + frow, brow0 = kMt + wn * 16 * TN + frow;
+  const int arow0 = wm * 16 * TM + frow, brow0 = kH + wn * 16 * TN + frow;
   auto fragment = [&](const uint8_t* buf, int r) {
     const int x = (r >> 1) & 7;
     const u32x4 lo = *reinterpret_cast<const u32x4*>(buf + r * 128 + 16 * (fc ^ x));
     const u32x4 hi = *reinterpret_cast<const u32x4*>(buf + r * 128 + 16 * ((fc + 4) ^ x));
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
+  // h's slice in LDS: a row's blocks one after the other, rows 128 bytes further
+  // apart than that, so that neighbours meet other banks; pieces swizzled as
+  // in a stage.  Rows past M read the last one's.
+  const int own_row = (blocks + 1) * kQuantBlock;
+  auto quantize_own = [&]() {
+#pragma unroll
+    for (int k = 0; k < kOwnUnits; ++k) {
+      if (k * (C::kThreads / kLanesPerBlock) >= a.M * blocks) break;
+      int byte;
+      const uint2 q = quantize8(ox[k], &byte);  // the last unit again in spare lanes: the same codes
+      const int sub = threadIdx.x % kLanesPerBlock;
+      *reinterpret_cast<uint2*>(own + om[k] * own_row + ob[k] * kQuantBlock +
+                                16 * ((sub / 2) ^ ((om[k] >> 1) & 7)) + 8 * (sub & 1)) = q;
+      if (sub == 0) own[kHeadQOwn + ob[k] * a.M + om[k]] = (uint8_t)byte;
+    }
+  };
+  const int own_m = min(frow, a.M - 1);
+  auto own_fragment = [&](int b) {
+    const uint8_t* p = own + own_m * own_row + b * kQuantBlock;
+    const int x = (own_m >> 1) & 7;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(p + 16 * (fc ^ x));
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(p + 16 * ((fc + 4) ^ x));
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+
   // Segments of up to kSeg blocks: their scales go to LDS, then the stages run
   // with no other memory loads between the DMAs that the waits count.
   for (int first = b0; first < b0 + blocks; first += kSeg) {
@@ -228,7 +272,16 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
 #pragma unroll
     for (int s = 0; s < NBUF - 1; ++s)
       if (s < stages) issue(s);
-    load_scales(first, seg);
+    const int words = (seg + 3) / 4 * kRows;
+    if constexpr (kOwnH) {
+      static_assert(kSeg / 4 * kRows <= C::kThreads, "one word each");
+      uint32_t w = 0;
+      if ((int)threadIdx.x < words) w = scale_word(threadIdx.x, first);
+      if (first == b0) quantize_own();
+      if ((int)threadIdx.x < words) sc[threadIdx.x] = w;
+    } else {
+      for (int i = threadIdx.x; i < words; i += C::kThreads) sc[i] = scale_word(i, first);
+    }
     __syncthreads();
 
     uint32_t sa[TM], sb[TN];
@@ -242,16 +295,19 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
       const int kb = stage_of(s) * WK + wk;  // this wave's block of the segment
       if ((kb & 3) < WK || s == 0) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = sc[kb / 4 * kRows + arow0 + 16 * i] >> (8 * (kb & 3));
+        for (int i = 0; i < TM; ++i)
+          if (!kOwnH) sa[i] = sc[kb / 4 * kRows + arow0 + 16 * i] >> (8 * (kb & 3));
 #pragma unroll
         for (int j = 0; j < TN; ++j) sb[j] = sc[kb / 4 * kRows + brow0 + 16 * j] >> (8 * (kb & 3));
       } else {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] >>= 8 * WK;
+        for (int i = 0; i < TM; ++i)
+          if (!kOwnH) sa[i] >>= 8 * WK;
 #pragma unroll
         for (int j = 0; j < TN; ++j) sb[j] >>= 8 * WK;
       }
       if (WK > 1 && kb >= seg) continue;  // the last stage is short
+      if (kOwnH) sa[0] = own[kHeadQOwn + (first - b0 + kb) * a.M + own_m];
       const uint8_t* buf = lds + s % NBUF * C::kStage + wk * kRows * 128;
       i32x8 bf[TN];
 #pragma unroll
@@ -265,7 +321,7 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
           for (int p = 0; p < 4; ++p) bv[j][p] = codes_to_bf16(bf[j][2 * p], bf[j][2 * p + 1], scale_float(sb[j]));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const i32x8 af = fragment(buf, arow0 + 16 * i);
+          const i32x8 af = kOwnH ? own_fragment(first - b0 + kb) : fragment(buf, arow0 + 16 * i);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const bf16x8 av = codes_to_bf16(af[2 * p], af[2 * p + 1], scale_float(sa[i]));
@@ -277,7 +333,7 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
       } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const i32x8 af = fragment(buf, arow0 + 16 * i);
+          const i32x8 af = kOwnH ? own_fragment(first - b0 + kb) : fragment(buf, arow0 + 16 * i);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf[j], acc[i][j], 0, 0, 0, (int)sa[i], 0,
@@ -328,7 +384,7 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
   const bool vec = a.N % 4 == 0 && (uintptr_t)dst % (bf16 ? 8 : 16) == 0;
   bool none[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) none[e] = token[kMt + c4 + e] < 0;
+  for (int e = 0; e < 4; ++e) none[e] = token[kH + c4 + e] < 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     if (i > 0) __syncthreads();
@@ -385,9 +441,9 @@ __global__ void __launch_bounds__(kBlock) headq_reduce_kernel(HeadQArgs a) {
   }
 }
 
-template <int WM, int WN, int WK, int TM, int TN, int NBUF>
+template <int WM, int WN, int WK, int TM, int TN, int NBUF, bool kOwnH = false>
 hipError_t launch_tile(HeadQArgs a, const HeadQPlan& plan, hipStream_t st) {
-  using C = HeadQTile<WM, WN, WK, TM, TN, NBUF>;
+  using C = HeadQTile<WM, WN, WK, TM, TN, NBUF, kOwnH>;
   if (plan.mt != C::kMt || plan.nt != C::kNt) return hipErrorInvalidValue;
   a.m_tiles = (a.M + C::kMt - 1) / C::kMt;
   const long long tiles = ((long long)a.N + C::kNt - 1) / C::kNt * a.m_tiles;
@@ -398,8 +454,8 @@ hipError_t launch_tile(HeadQArgs a, const HeadQPlan& plan, hipStream_t st) {
   a.per_xcd = (int)((total + 7) / 8);
   a.dword_scales = a.nb % 4 == 0 && a.split_nb % 4 == 0 && (uintptr_t)a.hs % 4 == 0 && (uintptr_t)a.ws % 4 == 0;
   const dim3 grid((unsigned)a.per_xcd * 8), block(C::kThreads);
-  if (a.out_bf16) hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, false>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, true>), grid, block, 0, st, a);
+  if (a.out_bf16) hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, kOwnH, false>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((headq_kernel<WM, WN, WK, TM, TN, NBUF, kOwnH, true>), grid, block, 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split == 1) return e;
   const size_t quads = ((size_t)a.M * (size_t)a.N + 3) / 4;
@@ -427,6 +483,12 @@ hipError_t launch_head_quantized(const void* h, const void* W_codes, const void*
   a.out = out;
   a.out_bf16 = out_dtype == 1;
   a.partial = reinterpret_cast<float*>(base + w.partial);
+  if (plan.own_h) {
+    a.h = static_cast<const uint16_t*>(h);
+    a.d = d;
+    a.vec_h = d % 8 == 0 && (uintptr_t)h % 16 == 0;
+    return launch_tile<1, 2, 4, 1, 1, 3, true>(a, plan, st);
+  }
   const hipError_t e = launch_quantize_rows(h, M, d, 1, base + w.codes, base + w.scales, st);
   if (e != hipSuccess) return e;
   switch (plan.tile) {

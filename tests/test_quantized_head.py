@@ -84,7 +84,8 @@ def test_ids_out_of_range_and_repeated(M):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,d,V", [(5, 4096, 24000), (40, 2048, 17000), (200, 1024, 36000), (100, 384, 66000),
-                                   (300, 640, 26000), (513, 1024, 17410), (129, 4224, 52000)])
+                                   (300, 640, 26000), (513, 1024, 17410), (129, 4224, 52000),
+                                   (2, 8448, 8300), (16, 4096, 9000), (9, 3200, 8200), (5, 4095, 8200), (1, 23000, 8200)])
 def test_wide_shortlists(M, d, V):
     """Grids of many tiles, without a split."""
     check(M, d, V, 1, np.arange(V - 3), BF)
@@ -169,9 +170,11 @@ def test_refusals():
     assert call(cs=7) == UNSUP
     assert call(h=0x10001) == INVALID and call(wc=0x20008) == INVALID and call(ids=0x40002) == INVALID
     assert call(out=0x50002) == INVALID and call(out=0x50001, dt=1) == INVALID
-    need = size(4, 256, 1000, 10, 20)
-    assert need >= 4 * 256 + 4 * 2
-    assert call(work=None) == WS and call(work=0x100080) == WS and call(wb=need - 1) == WS
+    need = size(40, 256, 1000, 10, 20)
+    assert need >= 40 * 256 + 40 * 2
+    for o in (dict(work=None), dict(work=0x100080), dict(wb=need - 1)):
+        assert call(M=40, **o) == WS
+    assert size(4, 256, 1000, 10, 20) == 0                # few values of h: none needed
     assert call(M=0, h=None) == OK and call(n=0, out=None) == OK
     assert call(M=0x7fffffff, d=128, V=1 << 20, cs=1, n=1 << 20) == UNSUP
     assert call(d=0x7fffffff) == UNSUP
