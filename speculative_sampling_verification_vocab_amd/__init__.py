@@ -513,10 +513,23 @@ def _raw_stream(device: torch.device, stream=None) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _capturing(device: torch.device, stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Workspace], stream) -> torch.Tensor:
-    """At least `need` bytes of workspace: the caller's, or the default one of (device, stream)."""
+    """At least `need` bytes of workspace: the caller's, or the default one of
+    (device, stream).  A call under graph capture gets memory of the graph's own:
+    graphs that shared a default workspace would race when replayed at once, and
+    one that grows later would leave them with memory that is no longer theirs."""
     if workspace is not None:
         return workspace.get(need, stream, device)
+    if _capturing(device, stream):
+        with torch.cuda.stream(_stream_of(device, stream)):
+            return torch.empty(need, dtype=torch.uint8, device=device)
     ws = _default_ws.get((device, raw))
     if ws is not None and ws.buf.numel() >= need:
         return ws.buf  # allocated on this stream: calls on others have workspaces of their own

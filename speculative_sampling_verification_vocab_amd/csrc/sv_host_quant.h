@@ -118,7 +118,7 @@ inline spec_status_t check_head_quantized(int32_t M, int32_t d, int32_t V, int32
   *empty = M == 0 || n_sel == 0;
   if (*empty) return SPEC_OK;
   const int32_t N = n_sel * cluster_size;  // at most V
-  if (d > 0x7fffffff - kQuantBlock) return SPEC_ERR_UNSUPPORTED;
+  if (M > (1 << 30) || N > (1 << 30) || d > (1 << 30)) return SPEC_ERR_UNSUPPORTED;  // a tile past the end stays in int32
   *plan = head_quantized_plan(M, d, N);
   if (!head_quantized_layout(M, d, N, *plan, w)) return SPEC_ERR_UNSUPPORTED;
   size_t out = 0, wb = 0;

@@ -545,6 +545,7 @@ __device__ __forceinline__ void pick(const LpArgs& a, size_t row_i, const T* row
   __syncthreads();
   const int have = sh.count;
   if (sel > kSelect || have > kList) {
+    __syncthreads();  // every wave has read the counts before one of them is used again
     if (wave == 0) pick_by_chunks<T>(a, row_i, row, maxima, sh.list, &sh.count, law, lane);
     return;
   }

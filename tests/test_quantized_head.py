@@ -108,6 +108,24 @@ def test_scales_at_their_ends():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M", [3, 40])
+def test_small_weights(M, out):
+    """Weights down to 2^-118, whose smallest codes stand for values below the normal range of bf16 and fp32."""
+    h, W = case(M, 512, 90, 12)
+    W = (W.float() * 2.0 ** -112).to(BF)
+    want, mag = product(h, W, np.arange(90))
+    codes, scales = sv().spec_quantize_rows(W.to(DEV))
+    got = sv().spec_draft_head_quantized(h.to(DEV), codes, scales, torch.arange(90, dtype=torch.int32, device=DEV), 1,
+                                         dtype=out)
+    err = np.abs(R.as_f64(got) - want)
+    # flushing what lies below the normal range would cost 2^-126 |h| a product
+    tol = (512 + 16) * 2.0 ** -23 * mag + (2.0 ** -8 * np.abs(want) if out == BF else 0.0) + 2.0 ** -133
+    flushed = 2.0 ** -126 * np.abs(R.as_f64(h)).sum(1, keepdims=True)
+    assert np.all(err <= tol + flushed)
+
+
+@pytest.mark.gpu
 def test_nan_stays_in_its_row():
     h, W = case(6, 256, 50, 9)
     h[2, 17] = float("nan")

@@ -133,6 +133,40 @@ def test_masked_rows(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [500, 40003, 300001])
+def test_tokens_far_below_the_rest(V, dtype):
+    """A token's own logit is no reference for its row: the lowest value, -inf, far below, at a low temperature."""
+    x = normal(6, V, dtype, 22)
+    x[0, 7] = torch.finfo(dtype).min
+    x[1, 7] = -INF
+    x[2, 7] = -1.0e4
+    x[3, 7] = -60.0
+    x[4, :] = -50.0
+    x[4, V - 1] = 10.0
+    x[5, :V // 2] = torch.finfo(dtype).min
+    for T in (1.0, 0.01, 100.0):
+        check(x, [7, 7, 7, 7, 7, 7], 12, T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [9001, 66000, 300001])
+def test_many_equal_rows_at_once(V, dtype):
+    """Rows that fall back to one chunk after another, on every CU at once, among ordinary ones."""
+    N = 600
+    x = normal(N, V, dtype, 23)
+    x[::2] = 1.5
+    x[1::4, 100:5000] = 20.0
+    t = torch.arange(N, dtype=torch.int32) % V
+    got = [v.cpu().numpy() for v in sv().spec_token_logprobs(x.to(DEV), t.to(DEV), 20)]
+    some = [0, 1, 2, 3, 5, 301, 598, 599]
+    compare(x[some], t[some], 20, 1.0, [v[some] for v in got])
+    assert (got[2][::2] == np.arange(20)).all()
+    assert (got[2][1::4] == np.arange(100, 120)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("N,V", [(3, 40000), (3, 300001), (300, 40003)])
 def test_masked_before_a_fault(N, V, dtype):
     """-inf in the first tiles and a NaN or +inf in a later one, in each form of the launch."""
