@@ -27,6 +27,13 @@
 // every WK-th block of 128, their sums added through LDS at the end.
 // Narrow shortlists split d over several blocks of threads; their fp32 tiles
 // are added in a fixed order by a second launch.
+//
+// Measured at d = 4096, bf16 out (GPU time; see head_quantized_plan for the
+// tiles): N = 32768: M = 1, 16, 64, 128: 27, 28, 29, 34 us (134 MB of W: 19 us
+// at the read stream's rate); N = 128256: M = 8, 128: 100, 123 us; M = 1792:
+// 885 us, 2.1 PFLOP/s, where a library's product of 8192^3 reaches 3.1 (the
+// 256 x 256 tile's stages meet at one barrier with two buffers, and LDS reads
+// take three quarters of the products' time).
 
 #include "sv_common.h"
 #include "sv_host_quant.h"

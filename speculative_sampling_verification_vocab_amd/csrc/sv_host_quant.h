@@ -253,12 +253,20 @@ struct LogprobsShape {
 
 constexpr int kMaxTop = SPEC_MAX_TOP;
 constexpr int kChunksPerTile = 8;
-constexpr int kLpShortRow = 8;    // tiles of a row that always is one block's
-constexpr int kLpRowTiles = 16;   // tiles of a row that is one block's in small batches: one per wave
-constexpr int kLpWideRows = 256;  // the small batches; their blocks have 16 waves
+// Rows of up to 16 tiles are one block's, in one launch: 48 rows of 65536 bf16
+// take 10.5 us so and 12.1 us in parts, 2048 of 32000 37.0 and 39.7, 1024 of
+// 65536 30.5 and 34.6; 300 of 65536, the worst, 18.2 and 17.7.  Beyond that a
+// compute unit is too slow for a row of its own: 48 rows of 128256 take 17 us
+// in blocks of 16 waves and 15.3 in parts.
+constexpr int kLpRowTiles = 16;
+// Up to so many rows, one per CU, those blocks have 16 waves, else four: 256
+// rows of 32000 take 11.4 us with 16; 512 take 21.3 with 16 and 16.1 with four.
+constexpr int kLpWideRows = 256;
 constexpr int kLpManyRows = 768;  // rows joined by blocks of four waves from here
+// Parts of rows: as many as keep every CU in blocks, of up to 16 tiles (2048 to
+// 8192 of them and 8 to 16 tiles measured within 3 %).
 constexpr int kLpPartsWanted = 8192;
-constexpr int kLpPartTiles = 16;  // most tiles per part
+constexpr int kLpPartTiles = 16;
 
 struct LogprobsPart {
   double R;  // reference, in units of log 2: sums are of 2^(x * s - R)
@@ -284,7 +292,7 @@ inline spec_status_t check_logprobs(int32_t N, int32_t V, spec_dtype_t dtype, in
   // The plan goes by the tiles that an aligned row has, so that the alignment
   // decides nothing but NT.
   const int full = (V + s->tile - 1) / s->tile;
-  const bool one = full <= kLpShortRow || (N <= kLpWideRows && full <= kLpRowTiles);
+  const bool one = full <= kLpRowTiles;
   long long tiles = (long long)N * full / kLpPartsWanted / kWavesPerBlock * kWavesPerBlock;
   tiles = tiles < kWavesPerBlock ? kWavesPerBlock : tiles > kLpPartTiles ? kLpPartTiles : tiles;
   s->part_tiles = (int)tiles;
