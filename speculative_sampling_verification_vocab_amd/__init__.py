@@ -514,9 +514,10 @@ def _raw_stream(device: torch.device, stream=None) -> int:
 
 
 def _capturing(device: torch.device, stream) -> bool:
-    if stream is None:
+    """Whether the call's stream is under graph capture (torch asks about the current device's only)."""
+    if stream is None and torch.cuda.current_device() == device.index:
         return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_of(device, stream)):
         return torch.cuda.is_current_stream_capturing()
 
 
