@@ -394,8 +394,8 @@ spec_status_t spec_kv_commit(void* cache, const void* staging, const int32_t* ac
  *                  be NULL where that is 0); its contents need no initialisation.
  * A row that is not read, and one whose largest logit is not finite or that
  * holds a NaN, gets NaN in its float outputs and -1 in top_ids.
- * One launch for short rows and small batches, two for the others.  Sums are
- * held in fp32 over a lane's 64 (bf16) or 32 (fp32) logits of a tile and in
+ * One launch for rows of up to 65536 bf16 or 32768 fp32 logits, two for longer
+ * ones.  Sums are held in fp32 over a lane's 64 (bf16) or 32 (fp32) logits of a tile and in
  * fp64 beyond; results are the same on every call.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, sizes below
  * zero, V < 1, a temperature outside its range, an unknown dtype;
@@ -442,7 +442,7 @@ spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype
  * with Wq the values that the weight's codes stand for and hq those of h's,
  * quantised by the call as spec_quantize_rows does; products are exact and
  * accumulated in fp32 by the matrix cores (bf16 outputs: by their 8-bit form,
- * which cuts the low bits of products beside far larger ones, about 1.5e-5 of
+ * which cuts the low bits of products beside far larger ones, about 1.4e-5 of
  * the result, a hundredth of the output's own rounding).  With every cluster
  * selected it is the head over the whole vocabulary.
  *
@@ -455,10 +455,11 @@ spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype
  *   logits       [M, N] of out_dtype out, N = n_sel * cluster_size (bf16
  *                rounds to nearest even).
  *   workspace    spec_draft_head_quantized_workspace_bytes(), 256-byte
- *                aligned (may be NULL where that is 0): h's codes and, where the grid would leave compute
- *                units idle and d is split over several blocks per output
- *                tile, their fp32 partial tiles, added in a fixed order by a
- *                last launch.  The contents need no initialisation.
+ *                aligned (may be NULL where that is 0): h's codes and, where
+ *                the grid would leave compute units idle and d is split over
+ *                several blocks per output tile, their fp32 partial tiles,
+ *                added in a fixed order by a last launch.  The contents need
+ *                no initialisation.
  * Results are the same on every call.  Errors: SPEC_ERR_INVALID_ARG for NULL
  * or misaligned buffers or bad sizes; SPEC_ERR_WORKSPACE; SPEC_ERR_UNSUPPORTED
  * if V % cluster_size != 0, or for buffers or grids too large.

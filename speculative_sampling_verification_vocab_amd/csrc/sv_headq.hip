@@ -31,7 +31,7 @@
 // Measured at d = 4096, bf16 out (GPU time; see head_quantized_plan for the
 // tiles): N = 32768: M = 1, 16, 64, 128: 27, 28, 29, 34 us (134 MB of W: 19 us
 // at the read stream's rate); N = 128256: M = 8, 128: 100, 123 us; M = 1792:
-// 885 us, 2.1 PFLOP/s, where a library's product of 8192^3 reaches 3.1 (the
+// 872-925 us by the card, 2.0-2.2 PFLOP/s, where a library's product of 8192^3 reaches 3.1 (the
 // 256 x 256 tile's stages meet at one barrier with two buffers, and LDS reads
 // take three quarters of the products' time).
 
@@ -74,7 +74,10 @@ __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
+// A barrier that leaves DMAs in flight.  The wave's own LDS reads are done
+// before it, wherever the compiler puts the products that use them: the buffer
+// they come from is refilled behind it.
+__device__ __forceinline__ void block_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // One 16-byte global_load_lds per lane: lane l's bytes land at lds + 16 * l.
 __device__ __forceinline__ void dma16(const uint8_t* g, uint8_t* lds) {
@@ -98,7 +101,6 @@ __device__ __forceinline__ void store1(void* dst, bool bf16, size_t o, float v) 
   if (bf16) static_cast<uint16_t*>(dst)[o] = __builtin_bit_cast(uint16_t, (__bf16)v);
   else static_cast<float*>(dst)[o] = v;
 }
-
 
 // kOwnH: few enough values of h that every block quantises its slice of them
 // into LDS (kHeadQOwn bytes), with no launch before it; only W rows are staged.
