@@ -31,9 +31,9 @@
 // Measured at d = 4096, bf16 out (GPU time; see head_quantized_plan for the
 // tiles): N = 32768: M = 1, 16, 64, 128: 27, 28, 29, 34 us (134 MB of W: 19 us
 // at the read stream's rate); N = 128256: M = 8, 128: 100, 123 us; M = 1792:
-// 872-925 us by the card, 2.0-2.2 PFLOP/s, where a library's product of 8192^3 reaches 3.1 (the
-// 256 x 256 tile's stages meet at one barrier with two buffers, and LDS reads
-// take three quarters of the products' time).
+// 872-925 us by the card, 2.0-2.2 PFLOP/s, where a library's product of 8192^3
+// reaches 3.1 (the 256 x 256 tile's stages meet at one barrier with two
+// buffers, and LDS reads take three quarters of the products' time).
 
 #include "sv_common.h"
 #include "sv_host_quant.h"
@@ -311,9 +311,9 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) headq_kernel(HeadQArgs a
       } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-          if (!kOwnH) sa[i] >>= 8 * WK;
+          if (!kOwnH) sa[i] >>= 8 * (WK % 4);  // with WK = 4 each stage reads its word
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sb[j] >>= 8 * WK;
+        for (int j = 0; j < TN; ++j) sb[j] >>= 8 * (WK % 4);
       }
       if (WK > 1 && kb >= seg) continue;  // the last stage is short
       if (kOwnH) sa[0] = own[kHeadQOwn + (first - b0 + kb) * a.M + own_m];
