@@ -34,6 +34,8 @@
 // 872-925 us by the card, 2.0-2.2 PFLOP/s, where a library's product of 8192^3
 // reaches 3.1 (the 256 x 256 tile's stages meet at one barrier with two
 // buffers, and LDS reads take three quarters of the products' time).
+// fp32 out: M = 128, N = 32768: 49 us; M = 1792, N = 32768: 414 us, 1.16 PFLOP/s
+// (a library's bf16 product of 8192^3: 1.40).
 
 #include "sv_common.h"
 #include "sv_host_quant.h"
