@@ -2,7 +2,10 @@
 
 Python face of libspecverify.so.  Functions take torch tensors on a ROCm GPU
 and call the C ABI on torch's current stream; results are new tensors on the
-same device.  See include/specverify.h for the full contract.
+same device.  See include/specverify.h for the full contract.  A call that is
+given another stream runs on that one: the caller orders it after what writes
+its inputs and keeps those until it has run, and its results are allocated on
+that stream.
 
     accepted_len, out_tokens = spec_verify(target, draft, draft_tokens, uniforms,
                                            temperature=1.0, mode="sample")
@@ -54,6 +57,26 @@ def _stream_of(device: torch.device, stream=None):
 
 def _stream_handle(device: torch.device, stream=None):
     return ctypes.c_void_p(_stream_of(device, stream).cuda_stream)
+
+
+def _result(shape, dtype: torch.dtype, device: torch.device, stream=None) -> torch.Tensor:
+    """An uninitialised tensor that a call on `stream` writes.
+
+    The caching allocator hands a block that was freed out again to its own
+    stream without waiting, so the block must belong to the stream whose
+    kernels write it: on the current stream's, an earlier kernel of that stream
+    could still be at work, and a dropped result would go to another tensor
+    before the call has written it.  The current stream, on which the caller
+    may go on with the result, is recorded with the allocator."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def spec_verify_workspace_bytes(B: int, K: int, V: int, dtype: torch.dtype, mode: str = "sample") -> int:
@@ -124,10 +147,10 @@ def spec_verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_token
     B, K, V, dt, sampling = _check_verify_inputs(target, draft, draft_tokens, uniforms, mode)
     dev = target.device
     lib = _native.load()
-    acc = torch.empty(B, dtype=torch.int32, device=dev)
-    out = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    pt = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
-    pd = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
+    acc = _result((B,), torch.int32, dev, stream)
+    out = _result((B, K + 1), torch.int32, dev, stream)
+    pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
+    pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES[mode])
     ws = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
     args = [_ptr(target), _ptr(draft) if sampling else None,
@@ -173,10 +196,10 @@ class VerifyPlan:
         lib = _native.load()
         self._lib = lib
         self._dt, self._m = _DTYPES[dtype], _MODES[mode]
-        self.accepted_len = torch.empty(B, dtype=torch.int32, device=dev)
-        self.out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-        self.p_target = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
-        self.p_draft = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
+        self.accepted_len = _result((B,), torch.int32, dev, stream)
+        self.out_tokens = _result((B, K + 1), torch.int32, dev, stream)
+        self.p_target = _result((B, K), torch.float32, dev, stream) if return_probs else None
+        self.p_draft = _result((B, K), torch.float32, dev, stream) if return_probs else None
         s = _stream_of(dev, stream)
         need = lib.spec_verify_workspace_bytes(B, K, V, self._dt, self._m)
         with torch.cuda.stream(s):
@@ -294,8 +317,8 @@ def spec_draft_head_shortlist(h: torch.Tensor, W: torch.Tensor, cluster_ids: tor
         raise ValueError("W must be [V, d]")
     n_sel = cluster_ids.shape[1]
     dev = h.device
-    comp = torch.empty((B, K, n_sel * cluster_size), dtype=torch.float32, device=dev) if compact else None
-    dn = torch.empty((B, K, V), dtype=dense_dtype, device=dev) if dense else None
+    comp = _result((B, K, n_sel * cluster_size), torch.float32, dev, stream) if compact else None
+    dn = _result((B, K, V), dense_dtype, dev, stream) if dense else None
     lib = _native.load()
     st = lib.spec_draft_head_shortlist(_ptr(h), _ptr(W), _ptr(cluster_ids), B, K, d, V, cluster_size, n_sel,
                                        _ptr(comp), _ptr(dn), _DTYPES[dense_dtype] if dense else 0, None, 0,
@@ -331,7 +354,7 @@ def spec_kv_commit(cache: torch.Tensor, staging: torch.Tensor, accepted_len: tor
         if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous int32 [B]")
     if status is None:
-        status = torch.empty(B, dtype=torch.int32, device=cache.device)
+        status = _result((B,), torch.int32, cache.device, stream)
     else:
         _need_gpu(status, "status", cache.device)
         if status.dtype != torch.int32 or tuple(status.shape) != (B,):
@@ -389,10 +412,10 @@ def spec_verify_sparse_draft(target: torch.Tensor, draft_compact: torch.Tensor, 
         raise ValueError("uniforms must be float32 [B, K+1, 2]")
     lib = _native.load()
     dev = target.device
-    acc = torch.empty(B, dtype=torch.int32, device=dev)
-    out = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    pt = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
-    pd = torch.empty((B, K), dtype=torch.float32, device=dev) if return_probs else None
+    acc = _result((B,), torch.int32, dev, stream)
+    out = _result((B, K + 1), torch.int32, dev, stream)
+    pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
+    pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES["sample"])
     ws = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
     st = lib.spec_verify_sparse_draft(_ptr(target), _ptr(draft_compact) if K > 0 else None,
@@ -429,7 +452,7 @@ def spec_draft_head_positions(h: torch.Tensor, W: torch.Tensor, cluster_ids: tor
     if dt is None:
         raise ValueError("dtype must be bfloat16 or float32")
     if out is None:
-        out = torch.empty((B, K, L), dtype=dtype, device=h.device)
+        out = _result((B, K, L), dtype, h.device, stream)
     elif out.dtype != dtype or tuple(out.shape) != (B, K, L) or not out.is_contiguous() \
             or out.device != h.device:
         raise ValueError("out must be on h's device, a contiguous [B, K, L] tensor of dtype")
@@ -466,7 +489,7 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
         raise ValueError("dtype must be bfloat16 or float32")
     shape = tuple(h.shape[:-1]) + (N,)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=h.device)
+        out = _result(shape, dtype, h.device, stream)
     elif out.dtype != dtype or tuple(out.shape) != shape or not out.is_contiguous() \
             or out.device != h.device:
         raise ValueError("out must be on h's device, contiguous with shape h.shape[:-1] + (N,) and dtype")
@@ -573,8 +596,8 @@ def spec_quantize_rows(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = 
     rows = x.numel() // d
     _fits(rows, d)
     if out is None:
-        codes = torch.empty(lead + (nb * _BLOCK,), dtype=_CODES, device=dev)
-        scales = torch.empty(lead + (nb,), dtype=_SCALES, device=dev)
+        codes = _result(lead + (nb * _BLOCK,), _CODES, dev, stream)
+        scales = _result(lead + (nb,), _SCALES, dev, stream)
     else:
         if len(out) != 2:
             raise ValueError("out must hold codes and scales")
@@ -620,7 +643,7 @@ def spec_draft_head_quantized(h: torch.Tensor, W_codes: torch.Tensor, W_scales: 
     need = lib.spec_draft_head_quantized_workspace_bytes(M, d, V, cluster_size, n_sel)
     shape = shape[:-1] + (n_sel * cluster_size,)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = _result(shape, dtype, dev, stream)
     else:
         _need(out, "out", dtype, shape, dev)
     raw = _raw_stream(dev, stream)
@@ -682,7 +705,7 @@ def spec_kv_commit_quantized(codes: torch.Tensor, scales: torch.Tensor, staging:
     else:
         _need(new_len, "new_len", torch.int32, (B,), dev)
     if status is None:
-        status = torch.empty_like(cache_len)
+        status = _result((B,), torch.int32, dev, stream)
     else:
         _need(status, "status", torch.int32, (B,), dev)
     _call(_native.load().spec_kv_commit_quantized, "spec_kv_commit_quantized", dev, codes.data_ptr(),
@@ -705,7 +728,7 @@ def spec_kv_read_quantized(codes: torch.Tensor, scales: torch.Tensor, cache_len:
     dt = _kv_other(out, "out", codes)
     _need(cache_len, "cache_len", torch.int32, (B,), dev)
     if status is None:
-        status = torch.empty_like(cache_len)
+        status = _result((B,), torch.int32, dev, stream)
     else:
         _need(status, "status", torch.int32, (B,), dev)
     _call(_native.load().spec_kv_read_quantized, "spec_kv_read_quantized", dev, codes.data_ptr(), scales.data_ptr(),
@@ -741,11 +764,11 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int =
     _fits(N, V, top_n)
     lib = _native.load()
     need = lib.spec_token_logprobs_workspace_bytes(N, V, dt, top_n)
-    lp = torch.empty_like(tokens, dtype=torch.float32)
-    entropy = torch.empty_like(lp)
-    ids = torch.empty(lead + (top_n,), dtype=torch.int32, device=dev)
-    top = torch.empty_like(ids, dtype=torch.float32)
     raw = _raw_stream(dev, stream)
+    lp = _result(lead, torch.float32, dev, stream)
+    entropy = _result(lead, torch.float32, dev, stream)
+    ids = _result(lead + (top_n,), torch.int32, dev, stream)
+    top = _result(lead + (top_n,), torch.float32, dev, stream)
     ws, wsb = None, 0
     if need:
         buf = _scratch(dev, need, raw, workspace, stream)
