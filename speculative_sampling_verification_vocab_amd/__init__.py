@@ -32,6 +32,7 @@ _DTYPES = {torch.bfloat16: _native.SPEC_BF16, torch.float32: _native.SPEC_F32}
 _MODES = {"sample": _native.SPEC_MODE_SAMPLE, "greedy": _native.SPEC_MODE_GREEDY,
           "sample_early_exit": _native.SPEC_MODE_SAMPLE_EARLY_EXIT}
 _SAMPLING = ("sample", "sample_early_exit")
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def abi_version() -> int:
@@ -128,6 +129,41 @@ def _workspace_for(device, stream=None) -> Workspace:
     return ws
 
 
+def _raw_stream(device: torch.device, stream=None) -> int:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}, the device of the call's tensors")
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _capturing(device: torch.device, stream) -> bool:
+    """Whether the call's stream is under graph capture (torch asks about the current device's only)."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_stream_of(device, stream)):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Workspace], stream) -> torch.Tensor:
+    """At least `need` bytes of workspace: the caller's, or the default one of
+    (device, stream).  A call under graph capture gets memory of the graph's own:
+    graphs that shared a default workspace would race when replayed at once, also
+    with eager calls on their stream, and one that grows later would leave them
+    with memory that is no longer theirs."""
+    if workspace is not None:
+        return workspace.get(need, stream, device)
+    if _capturing(device, stream):
+        with torch.cuda.stream(_stream_of(device, stream)):
+            return torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _default_ws.get((device, raw))
+    if ws is not None and ws.buf.numel() >= need:
+        return ws.buf  # allocated on this stream: calls on others have workspaces of their own
+    return _workspace_for(device, stream).get(need, stream, device)
+
+
 def spec_verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_tokens: Optional[torch.Tensor],
                 uniforms: Optional[torch.Tensor], temperature: float = 1.0, mode: str = "sample", *,
                 return_probs: bool = False, workspace: Optional[Workspace] = None, stream=None,
@@ -152,7 +188,7 @@ def spec_verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_token
     pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
     pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES[mode])
-    ws = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
+    ws = _scratch(dev, need, _raw_stream(dev, stream), workspace, stream)
     args = [_ptr(target), _ptr(draft) if sampling else None,
             _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms) if sampling else None,
             B, K, V, dt, ctypes.c_float(temperature if sampling else 0.0), _MODES[mode],
@@ -417,7 +453,7 @@ def spec_verify_sparse_draft(target: torch.Tensor, draft_compact: torch.Tensor, 
     pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
     pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES["sample"])
-    ws = (workspace or _workspace_for(dev, stream)).get(need, stream, dev)
+    ws = _scratch(dev, need, _raw_stream(dev, stream), workspace, stream)
     st = lib.spec_verify_sparse_draft(_ptr(target), _ptr(draft_compact) if K > 0 else None,
                                       _ptr(cluster_ids) if K > 0 else None, ns, L, S, int(cluster_size),
                                       _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms), B, K, V, dt,
@@ -498,7 +534,7 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
     need = lib.spec_draft_head_static_workspace_bytes(M, d, V, int(cluster_size), cluster_ids.numel()) \
         if split and M > 0 and cluster_ids.numel() > 0 else 0
     if need:
-        buf = (workspace or _workspace_for(h.device, stream)).get(need, stream, h.device)
+        buf = _scratch(h.device, need, _raw_stream(h.device, stream), workspace, stream)
         ws, wsb = _ptr(buf), buf.numel()
     st = lib.spec_draft_head_static(_ptr(h.contiguous()), _ptr(W.contiguous()),
                                     _ptr(cluster_ids.contiguous()), M, d, V, int(cluster_size),
@@ -517,47 +553,12 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
 
 _BLOCK = 128
 _CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
-_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         _need_gpu(t, name, device)
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
-
-
-def _raw_stream(device: torch.device, stream=None) -> int:
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream must be on {device}, the device of the call's tensors")
-        return stream.cuda_stream
-    if _raw_current_stream is not None:
-        return _raw_current_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _capturing(device: torch.device, stream) -> bool:
-    """Whether the call's stream is under graph capture (torch asks about the current device's only)."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(_stream_of(device, stream)):
-        return torch.cuda.is_current_stream_capturing()
-
-
-def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Workspace], stream) -> torch.Tensor:
-    """At least `need` bytes of workspace: the caller's, or the default one of
-    (device, stream).  A call under graph capture gets memory of the graph's own:
-    graphs that shared a default workspace would race when replayed at once, and
-    one that grows later would leave them with memory that is no longer theirs."""
-    if workspace is not None:
-        return workspace.get(need, stream, device)
-    if _capturing(device, stream):
-        with torch.cuda.stream(_stream_of(device, stream)):
-            return torch.empty(need, dtype=torch.uint8, device=device)
-    ws = _default_ws.get((device, raw))
-    if ws is not None and ws.buf.numel() >= need:
-        return ws.buf  # allocated on this stream: calls on others have workspaces of their own
-    return _workspace_for(device, stream).get(need, stream, device)
 
 
 def _fits(*sizes):
