@@ -38,7 +38,10 @@
  *   - Argument errors are returned synchronously before anything is enqueued;
  *     outputs are then left untouched.  SPEC_ERR_HIP reports a failed launch.
  *   - Calls with distinct workspaces may run concurrently.  Two calls that
- *     share a workspace must be ordered (same stream or synchronised).
+ *     share a workspace must be ordered: made one after the other on the same
+ *     stream, or synchronised.  Most calls are several launches, so two host
+ *     threads that share a workspace (or a cache that both commit to) on one
+ *     stream make their calls under a lock.
  */
 #ifndef SPECVERIFY_H_
 #define SPECVERIFY_H_

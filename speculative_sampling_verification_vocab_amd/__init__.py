@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -92,8 +93,10 @@ def spec_verify_launch_count(B: int, K: int, V: int, dtype: torch.dtype, mode: s
 class Workspace:
     """A device scratch buffer reused across calls; it grows to the largest size asked for.
 
-    Calls that share one Workspace must be ordered on the GPU (same stream, or
-    synchronised).  The buffer is allocated on the stream of the call that
+    Calls that share one Workspace must be ordered on the GPU: made one after
+    the other on one stream, or synchronised.  A call is several launches and two
+    host threads' may alternate on a stream, so threads share a Workspace only
+    under a lock of their own.  The buffer is allocated on the stream of the call that
     grows it, and every use on another stream is recorded with the caching
     allocator (``record_stream``), so a buffer that is replaced is not handed
     out again while kernels on any stream that used it may still run."""
@@ -119,13 +122,15 @@ class Workspace:
 _default_ws = {}
 
 
-def _workspace_for(device, stream=None) -> Workspace:
-    """The default workspace of (device, stream): calls on different streams never share scratch."""
-    dev = torch.device(device)
-    key = (dev, _stream_of(dev, stream).cuda_stream)
+def _workspace_for(device: torch.device, raw: int) -> Workspace:
+    """The default workspace of (device, stream, host thread): calls on different
+    streams never share scratch, nor do calls of threads whose launches may
+    alternate on one stream.  (A later thread with an ended one's identity goes
+    on with its workspace: the ended one's launches are all on the stream.)"""
+    key = (device, raw, threading.get_ident())
     ws = _default_ws.get(key)
     if ws is None:
-        ws = _default_ws[key] = Workspace(dev)
+        ws = _default_ws[key] = Workspace(device)
     return ws
 
 
@@ -149,7 +154,7 @@ def _capturing(device: torch.device, stream) -> bool:
 
 def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Workspace], stream) -> torch.Tensor:
     """At least `need` bytes of workspace: the caller's, or the default one of
-    (device, stream).  A call under graph capture gets memory of the graph's own:
+    (device, stream, host thread).  A call under graph capture gets memory of the graph's own:
     graphs that shared a default workspace would race when replayed at once, also
     with eager calls on their stream, and one that grows later would leave them
     with memory that is no longer theirs."""
@@ -158,10 +163,10 @@ def _scratch(device: torch.device, need: int, raw: int, workspace: Optional[Work
     if _capturing(device, stream):
         with torch.cuda.stream(_stream_of(device, stream)):
             return torch.empty(need, dtype=torch.uint8, device=device)
-    ws = _default_ws.get((device, raw))
-    if ws is not None and ws.buf.numel() >= need:
+    ws = _workspace_for(device, raw)
+    if ws.buf.numel() >= need:
         return ws.buf  # allocated on this stream: calls on others have workspaces of their own
-    return _workspace_for(device, stream).get(need, stream, device)
+    return ws.get(need, stream, device)
 
 
 def spec_verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_tokens: Optional[torch.Tensor],
