@@ -99,12 +99,15 @@ class Workspace:
     under a lock of their own.  The buffer is allocated on the stream of the call that
     grows it, and every use on another stream is recorded with the caching
     allocator (``record_stream``), so a buffer that is replaced is not handed
-    out again while kernels on any stream that used it may still run."""
+    out again while kernels on any stream that used it may still run.  A buffer
+    that a captured call used stays alive as long as the Workspace, which must
+    outlive the graph: replays go on writing it after a larger one replaced it."""
 
     def __init__(self, device):
         self.device = torch.device(device)
         self.buf = torch.empty(0, dtype=torch.uint8, device=self.device)
         self._stream = None
+        self._captured = []  # buffers that graphs use
 
     def get(self, nbytes: int, stream=None, device=None) -> torch.Tensor:
         if device is not None and torch.device(device) != self.device:
@@ -116,6 +119,8 @@ class Workspace:
             self._stream = s
         elif s != self._stream:
             self.buf.record_stream(s)
+        if nbytes and _capturing(self.device, stream) and not any(b is self.buf for b in self._captured):
+            self._captured.append(self.buf)
         return self.buf
 
 

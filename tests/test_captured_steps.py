@@ -1,6 +1,8 @@
 """Every entry point with a default workspace under graph capture: the memory
 is the graph's own, so that graphs captured on one stream can be replayed at
 once, beside eager calls on that stream."""
+import weakref
+
 import pytest
 import torch
 
@@ -72,3 +74,50 @@ def test_whole_steps_replayed_at_once():
             eager = whole(2)
         torch.cuda.synchronize()
         assert same(outs[0], want[0]) and same(outs[1], want[1]) and same(eager, want[2])
+
+
+def test_a_workspace_keeps_the_buffers_that_graphs_use(monkeypatch):
+    gpus = Gpus(monkeypatch)
+    side = Stream(0)
+    ws = sv().Workspace(torch.device("cuda", 0))
+    first = weakref.ref(ws.get(1000))
+    gpus.made.clear()
+    ws.get(2000)
+    assert first() is None                         # replaced, and no graph uses it
+    with gpus.stream(side):
+        gpus.captured.append(side)
+        for _ in range(3):
+            used = weakref.ref(ws.get(1500))
+        gpus.captured.clear()
+    ws.get(1 << 20)
+    gpus.made.clear()
+    assert used() is not None and ws.buf is not used() and ws.buf.numel() == 1 << 20
+    del ws
+    assert used() is None
+
+
+@pytest.mark.gpu
+def test_a_workspace_that_grows_after_a_capture():
+    """A larger eager call replaces the buffer of a captured one; tensors made since keep their values through replays."""
+    g = torch.Generator().manual_seed(41)
+    x = torch.randn(50, 70000, generator=g).to(BF).to(DEV)
+    big = torch.randn(400, 70000, generator=g).to(BF).to(DEV)
+    t = torch.randint(0, 70000, (400,), generator=g).to(torch.int32).to(DEV)
+    ws = sv().Workspace(DEV)
+    want = sv().spec_token_logprobs(x, t[:50], 9, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sv().spec_token_logprobs(x, t[:50], 9, workspace=ws)
+    size = ws.buf.numel()
+    ref = sv().spec_token_logprobs(big, t, 9, workspace=ws)
+    assert ws.buf.numel() > size
+    others = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    for _ in range(4):
+        for v in out:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, want)
+        assert all((o == 7).all() for o in others)
+        assert same(sv().spec_token_logprobs(big, t, 9, workspace=ws), ref)
