@@ -433,7 +433,7 @@ size_t spec_token_logprobs_workspace_bytes(int32_t N, int32_t V, spec_dtype_t dt
  * One launch.  Any alignment of whole elements works; rows of d % 8 == 0
  * from a 16-byte boundary take aligned vector loads.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, R < 0, d < 1
- * or an unknown dtype; SPEC_ERR_UNSUPPORTED for more than 2^30 - 1 blocks.
+ * or an unknown dtype; SPEC_ERR_UNSUPPORTED for more than 2^30 - 64 blocks.
  */
 spec_status_t spec_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype_t dtype, void* codes,
                                  void* scales, void* stream);

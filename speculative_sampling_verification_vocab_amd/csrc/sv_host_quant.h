@@ -31,6 +31,14 @@ inline bool overlap(const void* p, size_t bytes, const void* q, size_t q_bytes) 
 
 // ---- rows -----------------------------------------------------------------------
 
+// Blocks of the format that a block of threads quantises in a long launch, four
+// per group of 16 lanes; short launches take fewer.
+constexpr int kRowsPerBlock = kBlock / 16 * 4;
+
+// Format blocks that one launch quantises: 2^30 - 64 at most, whose numbers
+// stay in int32 with the grid's round-up.
+inline bool rows_fit(size_t blocks) { return (blocks + kRowsPerBlock - 1) / kRowsPerBlock <= max_blocks(kBlock); }
+
 // spec_quantize_rows; *empty when there is nothing to launch.
 inline spec_status_t validate_quantize_rows(const void* x, int32_t R, int32_t d, spec_dtype_t dtype,
                                             const void* codes, const void* scales, bool* empty) {
@@ -39,10 +47,7 @@ inline spec_status_t validate_quantize_rows(const void* x, int32_t R, int32_t d,
   if (*empty) return SPEC_OK;
   if (!x || !codes || !scales) return SPEC_ERR_INVALID_ARG;
   if ((uintptr_t)x % elem_size(dtype) || (uintptr_t)codes % 16) return SPEC_ERR_INVALID_ARG;
-  const size_t blocks = (size_t)R * (size_t)quant_blocks(d);
-  // Block numbers stay in int32 with the grid's round-up, 16 lanes each in its threads (four per lane in long grids).
-  if (blocks > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;
-  return SPEC_OK;
+  return rows_fit((size_t)R * (size_t)quant_blocks(d)) ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
 }
 
 // ---- drafter head ---------------------------------------------------------------
@@ -126,7 +131,7 @@ inline spec_status_t check_head_quantized(int32_t M, int32_t d, int32_t V, int32
   if (!mul_fits((size_t)V, (size_t)quant_blocks(d) * kQuantBlock, kMaxBytes, &wb)) return SPEC_ERR_UNSUPPORTED;
   const unsigned long long tiles = (((unsigned long long)M + plan->mt - 1) / plan->mt) *
                                    (((unsigned long long)N + plan->nt - 1) / plan->nt) * plan->split;
-  if (tiles + 7 > max_blocks(512) || (size_t)M * (size_t)quant_blocks(d) > 0x7fffffffu / 2) return SPEC_ERR_UNSUPPORTED;
+  if (tiles + 7 > max_blocks(512) || !rows_fit((size_t)M * (size_t)quant_blocks(d))) return SPEC_ERR_UNSUPPORTED;
   if (((size_t)M * (size_t)N + 1023) / 1024 > max_blocks(256)) return SPEC_ERR_UNSUPPORTED;  // the sum of partials
   return SPEC_OK;
 }

@@ -56,9 +56,10 @@ hipError_t launch_rows(const void* x, void* codes, void* scales, uint32_t blocks
   constexpr int kPer = kBlock / kLanesPerBlock;
   const T* p = static_cast<const T*>(x);
   uint8_t *c = static_cast<uint8_t*>(codes), *s = static_cast<uint8_t*>(scales);
-  if (blocks >= (uint32_t)(kPer * 4 * 1024))
-    hipLaunchKernelGGL((quantize_rows_kernel<T, kVec, 4>), dim3((blocks + kPer * 4 - 1) / (kPer * 4)), dim3(kBlock), 0,
-                       st, p, c, s, blocks, nb, d);
+  static_assert(kRowsPerBlock == kPer * 4, "the grid that rows_fit checks");
+  if (blocks >= (uint32_t)(kRowsPerBlock * 1024))
+    hipLaunchKernelGGL((quantize_rows_kernel<T, kVec, 4>), dim3((blocks + kRowsPerBlock - 1) / kRowsPerBlock),
+                       dim3(kBlock), 0, st, p, c, s, blocks, nb, d);
   else
     hipLaunchKernelGGL((quantize_rows_kernel<T, kVec, 1>), dim3((blocks + kPer - 1) / kPer), dim3(kBlock), 0, st, p, c,
                        s, blocks, nb, d);
