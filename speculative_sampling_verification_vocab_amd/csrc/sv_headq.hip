@@ -38,6 +38,7 @@
 // (a library's bf16 product of 8192^3: 1.40).
 
 #include "sv_common.h"
+#include "sv_dma.h"
 #include "sv_host_quant.h"
 #include "sv_internal.h"
 #include "sv_quant.h"
@@ -69,24 +70,6 @@ struct HeadQArgs {
   int out_bf16;
   float* partial;         // split > 1: fp32 [split][M][N]
 };
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// A barrier that leaves DMAs in flight.  The wave's own LDS reads are done
-// before it, wherever the compiler puts the products that use them: the buffer
-// they come from is refilled behind it.
-__device__ __forceinline__ void block_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// One 16-byte global_load_lds per lane: lane l's bytes land at lds + 16 * l.
-__device__ __forceinline__ void dma16(const uint8_t* g, uint8_t* lds) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_global_load_lds(g, lds, 16, 0, 0);
-#endif
-}
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});

@@ -29,6 +29,7 @@
 // contributes zero columns.
 
 #include "sv_common.h"
+#include "sv_dma.h"
 #include "sv_internal.h"
 
 namespace sv {
@@ -311,34 +312,6 @@ __global__ void __launch_bounds__(kWave * WM * WN * WK) head_static_kernel(Stati
   store_tile<TM, TN>(a, acc, m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane, false);
 }
 
-// LDS-DMA form, for d % 64 == 0 and 16-byte aligned rows: global_load_lds
-// moves each stage straight from memory into LDS (no register staging, no
-// ds_write), NBUF stages deep.  One DMA instruction writes 1 KiB: 8 rows of
-// 64 dims.  Within a 128-byte row the 16-byte chunk c sits in slot
-// c ^ ((row >> 1) & 7): the 16 rows that one fragment read touches then fall
-// on distinct banks, and a DMA lane picks its source chunk to match its slot.
-// Rows past M, past N or of out-of-range clusters load h's first row: their
-// outputs are not stored, or (out-of-range clusters) stored as zeros.
-// The compiler does not track LDS-DMA completion, so the waits are explicit:
-// before a stage is read, every wave waits until at most the later stages'
-// DMAs are in flight, then the block meets at a barrier.
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
-
-// One 16-byte global_load_lds per lane: lane l's bytes land at lds + 16 * l
-// (lds is the wave's uniform base).  The default cache policy: the
-// nontemporal one measured 10-35 % slower in this kernel.
-__device__ __forceinline__ void dma16(const uint16_t* g, uint8_t* lds) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_global_load_lds(g, lds, 16, 0, 0);
-#endif
-}
-
 // Block epilogue through LDS: the waves that hold final sums (own) write
 // their chunks into a row-major kMt x kNt fp32 tile in LDS (stage, room for
 // kMt * (kNt + 4) floats), then the whole block stores it row by row, 16
@@ -398,6 +371,17 @@ __device__ __forceinline__ void store_block_tile(const StaticArgs& a, const f32x
   }
 }
 
+// LDS-DMA form, for d % 64 == 0 and 16-byte aligned rows: global_load_lds
+// moves each stage straight from memory into LDS (no register staging, no
+// ds_write), NBUF stages deep.  One DMA instruction writes 1 KiB: 8 rows of
+// 64 dims.  Within a 128-byte row the 16-byte chunk c sits in slot
+// c ^ ((row >> 1) & 7): the 16 rows that one fragment read touches then fall
+// on distinct banks, and a DMA lane picks its source chunk to match its slot.
+// Rows past M, past N or of out-of-range clusters load h's first row: their
+// outputs are not stored, or (out-of-range clusters) stored as zeros.
+// The compiler does not track LDS-DMA completion, so the waits are explicit:
+// before a stage is read, every wave waits until at most the later stages'
+// DMAs are in flight, then the block meets at a barrier.
 template <int WM, int WN, int WK, int TM, int TN, int NBUF>
 __global__ void __launch_bounds__(kWave * WM * WN * WK) head_static_dma_kernel(StaticArgs a) {
   constexpr int NW = WM * WN * WK;
