@@ -386,8 +386,8 @@ spec_status_t spec_kv_commit(void* cache, const void* staging, const int32_t* ac
  *   temperature    finite, at least the smallest normal float: the law is
  *                  softmax(logits / T).
  *   top_n          alternatives per row, 0 .. SPEC_MAX_TOP.
- *   logprobs       [N] float out: ln P(token); -inf where its logit is -inf.
- *   entropy        NULL or [N] float out: -sum P ln P, in nats.
+ *   logprobs       [N] float out: ln P(token), at most 0; -inf where its logit is -inf.
+ *   entropy        NULL or [N] float out: -sum P ln P, in nats, at least 0.
  *   top_ids        [N, top_n] int32 out: the tokens with the largest logits in
  *                  descending order, equal logits by lower id first.  Tokens
  *                  at -inf are no alternatives: entries past the others are -1.

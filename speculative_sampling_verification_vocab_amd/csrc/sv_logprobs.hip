@@ -178,12 +178,15 @@ __device__ __forceinline__ double wave_max64(double v) {
 constexpr double kLn2 = 0.69314718055994530942;
 
 // A row's law: ln P(x) = ln 2 ((x s - ref) - log2 Z), in that order, for ref may
-// dwarf log2 Z.
+// dwarf log2 Z.  Where one token has all of the probability, the roundings of
+// its own term in Z are left (6e-8): they carry no result past its bound, a
+// logarithm of a probability past 0 or an entropy below it.
 struct RowLaw {
   double ref, log2Z, s;
 };
 __device__ __forceinline__ float log_prob(const RowLaw& w, float x) {
-  return (float)(kLn2 * ((double)x * w.s - w.ref - w.log2Z));
+  const double v = kLn2 * ((double)x * w.s - w.ref - w.log2Z);
+  return v > 0.0 ? 0.0f : (float)v;
 }
 
 // A row without a law: NaN, and no alternatives.
@@ -587,7 +590,8 @@ __device__ __forceinline__ bool write_law(const LpArgs& a, size_t row_i, float x
   *law = RowLaw{R, log2(Z), (double)a.s};
   if (lane == 0) {
     a.logprobs[row_i] = log_prob(*law, xt);
-    if (a.entropy) a.entropy[row_i] = (float)(kLn2 * (law->log2Z - H / Z));
+    const double entropy = kLn2 * (law->log2Z - H / Z);
+    if (a.entropy) a.entropy[row_i] = entropy < 0.0 ? 0.0f : (float)entropy;
   }
   return true;
 }
