@@ -57,8 +57,25 @@ def _stream_of(device: torch.device, stream=None):
     return stream if stream is not None else torch.cuda.current_stream(device)
 
 
-def _stream_handle(device: torch.device, stream=None):
-    return ctypes.c_void_p(_stream_of(device, stream).cuda_stream)
+def _raw_stream(device: torch.device, stream=None) -> int:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}, the device of the call's tensors")
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(fn, what: str, device: torch.device, *args):
+    """One C call with `device` current, as a launch on one of its streams needs."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _native.check(st, what)
 
 
 def _result(shape, dtype: torch.dtype, device: torch.device, stream=None) -> torch.Tensor:
@@ -139,16 +156,6 @@ def _workspace_for(device: torch.device, raw: int) -> Workspace:
     return ws
 
 
-def _raw_stream(device: torch.device, stream=None) -> int:
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream must be on {device}, the device of the call's tensors")
-        return stream.cuda_stream
-    if _raw_current_stream is not None:
-        return _raw_current_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _capturing(device: torch.device, stream) -> bool:
     """Whether the call's stream is under graph capture (torch asks about the current device's only)."""
     if stream is None and torch.cuda.current_device() == device.index:
@@ -198,18 +205,18 @@ def spec_verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_token
     pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
     pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES[mode])
-    ws = _scratch(dev, need, _raw_stream(dev, stream), workspace, stream)
+    raw = _raw_stream(dev, stream)
+    ws = _scratch(dev, need, raw, workspace, stream)
     args = [_ptr(target), _ptr(draft) if sampling else None,
             _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms) if sampling else None,
             B, K, V, dt, ctypes.c_float(temperature if sampling else 0.0), _MODES[mode],
-            _ptr(acc), _ptr(out), _ptr(pt), _ptr(pd), _ptr(ws), ws.numel(), _stream_handle(dev, stream)]
+            _ptr(acc), _ptr(out), _ptr(pt), _ptr(pd), _ptr(ws), ws.numel(), raw]
     if events is not None:
         evs = list(events)
         arr = (ctypes.c_void_p * max(1, len(evs)))(*[e.cuda_event if e is not None else None for e in evs])
-        st = lib.spec_verify_timed(*args, arr, len(evs))
+        _call(lib.spec_verify_timed, "spec_verify", dev, *args, arr, len(evs))
     else:
-        st = lib.spec_verify(*args)
-    _native.check(st, "spec_verify")
+        _call(lib.spec_verify, "spec_verify", dev, *args)
     if return_probs:
         return acc, out, pt, pd
     return acc, out
@@ -247,10 +254,10 @@ class VerifyPlan:
         self.p_target = _result((B, K), torch.float32, dev, stream) if return_probs else None
         self.p_draft = _result((B, K), torch.float32, dev, stream) if return_probs else None
         s = _stream_of(dev, stream)
+        self._stream = _raw_stream(dev, stream)
         need = lib.spec_verify_workspace_bytes(B, K, V, self._dt, self._m)
         with torch.cuda.stream(s):
             self._ws = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
-        self._stream = s.cuda_stream
         self._tail = [self.accepted_len.data_ptr(), self.out_tokens.data_ptr(),
                       self.p_target.data_ptr() if return_probs else None,
                       self.p_draft.data_ptr() if return_probs else None,
@@ -276,13 +283,11 @@ class VerifyPlan:
         args = [tp, dp, kp, up, self.B, self.K, self.V, self._dt,
                 ctypes.c_float(temperature if self._sampling else 0.0), self._m, *self._tail]
         if events is None:
-            st = self._lib.spec_verify(*args)
+            _call(self._lib.spec_verify, "spec_verify", self.device, *args)
         else:
             evs = list(events)
             arr = (ctypes.c_void_p * max(1, len(evs)))(*[e.cuda_event if e is not None else None for e in evs])
-            st = self._lib.spec_verify_timed(*args, arr, len(evs))
-        if st:
-            _native.check(st, "spec_verify")
+            _call(self._lib.spec_verify_timed, "spec_verify", self.device, *args, arr, len(evs))
         return self._out
 
 
@@ -337,11 +342,10 @@ def spec_verify_noalloc(target: torch.Tensor, draft: Optional[torch.Tensor], dra
         if tuple(t.shape) != shape or t.dtype != dtype:
             raise ValueError(f"out tensor must be {dtype} {list(shape)}")
     pt, pd = (out[2], out[3]) if len(out) == 4 else (None, None)
-    st = _native.load().spec_verify_noalloc(
-        _ptr(target), _ptr(draft) if sampling else None, _ptr(draft_tokens) if K > 0 else None,
-        _ptr(uniforms) if sampling else None, B, K, V, dt, ctypes.c_float(temperature if sampling else 0.0),
-        _MODES[mode], _ptr(out[0]), _ptr(out[1]), _ptr(pt), _ptr(pd), _stream_handle(target.device, stream))
-    _native.check(st, "spec_verify_noalloc")
+    _call(_native.load().spec_verify_noalloc, "spec_verify_noalloc", target.device, _ptr(target),
+          _ptr(draft) if sampling else None, _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms) if sampling else None,
+          B, K, V, dt, ctypes.c_float(temperature if sampling else 0.0), _MODES[mode], _ptr(out[0]), _ptr(out[1]),
+          _ptr(pt), _ptr(pd), _raw_stream(target.device, stream))
     return tuple(out)
 
 
@@ -366,10 +370,9 @@ def spec_draft_head_shortlist(h: torch.Tensor, W: torch.Tensor, cluster_ids: tor
     comp = _result((B, K, n_sel * cluster_size), torch.float32, dev, stream) if compact else None
     dn = _result((B, K, V), dense_dtype, dev, stream) if dense else None
     lib = _native.load()
-    st = lib.spec_draft_head_shortlist(_ptr(h), _ptr(W), _ptr(cluster_ids), B, K, d, V, cluster_size, n_sel,
-                                       _ptr(comp), _ptr(dn), _DTYPES[dense_dtype] if dense else 0, None, 0,
-                                       _stream_handle(dev, stream))
-    _native.check(st, "spec_draft_head_shortlist")
+    _call(lib.spec_draft_head_shortlist, "spec_draft_head_shortlist", dev, _ptr(h), _ptr(W), _ptr(cluster_ids), B, K,
+          d, V, cluster_size, n_sel, _ptr(comp), _ptr(dn), _DTYPES[dense_dtype] if dense else 0, None, 0,
+          _raw_stream(dev, stream))
     return comp, dn
 
 
@@ -405,9 +408,8 @@ def spec_kv_commit(cache: torch.Tensor, staging: torch.Tensor, accepted_len: tor
         _need_gpu(status, "status", cache.device)
         if status.dtype != torch.int32 or tuple(status.shape) != (B,):
             raise ValueError("status must be contiguous int32 [B]")
-    st = _native.load().spec_kv_commit(_ptr(cache), _ptr(staging), _ptr(accepted_len), _ptr(cache_len),
-                                       _ptr(status), P, B, K, Lmax, E, dt, _stream_handle(cache.device, stream))
-    _native.check(st, "spec_kv_commit")
+    _call(_native.load().spec_kv_commit, "spec_kv_commit", cache.device, _ptr(cache), _ptr(staging),
+          _ptr(accepted_len), _ptr(cache_len), _ptr(status), P, B, K, Lmax, E, dt, _raw_stream(cache.device, stream))
     return status
 
 
@@ -463,13 +465,12 @@ def spec_verify_sparse_draft(target: torch.Tensor, draft_compact: torch.Tensor, 
     pt = _result((B, K), torch.float32, dev, stream) if return_probs else None
     pd = _result((B, K), torch.float32, dev, stream) if return_probs else None
     need = lib.spec_verify_workspace_bytes(B, K, V, dt, _MODES["sample"])
-    ws = _scratch(dev, need, _raw_stream(dev, stream), workspace, stream)
-    st = lib.spec_verify_sparse_draft(_ptr(target), _ptr(draft_compact) if K > 0 else None,
-                                      _ptr(cluster_ids) if K > 0 else None, ns, L, S, int(cluster_size),
-                                      _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms), B, K, V, dt,
-                                      ctypes.c_float(temperature), _ptr(acc), _ptr(out), _ptr(pt), _ptr(pd),
-                                      _ptr(ws), ws.numel(), _stream_handle(dev, stream))
-    _native.check(st, "spec_verify_sparse_draft")
+    raw = _raw_stream(dev, stream)
+    ws = _scratch(dev, need, raw, workspace, stream)
+    _call(lib.spec_verify_sparse_draft, "spec_verify_sparse_draft", dev, _ptr(target),
+          _ptr(draft_compact) if K > 0 else None, _ptr(cluster_ids) if K > 0 else None, ns, L, S, int(cluster_size),
+          _ptr(draft_tokens) if K > 0 else None, _ptr(uniforms), B, K, V, dt, ctypes.c_float(temperature),
+          _ptr(acc), _ptr(out), _ptr(pt), _ptr(pd), _ptr(ws), ws.numel(), raw)
     return (acc, out, pt, pd) if return_probs else (acc, out)
 
 
@@ -503,11 +504,8 @@ def spec_draft_head_positions(h: torch.Tensor, W: torch.Tensor, cluster_ids: tor
             or out.device != h.device:
         raise ValueError("out must be on h's device, a contiguous [B, K, L] tensor of dtype")
     ns = (ctypes.c_int32 * max(1, K))(*[int(x) for x in n_sel])
-    st = _native.load().spec_draft_head_positions(_ptr(h.contiguous()), _ptr(W.contiguous()),
-                                                  _ptr(cluster_ids.contiguous()), ns, B, K, d, V,
-                                                  int(cluster_size), S, L, _ptr(out), dt,
-                                                  _stream_handle(h.device, stream))
-    _native.check(st, "spec_draft_head_positions")
+    _call(_native.load().spec_draft_head_positions, "spec_draft_head_positions", h.device, _ptr(h), _ptr(W),
+          _ptr(cluster_ids), ns, B, K, d, V, int(cluster_size), S, L, _ptr(out), dt, _raw_stream(h.device, stream))
     return out
 
 
@@ -540,17 +538,15 @@ def spec_draft_head_static(h: torch.Tensor, W: torch.Tensor, cluster_ids: torch.
             or out.device != h.device:
         raise ValueError("out must be on h's device, contiguous with shape h.shape[:-1] + (N,) and dtype")
     lib = _native.load()
+    raw = _raw_stream(h.device, stream)
     ws, wsb = None, 0
     need = lib.spec_draft_head_static_workspace_bytes(M, d, V, int(cluster_size), cluster_ids.numel()) \
         if split and M > 0 and cluster_ids.numel() > 0 else 0
     if need:
-        buf = _scratch(h.device, need, _raw_stream(h.device, stream), workspace, stream)
+        buf = _scratch(h.device, need, raw, workspace, stream)
         ws, wsb = _ptr(buf), buf.numel()
-    st = lib.spec_draft_head_static(_ptr(h.contiguous()), _ptr(W.contiguous()),
-                                    _ptr(cluster_ids.contiguous()), M, d, V, int(cluster_size),
-                                    cluster_ids.numel(), _ptr(out), dt, ws, wsb,
-                                    _stream_handle(h.device, stream))
-    _native.check(st, "spec_draft_head_static")
+    _call(lib.spec_draft_head_static, "spec_draft_head_static", h.device, _ptr(h), _ptr(W), _ptr(cluster_ids), M, d,
+          V, int(cluster_size), cluster_ids.numel(), _ptr(out), dt, ws, wsb, raw)
     return out
 
 
@@ -575,17 +571,6 @@ def _fits(*sizes):
     """The C ABI's sizes are 32-bit; ctypes would cut a larger one off without a word."""
     if max(sizes) > 0x7fffffff:
         raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
-
-
-def _call(fn, what: str, device: torch.device, *args):
-    """One C call with `device` current, as a launch on one of its streams needs."""
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args)
-    if st:
-        _native.check(st, what)
 
 
 def spec_quantize_rows(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None, stream=None):

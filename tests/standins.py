@@ -17,7 +17,7 @@ F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
 class Stream:
-    handles = itertools.count(0x1000, 0x10)
+    handles = itertools.count(0x70000001, 0x10)
 
     def __init__(self, device, handle=None):
         self.device = torch.device("cuda", device)
