@@ -10,11 +10,15 @@
 // 32-code groups share the scale: lane group g gives the 16-byte pieces g and
 // g + 4 of the row.
 //
-// That instruction adds each group of 8 products with their low bits cut off
-// some 16 binary places below the group's largest: 1.4e-5 of the result (rms,
-// normal data, measured; the groups' sums and the accumulator lose nothing
-// like it).  Rounding to bf16 hides that 100 times over, so bf16 outputs take
-// it.  fp32 outputs take v_mfma_f32_16x16x32_bf16 on the codes' values, which
+// That instruction adds each group of 8 consecutive dims' products with what
+// lies below 2^-13 of the largest one's power of two cut off, toward zero
+// (measured; a product has 8 significant bits, so the largest one and those
+// down to 2^-5 of it stay whole, and the groups' sums and the accumulator lose
+// fp32 roundings only).  A group is off by at most 7 * 2^-13 of its largest
+// product: 1.4e-5 of the result for normal data (rms), a hundredth of the
+// rounding to bf16, and less than that rounding for any data whose large
+// products do not cancel each other.  bf16 outputs take it, for half the matrix
+// time.  fp32 outputs take v_mfma_f32_16x16x32_bf16 on the codes' values, which
 // bf16 holds exactly (6e-9): one conversion per two codes, which applies the
 // scale, and twice the matrix time.
 //
