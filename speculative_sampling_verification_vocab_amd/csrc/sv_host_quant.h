@@ -62,9 +62,22 @@ struct HeadQPlan {
 };
 
 constexpr int kHeadQCUs = 256;     // compute units that a grid should reach
+// Slices of d where there are fewer tiles than that: at most 8, of at least four
+// blocks of 128.  d = 4096, us in 1, 2, 4, 8, 16 slices: M = 128, N = 8016 (plan:
+// 4): 29.2, 24.3, 23.1, 31.2, 49.2; M = 64, N = 2000 (8): 21.5, 17.4, 15.1, 15.7,
+// 19.9; M = 5, N = 500 (8): 8.4, 8.5, 8.1, 8.8, 11.2.  Few rows gain nothing and
+// lose up to 1.2 (M = 16, d = 1024, N = 1000, 2 slices: 7.5 against 6.3 in one).
 constexpr int kHeadQMaxSplit = 8;
-constexpr int kHeadQOwn = 24 << 10;  // bytes of h's codes that a block quantises for itself (two blocks per CU still fit)
-constexpr int kHeadQSquares = 200;   // tiles of 256 x 256 from which more than 128 rows are cut so
+// Bytes of h's codes that a block quantises for itself: 192 blocks of 128, six
+// for each 16 lanes, whose values wait in registers (48 a thread) while the
+// tile's rows are looked up.
+constexpr int kHeadQOwn = 24 << 10;
+// Tiles of 256 x 256 from which more than 128 rows are cut so, us against tiles
+// of 128 x 128 at d = 4096: 64 tiles (M = 1000, N = 4000) 43.7 and 33.2; 126 (M =
+// 300, N = 16000) 50.8 and 55.0; 188 (M = 300, N = 24000) 65.2 and 78.3; 256 (M =
+// 300, N = 32768) 67.9 and 82.4, 512 rows computed for 300 or not; 2004 (M = 1000,
+// N = 128256) 525 and 826.  The larger are ahead from about 100 tiles on.
+constexpr int kHeadQSquares = 200;
 
 inline HeadQPlan head_quantized_plan(int32_t M, int32_t d, int32_t N) {
   HeadQPlan p{};
@@ -76,7 +89,11 @@ inline HeadQPlan head_quantized_plan(int32_t M, int32_t d, int32_t N) {
   // the bytes that its compute unit can have on their way, about 90 requests of
   // 128 bytes (34 bytes a nanosecond), and every tile reads its rows of h beside
   // its rows of W.  M = 128, d = 4096: N = 128256 takes 123 us in tiles of 128 x
-  // 256 and 142 in 128 x 128; N = 32768, 128 and 256 of them, 44 and 34 us.
+  // 256 and 142 in 128 x 128; N = 32768, 128 and 256 of them, 42 and 34 us.  Up to
+  // 64 rows, us at N = 8016, 32768, 128256: M = 16 in 16 x 32 tiles 11.4, 28.4, 100,
+  // in 32 x 64 14.4, 26.6, 104; M = 32 in 32 x 64 14.9, 26.4, 106, in 16 x 32 12.5,
+  // 41.3, 148, in 64 x 128 16.3, 27.0, 109; M = 64 in 64 x 128 17.7, 28.2, 118, in
+  // 32 x 64 16.5, 44.2, 144, in 128 x 128 19.5, 31.3, 124.
   if (M <= 16) p.tile = 0, p.mt = 16, p.nt = 32;
   else if (M <= 32) p.tile = 1, p.mt = 32, p.nt = 64;
   else if (M <= 64) p.tile = 2, p.mt = 64, p.nt = 128;
@@ -88,8 +105,9 @@ inline HeadQPlan head_quantized_plan(int32_t M, int32_t d, int32_t N) {
   if (s > nb / 4) s = nb / 4;  // at least four blocks of 128 per slice
   p.split = s < 1 ? 1 : (int)s;
   const long long slice = (nb + p.split - 1) / p.split;
-  // One launch less, where every CU has at most its first two blocks (M = 5, N =
-  // 8016: 11.4 us either way on the GPU, 9.9 and 12.8 us on the host); more
+  // One launch less, where every CU has at most its first two blocks (N = 8016,
+  // M = 1: 10.5 against 11.2 us on the GPU, M = 5: 11.8 against 11.4, and 9.9
+  // against 12.8 us on the host); more
   // rounds of blocks would each quantise h again (M = 1, N = 32768: 28.4 and 27.3 us).
   p.own_h = p.tile == 0 && tiles(p.mt, p.nt) * p.split <= 2 * kHeadQCUs && (size_t)M * (size_t)(slice + 1) * kQuantBlock <= (size_t)kHeadQOwn;
   return p;

@@ -51,8 +51,9 @@ hipError_t launch_kv_commit(void* cache, const void* staging, const int32_t* acc
 // Rows into the 8-bit block format (one launch).
 hipError_t launch_quantize_rows(const void* x, int R, int d, int dtype, void* codes, void* scales, hipStream_t st);
 
-// Head on a quantised weight: h's rows quantised into the workspace, the
-// product, and with plan.split > 1 the sum of the slices.
+// Head on a quantised weight: h's rows quantised into the workspace (with
+// plan.own_h by the product's blocks, with no launch), the product, and with
+// plan.split > 1 the sum of the slices.
 hipError_t launch_head_quantized(const void* h, const void* W_codes, const void* W_scales, const int32_t* cluster_ids,
                                  int M, int d, int V, int cluster_size, int n_sel, void* out, int out_dtype,
                                  const HeadQPlan& plan, const HeadQWorkspace& w, void* workspace, hipStream_t st);
@@ -66,7 +67,8 @@ hipError_t launch_kv_read_quantized(const void* codes, const void* scales, const
                                     int32_t* status, int P, int B, int Lmax, int Lout, int E, int dtype,
                                     const KvQPlan& plan, hipStream_t st);
 
-// Token log-probabilities: tiles, then pick (two launches).
+// Token log-probabilities: one launch for rows of up to kLpRowTiles tiles
+// (s.NP == 0), else parts of rows, then their join and the alternatives.
 hipError_t launch_logprobs(const LogprobsShape& s, const LogprobsWorkspace& w, const void* logits,
                            const int32_t* tokens, int dtype, float temperature, float* logprobs, float* entropy,
                            int32_t* top_ids, float* top_logprobs, void* workspace, hipStream_t st);
