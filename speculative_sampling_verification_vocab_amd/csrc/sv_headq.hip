@@ -35,9 +35,9 @@
 // Measured at d = 4096, bf16 out (GPU time; see head_quantized_plan for the
 // tiles): N = 32768: M = 1, 16, 64, 128: 27, 28, 29, 34 us (134 MB of W: 19 us
 // at the read stream's rate); N = 128256: M = 8, 128: 100, 123 us; M = 1792:
-// 872-925 us by the card, 2.0-2.2 PFLOP/s, where a library's product of 8192^3
+// 880-930 us by the card, 2.0-2.1 PFLOP/s, where a library's product of 8192^3
 // reaches 3.1 (the 256 x 256 tile's stages meet at one barrier with two
-// buffers, and LDS reads take three quarters of the products' time).
+// buffers; the matrix cores are busy in 45 % of the cycles, the LDS in 25 %).
 // fp32 out: M = 128, N = 32768: 49 us; M = 1792, N = 32768: 414 us, 1.16 PFLOP/s
 // (a library's bf16 product of 8192^3: 1.40).
 
