@@ -60,9 +60,9 @@ CSRC = os.path.join(ROOT, "speculative_sampling_verification_vocab_amd", "csrc")
 KERNEL_SOURCES = [os.path.join(CSRC, f) for f in ("sv_verify.hip", "sv_common.h")]
 HEAD_SOURCES = [os.path.join(CSRC, f) for f in ("sv_head.hip", "sv_common.h")]
 STATIC_PROFILE_PMC = os.path.join(ROOT, "profiles", "head_static_kernel_frspec_m128_n32768_d4096_pmc.md")
-STATIC_SOURCES = [os.path.join(CSRC, f) for f in ("sv_static.hip", "sv_common.h")]
+STATIC_SOURCES = [os.path.join(CSRC, f) for f in ("sv_static.hip", "sv_dma.h", "sv_common.h")]
 MFMA_PROFILE_PMC = os.path.join(ROOT, "profiles", "head_kernels_mfma_busy_pmc.md")
-MFMA_SOURCES = [os.path.join(CSRC, f) for f in ("sv_head.hip", "sv_static.hip", "sv_common.h")]
+MFMA_SOURCES = [os.path.join(CSRC, f) for f in ("sv_head.hip", "sv_static.hip", "sv_dma.h", "sv_common.h")]
 
 
 def log(*a):
