@@ -381,7 +381,7 @@ inline spec_status_t validate_kv_commit(const void* cache, const void* staging, 
   const size_t planes = (size_t)P * (size_t)B;
   const size_t rows = planes * (size_t)(L_max > K ? L_max : K);
   if (planes / (size_t)B != (size_t)P || (row != 0 && rows > SIZE_MAX / 2 / row)) return SPEC_ERR_INVALID_ARG;
-  const bool copies = P > 0 && K > 0 && E > 0;
+  const bool copies = P > 0 && K > 0 && L_max > 0 && E > 0;  // a cache of no rows: lengths and status only
   if (copies && (!cache || !staging)) return SPEC_ERR_INVALID_ARG;
   if (copies && ((uintptr_t)cache % esz != 0 || (uintptr_t)staging % esz != 0)) return SPEC_ERR_INVALID_ARG;
   const bool vec = row % 16 == 0 && ((uintptr_t)cache % 16 == 0) && ((uintptr_t)staging % 16 == 0);

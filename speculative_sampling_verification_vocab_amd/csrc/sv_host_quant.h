@@ -233,7 +233,8 @@ inline spec_status_t validate_kv_commit_quantized(const void* codes, const void*
   if (status && (overlap(status, lens, accepted_len, lens) || overlap(status, lens, cache_len, lens) ||
                  overlap(status, lens, new_len, lens)))
     return SPEC_ERR_INVALID_ARG;
-  const spec_status_t sc = check_kv_quantized(P, B, K, K, L_max, E, dtype, false, plan);
+  // No more rows than the cache has are committed (none, and no buffers, with L_max == 0).
+  const spec_status_t sc = check_kv_quantized(P, B, K < L_max ? K : L_max, K, L_max, E, dtype, false, plan);
   if (sc != SPEC_OK || !plan->copies) return sc;
   if (!codes || !scales || !staging || (uintptr_t)staging % elem_size(dtype)) return SPEC_ERR_INVALID_ARG;
   plan->vec = E % 8 == 0 && (uintptr_t)staging % 16 == 0 && (uintptr_t)codes % 8 == 0;
