@@ -28,6 +28,9 @@
  *   - The same head and commit in an 8-bit block format (rows quantised, the
  *     head on quantised weights, the cache quantised as it is written and
  *     read back), and the log-probabilities of the emitted tokens.
+ *   - A step with a tree of drafts: attention of its nodes over the cache (of
+ *     values or 8-bit) and their ancestors, tokens drawn at the nodes with
+ *     request settings, and the commit of the path that the drawn tokens take.
  *
  * Conventions shared by every entry point:
  *   - All array arguments are device pointers (hipMalloc / torch CUDA tensors),
@@ -56,6 +59,7 @@ extern "C" {
 #define SPEC_ABI_VERSION 2
 #define SPEC_MAX_K 64
 #define SPEC_MAX_TOP 32      /* alternatives per row of spec_token_logprobs */
+#define SPEC_MAX_NODES 64    /* nodes of a draft tree */
 #define SPEC_QUANT_BLOCK 128 /* values that share a scale in the 8-bit format */
 
 /*
@@ -530,6 +534,158 @@ spec_status_t spec_kv_commit_quantized(void* codes, void* scales, const void* st
 spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, const int32_t* cache_len, void* out,
                                      int32_t* status, int32_t P, int32_t B, int32_t L_max, int32_t L_out,
                                      int32_t E, spec_dtype_t dtype, void* stream);
+
+/*
+ * Trees of drafts, as the next three operators take them: a tree has N nodes,
+ * 1 .. SPEC_MAX_NODES, each with the index of its parent, which comes before
+ * it, or -1.  A node whose parent is outside [-1, i), or that has such an
+ * ancestor, is absent (pad ragged trees with -2).  A chain of drafts is the
+ * tree with parents -1, 0, 1, ...; a single token the tree of one node.
+ *
+ * spec_tree_attention: attention of a tree's nodes over the cached tokens and
+ * the tree's own entries, for one layer.
+ *
+ *   q            [B, N, Hq, D] of dtype: the nodes' queries.
+ *   k_cache, v_cache  [B, L_max, Hkv, D] of dtype: two planes of the cache that
+ *                spec_tree_commit and spec_kv_commit write (E = Hkv * D).
+ *                Entries from cache_len[b] on are not used, whatever they hold.
+ *   k_new, v_new [B, N, Hkv, D] of dtype: the nodes' own entries (planes of
+ *                the commit's staging).
+ *   parents      [B, N] int32.
+ *   cache_len    [B] int32: the sequences' cached entries.
+ *   scale        finite, > 0 (usually D^-0.5).
+ *   window       0: none.  W > 0: a node sees positions above its own - W only,
+ *                and the first `sinks`.  Node i's position is cache_len[b] + its
+ *                number of ancestors; cache entry j's is j.
+ *   sinks        >= 0; unused without a window.
+ *   out          [B, N, Hq, D] of dtype out: for query head h, which reads KV head
+ *                h / (Hq / Hkv), sum_j softmax_j(scale * q.k_j) v_j over the cache
+ *                entries j and the node's ancestors and itself, as far as the
+ *                window lets it see them.  Zeros for an absent node, and for
+ *                one whose scores are all -inf; NaN for a sequence whose
+ *                cache_len is outside [0, L_max].  What a node does not see has
+ *                no effect on it, infinities and NaN included.
+ *   workspace    spec_tree_attention_workspace_bytes(), 256-byte aligned (may be
+ *                NULL where that is 0): partial results where few rows share
+ *                long caches.  The contents need no initialisation.
+ * D is a multiple of 8 up to 256, Hq a multiple of Hkv.  Scores, the softmax's
+ * sums and the output are accumulated in fp32; with bf16 the weights are
+ * rounded to bf16 for their product with the values.  Results are the same on
+ * every call.  One launch, two where the workspace is used.  Any alignment of
+ * whole elements works.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, negative sizes,
+ * a scale, window or sinks out of range, an unknown dtype; SPEC_ERR_UNSUPPORTED
+ * for N > SPEC_MAX_NODES, a D or Hq other than said, L_max > 2^30, Hkv * D or Hq
+ * > 2^22, or sizes too large for one launch; SPEC_ERR_WORKSPACE.
+ */
+spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_new,
+                                  const void* v_new, const int32_t* parents, const int32_t* cache_len, int32_t B,
+                                  int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max, float scale,
+                                  int32_t window, int32_t sinks, spec_dtype_t dtype, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * spec_tree_attention over a cache in the 8-bit block format: k_codes, v_codes
+ * [B, L_max, Hkv, D] bytes and k_scales, v_scales [B, L_max, ceil(Hkv * D / 128)]
+ * bytes are planes of the cache that spec_tree_commit_quantized and
+ * spec_kv_commit_quantized write.  q, k_new, v_new and out are of dtype; the
+ * nodes' own entries are not quantised.  A code stands for its value exactly
+ * (in bf16 where that is a normal number).
+ */
+spec_status_t spec_tree_attention_quantized(const void* q, const void* k_codes, const void* k_scales,
+                                            const void* v_codes, const void* v_scales, const void* k_new,
+                                            const void* v_new, const int32_t* parents, const int32_t* cache_len,
+                                            int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
+                                            float scale, int32_t window, int32_t sinks, spec_dtype_t dtype, void* out,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of both (0: none is needed, or the shape is empty or invalid). */
+size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
+                                           spec_dtype_t dtype);
+
+/*
+ * Tokens drawn from rows of logits with request settings, from given uniforms.
+ *
+ *   logits       [R, V] of dtype: finite or -inf.
+ *   uniforms     [R] float in [0, 1).
+ *   temperature, top_k, top_p, min_p
+ *                [R] each (float, int32, float, float; device), or NULL: the
+ *                value `all_...` for every row.
+ *                temperature >= 0, finite: weights are w_v = exp((x_v - max) / T);
+ *                  0 takes the token of the largest logit, the lowest id of
+ *                  equal ones.
+ *                top_k: tokens are ranked by logit, equal ones by lower id; the
+ *                  first top_k are kept (all of them if it is < 1 or >= V).
+ *                top_p: of those, the first whose weights reach top_p of the
+ *                  weight of the top_k (all of them if it is >= 1, one if <= 0).
+ *                min_p: of those, the ones with w_v >= min_p (min_p <= 0: all of
+ *                  them; above 1: as 1).
+ *   tokens       [R] int32 out: the smallest kept id at which the kept weights,
+ *                summed in id order, exceed uniforms[r] of their total.  -1 where
+ *                the row's largest logit is not finite, the row holds a NaN, or a
+ *                setting or the uniform is NaN or out of range.
+ * Weights are computed in 64 bits and held as whole multiples of 2^-F of the
+ * largest one, F = 62 - ceil(log2 V) (at most 50): the result does not depend on
+ * the order of any sum, and differs from the exact law's only where a uniform
+ * or a cut is nearer than about V * 2^-F to a border.  Results are the same on
+ * every call.  One launch.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, R < 0, V < 1, a
+ * value for every row that is NaN or out of range, an unknown dtype;
+ * SPEC_ERR_UNSUPPORTED for V > 2^30 or a grid too large for one launch.
+ */
+spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int32_t R, int32_t V, spec_dtype_t dtype,
+                                 const float* temperature, float all_temperature, const int32_t* top_k,
+                                 int32_t all_top_k, const float* top_p, float all_top_p, const float* min_p,
+                                 float all_min_p, int32_t* tokens, void* stream);
+
+/*
+ * Commit of the path that the drawn tokens take through a tree of drafts.
+ * Node 0 is the root, the token emitted last (its entry is not in the cache
+ * yet).  From there the walk goes on to the child with the lowest index whose
+ * token equals the one drawn at the node, until there is none.  With
+ * tokens drawn from the target's law at every node (spec_sample_tokens), the
+ * emitted tokens follow that law, whatever the drafts were.
+ *
+ *   cache        [P, B, L_max, E] of dtype, updated in place, and
+ *   staging      [P, B, N, E] of dtype: the nodes' entries, as for spec_kv_commit.
+ *                The path's entries go to cache positions cache_len[b] and on;
+ *                other entries are left as they were.
+ *   tokens       [B, N] int32: the nodes' tokens (the root's is not used).
+ *   parents      [B, N] int32; a sequence's parents[0] must be -1.
+ *   sampled      [B, N] int32: the token drawn at each node.
+ *   cache_len    [B] int32, and
+ *   new_len      [B] int32 out: cache_len + the path's nodes where it is committed,
+ *                else cache_len.  Either cache_len itself (advanced in place,
+ *                by a second launch) or a buffer apart from it (one launch).
+ *   accepted_len [B] int32 out: the path's drafts (its nodes but the root), or -1
+ *                when the sequence is faulty: parents[0] is not -1 (a padded
+ *                sequence), or a token drawn on the path is negative.
+ *   out_tokens   [B, N] int32 out: the tokens drawn along the path, then -1.
+ *   path         [B, N] int32 out, or NULL: the path's nodes, then -1.
+ *   status       [B] int32 out, or NULL: 0 committed; 1 no room (cache_len < 0 or
+ *                cache_len + the path > L_max); 2 faulty.  Nothing is committed
+ *                unless 0.
+ * Any alignment of whole elements works; rows of 16-byte multiples in aligned
+ * buffers take vectors.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, sizes out of
+ * range, an unknown dtype, or outputs that overlap each other or an input (but
+ * for new_len == cache_len); SPEC_ERR_UNSUPPORTED for N > SPEC_MAX_NODES or a
+ * grid too large for one launch.
+ */
+spec_status_t spec_tree_commit(void* cache, const void* staging, const int32_t* tokens, const int32_t* parents,
+                               const int32_t* sampled, const int32_t* cache_len, int32_t* new_len,
+                               int32_t* accepted_len, int32_t* out_tokens, int32_t* path, int32_t* status, int32_t P,
+                               int32_t B, int32_t N, int32_t L_max, int32_t E, spec_dtype_t dtype, void* stream);
+
+/*
+ * spec_tree_commit into a cache in the 8-bit block format: codes [P, B, L_max, E]
+ * and scales [P, B, L_max, ceil(E / 128)] bytes, as for spec_kv_commit_quantized.
+ */
+spec_status_t spec_tree_commit_quantized(void* codes, void* scales, const void* staging, const int32_t* tokens,
+                                         const int32_t* parents, const int32_t* sampled, const int32_t* cache_len,
+                                         int32_t* new_len, int32_t* accepted_len, int32_t* out_tokens, int32_t* path,
+                                         int32_t* status, int32_t P, int32_t B, int32_t N, int32_t L_max, int32_t E,
+                                         spec_dtype_t dtype, void* stream);
 
 /*
  * Measurement aid, not part of the method: reads `bytes` (a multiple of

@@ -27,6 +27,8 @@ __all__ = ["spec_verify", "VerifyPlan", "spec_verify_noalloc", "spec_verify_work
            "spec_kv_commit", "spec_verify_sparse_draft", "position_budget", "spec_draft_head_positions",
            "spec_draft_head_static", "spec_quantize_rows", "spec_draft_head_quantized",
            "spec_kv_commit_quantized", "spec_kv_read_quantized", "spec_token_logprobs",
+           "spec_tree_attention", "spec_tree_attention_quantized", "spec_sample_tokens", "spec_tree_commit",
+           "spec_tree_commit_quantized",
            "Workspace", "SpecVerifyError", "abi_version"]
 
 _DTYPES = {torch.bfloat16: _native.SPEC_BF16, torch.float32: _native.SPEC_F32}
@@ -781,3 +783,197 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int =
     _call(lib.spec_token_logprobs, "spec_token_logprobs", dev, logits.data_ptr(), tokens.data_ptr(), N, V, dt,
           temperature, top_n, lp.data_ptr(), entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), ws, wsb, raw)
     return lp, entropy, ids, top
+
+
+# ---- a step with a tree of drafts -------------------------------------------------
+
+def _tree_attention(q, cache, scales, new, parents, cache_len, scale, window, sinks, out, workspace, stream):
+    """cache: keys and values; scales: theirs (None: not quantised); new: the nodes' keys and values."""
+    _need_gpu(q, "q")
+    dt = _DTYPES.get(q.dtype)
+    if dt is None or q.dim() != 4:
+        raise ValueError("q must be bfloat16 or float32 [B, N, Hq, D]")
+    dev = q.device
+    B, N, Hq, D = q.shape
+    k = cache[0]
+    if k.dim() != 4:
+        raise ValueError("the cache's keys must be [B, L_max, Hkv, D]")
+    L, Hkv = k.shape[1], k.shape[2]
+    names = ("k_cache", "v_cache") if scales is None else ("k_codes", "v_codes")
+    for t, name in zip(cache, names):
+        _need(t, name, q.dtype if scales is None else _CODES, (B, L, Hkv, D), dev)
+    if scales is not None:
+        for t, name in zip(scales, ("k_scales", "v_scales")):
+            _need(t, name, _SCALES, (B, L, (Hkv * D + 127) // 128), dev)
+    for t, name in zip(new, ("k_new", "v_new")):
+        _need(t, name, q.dtype, (B, N, Hkv, D), dev)
+    _need(parents, "parents", torch.int32, (B, N), dev)
+    _need(cache_len, "cache_len", torch.int32, (B,), dev)
+    window, sinks = int(window), int(sinks)
+    _fits(B, N, Hq, D, L, Hkv, window, sinks)
+    if D < 1 or Hkv < 1 or Hq < 1:
+        raise ValueError("q must have heads of at least one value, and the cache heads")
+    if scale is None:
+        scale = D ** -0.5
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must be >= 0")
+    lib = _native.load()
+    need = lib.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, L, dt)
+    if out is None:
+        out, = _results(lambda: (torch.empty_like(q),), dev, stream)
+    else:
+        _need(out, "out", q.dtype, q.shape, dev)
+    raw = _raw_stream(dev, stream)
+    ws, wsb = None, 0
+    if need:
+        buf = _scratch(dev, need, raw, workspace, stream)
+        ws, wsb = buf.data_ptr(), buf.numel()
+    tail = (new[0].data_ptr(), new[1].data_ptr(), parents.data_ptr(), cache_len.data_ptr(), B, N, Hq, Hkv, D, L, scale,
+            window, sinks, dt, out.data_ptr(), ws, wsb, raw)
+    if scales is None:
+        _call(lib.spec_tree_attention, "spec_tree_attention", dev, q.data_ptr(), k.data_ptr(), cache[1].data_ptr(),
+              *tail)
+    else:
+        _call(lib.spec_tree_attention_quantized, "spec_tree_attention_quantized", dev, q.data_ptr(), k.data_ptr(),
+              scales[0].data_ptr(), cache[1].data_ptr(), scales[1].data_ptr(), *tail)
+    return out
+
+
+def spec_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tensor,
+                        v_new: torch.Tensor, parents: torch.Tensor, cache_len: torch.Tensor, *,
+                        scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                        out: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None,
+                        stream=None) -> torch.Tensor:
+    """Attention of a tree of drafts over the cache and the tree's own entries,
+    for one layer (see spec_tree_attention in specverify.h).
+
+    q [B, N, Hq, D] bf16 or float32; k_cache and v_cache [B, L_max, Hkv, D] and
+    k_new and v_new [B, N, Hkv, D] of the same dtype (planes of the cache and of
+    the staging buffer of spec_tree_commit); parents int32 [B, N] (-1: follows
+    the cache; a node's parent comes before it; -2 pads); cache_len int32 [B].
+    scale defaults to D^-0.5.  With a window, a node sees the last `window`
+    positions up to its own and the first `sinks`.  Returns [B, N, Hq, D]."""
+    return _tree_attention(q, (k_cache, v_cache), None, (k_new, v_new), parents, cache_len, scale, window, sinks, out,
+                           workspace, stream)
+
+
+def spec_tree_attention_quantized(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                                  v_codes: torch.Tensor, v_scales: torch.Tensor, k_new: torch.Tensor,
+                                  v_new: torch.Tensor, parents: torch.Tensor, cache_len: torch.Tensor, *,
+                                  scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                                  out: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None,
+                                  stream=None) -> torch.Tensor:
+    """spec_tree_attention over a cache in the 8-bit block format (see
+    spec_tree_attention_quantized in specverify.h): k_codes and v_codes
+    float8_e4m3fn [B, L_max, Hkv, D], k_scales and v_scales float8_e8m0fnu
+    [B, L_max, ceil(Hkv * D / 128)] (planes of spec_tree_commit_quantized's cache);
+    the others as there, bf16 or float32."""
+    return _tree_attention(q, (k_codes, v_codes), (k_scales, v_scales), (k_new, v_new), parents, cache_len, scale,
+                           window, sinks, out, workspace, stream)
+
+
+def _row_setting(v, name: str, dtype: torch.dtype, shape, device):
+    """(pointer, value) of a setting that is one for all rows or a tensor with one for each."""
+    if isinstance(v, torch.Tensor):
+        _need(v, name, dtype, shape, device)
+        return v.data_ptr(), 0
+    if dtype is torch.int32:
+        return None, max(-1, min(int(v), 0x7fffffff))
+    return None, float(v)
+
+
+def spec_sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tokens drawn from rows of logits from given uniforms (see spec_sample_tokens in specverify.h).
+
+    logits [..., V] (bf16 or float32), uniforms float32 [...] in [0, 1).  Each of
+    temperature (0: the largest logit), top_k (< 1: off), top_p (>= 1: off) and
+    min_p (<= 0: off) is a number, or a tensor [...] with a value per row (float32;
+    top_k int32).  Returns tokens int32 [...], -1 for a row whose largest
+    logit is not finite, that holds a NaN, or whose settings are out of range."""
+    _need_gpu(logits, "logits")
+    dt = _DTYPES.get(logits.dtype)
+    shape = logits.shape
+    if dt is None or not shape or shape[-1] < 1:
+        raise ValueError("logits must be bfloat16 or float32 [..., V] with V >= 1")
+    V, lead, dev = shape[-1], shape[:-1], logits.device
+    _need(uniforms, "uniforms", torch.float32, lead, dev)
+    R = uniforms.numel()
+    _fits(R, V)
+    settings = (*_row_setting(temperature, "temperature", torch.float32, lead, dev),
+                *_row_setting(top_k, "top_k", torch.int32, lead, dev),
+                *_row_setting(top_p, "top_p", torch.float32, lead, dev),
+                *_row_setting(min_p, "min_p", torch.float32, lead, dev))
+    if out is None:
+        out, = _results(lambda: (torch.empty_like(uniforms, dtype=torch.int32),), dev, stream)
+    else:
+        _need(out, "out", torch.int32, lead, dev)
+    _call(_native.load().spec_sample_tokens, "spec_sample_tokens", dev, logits.data_ptr(), uniforms.data_ptr(), R, V, dt,
+          *settings, out.data_ptr(), _raw_stream(dev, stream))
+    return out
+
+
+def _tree_commit(fn, what, buffers, staging, P, B, L, E, dt, tokens, parents, sampled, cache_len, new_len, status,
+                 stream):
+    dev = staging.device
+    N = staging.shape[2]
+    _fits(P, B, N, L, E)
+    for t, name in ((tokens, "tokens"), (parents, "parents"), (sampled, "sampled")):
+        _need(t, name, torch.int32, (B, N), dev)
+    _need(cache_len, "cache_len", torch.int32, (B,), dev)
+    if new_len is None:
+        new_len = cache_len
+    else:
+        _need(new_len, "new_len", torch.int32, (B,), dev)
+    if status is not None:
+        _need(status, "status", torch.int32, (B,), dev)
+
+    def make():
+        made = (torch.empty_like(cache_len), torch.empty_like(tokens), torch.empty_like(tokens))
+        return made if status is not None else made + (torch.empty_like(cache_len),)
+    accepted, out, path, status = (_results(make, dev, stream) + (() if status is None else (status,)))
+    _call(fn, what, dev, *buffers, staging.data_ptr(), tokens.data_ptr(), parents.data_ptr(), sampled.data_ptr(),
+          cache_len.data_ptr(), new_len.data_ptr(), accepted.data_ptr(), out.data_ptr(), path.data_ptr(),
+          status.data_ptr(), P, B, N, L, E, dt, _raw_stream(dev, stream))
+    return accepted, out, path, status
+
+
+def spec_tree_commit(cache: torch.Tensor, staging: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
+                     sampled: torch.Tensor, cache_len: torch.Tensor, new_len: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None):
+    """Walk along a tree of drafts and commit of its path (see spec_tree_commit in specverify.h).
+
+    cache [P, B, L_max, ...] and staging [P, B, N, ...] (bf16 or float32, the same
+    trailing shape); tokens, parents and sampled int32 [B, N]: the nodes'
+    tokens (node 0: the root), their parents (-1 for the root; -2 pads) and the
+    token drawn at each; cache_len int32 [B], advanced in place, or left alone when
+    new_len (int32 [B]) takes the new lengths, which saves a launch.  Returns
+    (accepted_len int32 [B], out_tokens int32 [B, N], path int32 [B, N], status
+    int32 [B]): the accepted drafts (-1: faulty), the tokens drawn along the path
+    and its nodes (then -1), and 0 committed, 1 no room, 2 faulty."""
+    _need_gpu(cache, "cache")
+    dt = _DTYPES.get(cache.dtype)
+    if dt is None or cache.dim() < 3:
+        raise ValueError("cache must be bfloat16 or float32 [P, B, L_max, ...]")
+    _need_gpu(staging, "staging", cache.device)
+    if staging.dtype is not cache.dtype or staging.dim() != cache.dim() or staging.shape[:2] != cache.shape[:2] or \
+            staging.shape[3:] != cache.shape[3:]:
+        raise ValueError("staging must be [P, B, N, ...] with the dtype and trailing shape of cache")
+    P, B, L = cache.shape[:3]
+    return _tree_commit(_native.load().spec_tree_commit, "spec_tree_commit", (cache.data_ptr(),), staging, P, B, L,
+                        math.prod(cache.shape[3:]), dt, tokens, parents, sampled, cache_len, new_len, status, stream)
+
+
+def spec_tree_commit_quantized(codes: torch.Tensor, scales: torch.Tensor, staging: torch.Tensor, tokens: torch.Tensor,
+                               parents: torch.Tensor, sampled: torch.Tensor, cache_len: torch.Tensor,
+                               new_len: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                               stream=None):
+    """spec_tree_commit into a cache in the 8-bit block format (see
+    spec_tree_commit_quantized in specverify.h): codes and scales as in
+    spec_kv_commit_quantized, staging [P, B, N, ...] bf16 or float32; the others
+    and the results as in spec_tree_commit."""
+    P, B, L, E = _kv_shape(codes, scales)
+    dt = _kv_other(staging, "staging", codes)
+    return _tree_commit(_native.load().spec_tree_commit_quantized, "spec_tree_commit_quantized",
+                        (codes.data_ptr(), scales.data_ptr()), staging, P, B, L, E, dt, tokens, parents, sampled,
+                        cache_len, new_len, status, stream)

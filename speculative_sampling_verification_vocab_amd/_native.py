@@ -89,6 +89,20 @@ def load() -> ctypes.CDLL:
         lib.spec_token_logprobs.restype = ctypes.c_int
         lib.spec_token_logprobs_workspace_bytes.argtypes = [i32, i32, ctypes.c_int, i32]
         lib.spec_token_logprobs_workspace_bytes.restype = sz
+        f32 = ctypes.c_float
+        attention = [i32, i32, i32, i32, i32, i32, f32, i32, i32, ctypes.c_int, P, P, sz, P]
+        lib.spec_tree_attention.argtypes = [P] * 7 + attention
+        lib.spec_tree_attention.restype = ctypes.c_int
+        lib.spec_tree_attention_quantized.argtypes = [P] * 9 + attention
+        lib.spec_tree_attention_quantized.restype = ctypes.c_int
+        lib.spec_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_int]
+        lib.spec_tree_attention_workspace_bytes.restype = sz
+        lib.spec_sample_tokens.argtypes = [P, P, i32, i32, ctypes.c_int, P, f32, P, i32, P, f32, P, f32, P, P]
+        lib.spec_sample_tokens.restype = ctypes.c_int
+        lib.spec_tree_commit.argtypes = [P] * 11 + [i32, i32, i32, i32, i32, ctypes.c_int, P]
+        lib.spec_tree_commit.restype = ctypes.c_int
+        lib.spec_tree_commit_quantized.argtypes = [P] * 12 + [i32, i32, i32, i32, i32, ctypes.c_int, P]
+        lib.spec_tree_commit_quantized.restype = ctypes.c_int
         _lib = lib
         return lib
 

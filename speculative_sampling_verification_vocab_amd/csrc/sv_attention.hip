@@ -1,0 +1,884 @@
+// Attention of a tree of drafted tokens over a KV cache and the tree's own
+// entries (gfx950, wave64).  For node i and query head h of KV head k:
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(c q.k_j - m),  c = scale * log2(e),
+// over the entries j that node i sees, with m a running reference: when a
+// tile's largest c q.k_j passes m by more than 8, m becomes that maximum and
+// what was summed is scaled down; otherwise p_j <= 2^8 and nothing is.
+//
+// The rows of a KV head are its G query heads of every node.  Four waves of a
+// block take 16 MT rows each against keys of their own, 32 at a time, and a
+// tile never leaves the wave's registers:
+//   S^T = K Q^T   matrix products with the keys as rows: a lane reads KW
+//                 consecutive values of its key straight from memory;
+//   P             stays where S^T's result is: lane (g, m) holds keys 16 u + 4 g + r
+//                 (u < 2, r < 4) of row m, and the second product takes its
+//                 inner index in just that order;
+//   O^T += V^T P^T  a lane reads CW consecutive values of the same keys' rows,
+//                 whole rows of V at a time; in bf16, value j of eight keys is
+//                 brought into one operand by byte permutes.
+// So keys and values are read once, with no shared memory and no barrier in
+// the loop.  The waves' results meet in shared memory, 16 rows at a time, and
+// those of blocks that share the keys in a second launch (tree_join_kernel).
+//
+// Sums, maxima and both products' accumulators are fp32.  The weights p are
+// rounded to bf16 for the bf16 product, half a step of 2^-8 each at random,
+// like the values they multiply.
+//
+// Entries that a row does not see weigh exactly 0 whatever they hold: their
+// score is replaced, and where a tile with such entries has a value that is not
+// finite, that value is left out of the product and added to the rows that see it.
+
+#include <type_traits>
+
+#include "sv_internal.h"
+#include "sv_quant.h"
+#include "sv_tree.h"
+
+namespace sv {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+  const void *q, *k_new, *v_new;              // [B][N][Hq][D], [B][N][Hkv][D]
+  const uint8_t *k_cache, *v_cache;           // [B][L][Hkv][D] values or codes
+  const uint8_t *k_scales, *v_scales;         // [B][L][nb]
+  const int32_t *parents, *cache_len;         // [B][N], [B]
+  void* out;                                  // [B][N][Hq][D]
+  float2* stats;                              // [slots][16 mt] reference and sum
+  float* acc;                                 // [slots][16 mt][D]
+  int N, Hq, Hkv, G, D, L, nb, R, groups, split;
+  uint32_t items;                             // B * Hkv * split
+  int window, sinks;
+  float c;
+};
+
+constexpr float kSlack = 8.0f;      // how far a weight's exponent may pass its reference
+constexpr float kNinf = -__builtin_inff();
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- operands -------------------------------------------------------------------
+
+// n consecutive values of a row as the matrix product takes them: dwords of two
+// bf16, or floats.
+template <typename T, int n>
+struct Frag {
+  static constexpr int kWords = std::is_same<T, float>::value ? n : n / 2;
+  uint32_t w[kWords];
+};
+
+template <typename T, int n>
+__device__ __forceinline__ void load_values(const uint8_t* p, Frag<T, n>& f) {
+  constexpr int W = Frag<T, n>::kWords;
+#pragma unroll
+  for (int i = 0; i + 4 <= W; i += 4) {
+    const u32x4 v = *reinterpret_cast<const typename AnyVector<typename std::conditional<
+        std::is_same<T, float>::value, float, uint16_t>::type>::type*>(p + 4 * i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f.w[i + q] = v[q];
+  }
+  if constexpr (W % 4 == 2) {
+    typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
+    const pair v = *reinterpret_cast<const pair*>(p + 4 * (W - 2));
+    f.w[W - 2] = v[0];
+    f.w[W - 1] = v[1];
+  }
+}
+
+template <typename T, int n>
+__device__ __forceinline__ void clear(Frag<T, n>& f) {
+#pragma unroll
+  for (int i = 0; i < Frag<T, n>::kWords; ++i) f.w[i] = 0;
+}
+
+// n codes with their scale to a fragment.
+template <typename T, int n>
+__device__ __forceinline__ void decode(const uint32_t (&q)[n / 4], const float* scale, Frag<T, n>& f) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int i = 0; i < n / 4; ++i) {
+    const float s = scale[i / 2];
+    if constexpr (std::is_same<T, float>::value) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
+      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
+      f.w[4 * i] = __float_as_uint(lo[0] * s);
+      f.w[4 * i + 1] = __float_as_uint(lo[1] * s);
+      f.w[4 * i + 2] = __float_as_uint(hi[0] * s);
+      f.w[4 * i + 3] = __float_as_uint(hi[1] * s);
+    } else {
+      f.w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], s, false));
+      f.w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], s, true));
+    }
+  }
+#endif
+}
+
+// 2^(byte - 127) by its bits; 255 stands for NaN and 0 for 2^-127.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+
+template <typename T>
+constexpr int kEs = std::is_same<T, float>::value ? 4 : 2;
+
+// Rows of keys or values: base is the first one's address for the block's head,
+// and rows are `stride` bytes apart.
+struct Rows {
+  const uint8_t* base;
+  const uint8_t* scales;  // its first row's scale byte 0
+  uint32_t stride;
+};
+
+// The shape of a kernel's operands.
+template <typename T, bool kQ, int DP, int MT>
+struct Shape {
+  static constexpr bool kF32 = std::is_same<T, float>::value;
+  static constexpr int U = kF32 && DP == 256 ? 1 : 2;    // keys / 16 of a tile (registers)
+  static constexpr int kKeys = 16 * U;
+  static constexpr int kSlots = 4 * U;                   // keys of a tile that a lane holds weights of
+  static constexpr int KW = kQ ? 16 : kF32 ? 4 : 8;      // consecutive values of a key per lane
+  static constexpr int KS = DP / (4 * KW);               // such pieces per key
+  static constexpr int CW = DP == 64 || (kF32 && !kQ) ? 4 : 8;  // consecutive values of a value row per lane
+  static constexpr int VS = DP / (16 * CW);              // such pieces per row
+  static constexpr int OT = DP / 16;                     // result tiles of 16 values: (piece, value)
+  typedef Frag<T, KW> Keys[U][KS];
+  typedef Frag<T, CW> Values[kSlots][VS];
+};
+
+// The tile's key of a lane's slot i: 16 u + 4 g + r.
+__device__ __forceinline__ int key_of(int i, int lane) { return i / 4 * 16 + (lane >> 4) * 4 + i % 4; }
+
+// Keys u * 16 + lane % 16 of a tile whose last key is `last`.
+template <typename S, typename T>
+__device__ __forceinline__ void load_keys(const Rows& r, int last, int D, int lane, typename S::Keys& k) {
+  constexpr int n = S::KW > 8 ? 8 : S::KW;  // D is a multiple of 8
+#pragma unroll
+  for (int u = 0; u < S::U; ++u) {
+    const uint32_t row = (uint32_t)min(u * 16 + (lane & 15), last) * r.stride;
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s)
+#pragma unroll
+      for (int e = 0; e < S::KW; e += n) {
+        const int d = s * 4 * S::KW + (lane >> 4) * S::KW + e;
+        Frag<T, n> f;
+        load_values<T, n>(r.base + (row + (uint32_t)((d < D ? d : 0) * kEs<T>)), f);
+#pragma unroll
+        for (int i = 0; i < Frag<T, n>::kWords; ++i) k[u][s].w[e * kEs<T> / 4 + i] = f.w[i];
+      }
+  }
+}
+
+// Values of the lane's slots: whole rows, CW consecutive values per lane and piece.
+template <typename S, typename T>
+__device__ __forceinline__ void load_rows(const Rows& r, int last, int D, int lane, typename S::Values& v) {
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) {
+    const uint32_t row = (uint32_t)min(key_of(i, lane), last) * r.stride;
+#pragma unroll
+    for (int s = 0; s < S::VS; ++s) {
+      const int d = s * 16 * S::CW + (lane & 15) * S::CW;
+      load_values<T, S::CW>(r.base + (row + (uint32_t)((d < D ? d : 0) * kEs<T>)), v[i][s]);
+    }
+  }
+}
+
+// Keys as codes: 16 per piece, and a scale for each 8.
+template <typename S>
+struct KeyCodes {
+  uint32_t w[S::U][S::KS][4];
+  uint32_t scale[S::U][S::KS][2];
+};
+template <typename S>
+struct ValueCodes {
+  uint32_t w[S::kSlots][S::VS][S::CW / 4];
+  uint32_t scale[S::kSlots][S::VS];
+};
+
+// one: the head lies in whole blocks of 128, or inside one, so that a scale
+// serves 128 values (or all of them).
+template <typename S>
+__device__ __forceinline__ void load_key_codes(const Rows& r, int nb, int head, int last, int D, bool one, int lane,
+                                               KeyCodes<S>& c) {
+#pragma unroll
+  for (int u = 0; u < S::U; ++u) {
+    const uint32_t key = (uint32_t)min(u * 16 + (lane & 15), last);
+    const uint32_t row = key * r.stride;
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s) {
+      const int d = s * 64 + (lane >> 4) * 16;
+      if (D % 16 == 0) {
+        const u32x4 v = *reinterpret_cast<const u32x4_any1*>(r.base + (row + (uint32_t)(d < D ? d : 0)));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c.w[u][s][q] = v[q];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const u32x2_any v = *reinterpret_cast<const u32x2_any*>(r.base + (row + (uint32_t)(d + 8 * e < D ? d + 8 * e : 0)));
+          c.w[u][s][2 * e] = v[0];
+          c.w[u][s][2 * e + 1] = v[1];
+        }
+      }
+      if (one) {
+        if (s % 2 == 0) c.scale[u][s][0] = r.scales[key * (uint32_t)nb + (uint32_t)((head + s * 64) >> 7)];
+        else c.scale[u][s][0] = c.scale[u][s & ~1][0];
+        c.scale[u][s][1] = c.scale[u][s][0];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = d + 8 * e < D ? d + 8 * e : 0;
+          c.scale[u][s][e] = r.scales[key * (uint32_t)nb + (uint32_t)((head + at) >> 7)];
+        }
+      }
+    }
+  }
+}
+
+template <int n>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[n / 4]) {
+  if constexpr (n == 8) {
+    const u32x2_any v = *reinterpret_cast<const u32x2_any*>(p);
+    w[0] = v[0];
+    w[1] = v[1];
+  } else {
+    typedef uint32_t word __attribute__((aligned(1)));
+    w[0] = *reinterpret_cast<const word*>(p);
+  }
+}
+
+template <typename S>
+__device__ __forceinline__ void load_row_codes(const Rows& r, int nb, int head, int last, int D, int lane,
+                                               ValueCodes<S>& c) {
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) {
+    const uint32_t key = (uint32_t)min(key_of(i, lane), last);
+#pragma unroll
+    for (int s = 0; s < S::VS; ++s) {
+      const int d = s * 16 * S::CW + (lane & 15) * S::CW;
+      const int at = d < D ? d : 0;
+      load_codes<S::CW>(r.base + (key * r.stride + (uint32_t)at), c.w[i][s]);
+      c.scale[i][s] = r.scales[key * (uint32_t)nb + (uint32_t)((head + at) >> 7)];
+    }
+  }
+}
+
+// ---- products -------------------------------------------------------------------
+
+__device__ __forceinline__ f32x4 mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+__device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+
+// c += the products of n values of 16 keys with those of 16 rows.
+template <typename T, int n>
+__device__ __forceinline__ f32x4 product(const Frag<T, n>& a, const Frag<T, n>& b, f32x4 c) {
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) c = mfma(__uint_as_float(a.w[i]), __uint_as_float(b.w[i]), c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n / 2; i += 4) {
+      const uint32_t x[4] = {a.w[i], a.w[i + 1], a.w[i + 2], a.w[i + 3]};
+      const uint32_t y[4] = {b.w[i], b.w[i + 1], b.w[i + 2], b.w[i + 3]};
+      c = mfma(x, y, c);
+    }
+  }
+  return c;
+}
+
+// The two halves of dwords a and b that hold value `odd` of each.
+__device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, int odd) {
+  return __builtin_amdgcn_perm(b, a, odd ? 0x07060302u : 0x05040100u);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
+// What a wave keeps of its 16 MT rows.
+template <typename S, int MT>
+struct Sums {
+  f32x4 o[MT][S::OT];  // tile (piece s, value j): rows 4 g + r are values s * 16 CW + (4 g + r) * CW + j
+  float m[MT];         // reference, the same in the four lanes of a row
+  float l[MT];         // the lane's part of the sum
+};
+
+// Values past the head stand for zeros: the queries' are, but 0 times an infinity is not 0.
+template <typename S, typename T>
+__device__ __forceinline__ void cut_key(int D, int s, int lane, Frag<T, S::KW>& k) {
+#pragma unroll
+  for (int i = 0; i < Frag<T, S::KW>::kWords; ++i) {
+    const int d = s * 4 * S::KW + (lane >> 4) * S::KW + i * 4 / kEs<T>;
+    k.w[i] = d < D ? k.w[i] : 0u;
+  }
+}
+
+// Scores to weights: x[t][u][r] is row t * 16 + lane % 16's product with key 16 u + 4 g + r.  seen: null, or
+// bit i says whether the row sees the lane's slot i.  The references move where a row's largest score passes its own
+// by more than the slack.
+template <typename S, int MT, bool kMasked>
+__device__ __forceinline__ void weigh(f32x4 (&x)[MT][S::U], const uint32_t (&seen)[MT], float c, Sums<S, MT>& z) {
+  float top[MT];
+  bool move = false;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    top[t] = kNinf;
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i) {
+      if constexpr (kMasked) x[t][i / 4][i % 4] = seen[t] >> i & 1 ? x[t][i / 4][i % 4] : kNinf;
+      top[t] = fmaxf(top[t], x[t][i / 4][i % 4]);
+    }
+    top[t] *= c;
+    move |= top[t] > z.m[t] + kSlack;
+  }
+  if (__any(move)) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float w = fmaxf(top[t], __shfl_xor(top[t], 16));
+      w = fmaxf(w, __shfl_xor(w, 32));
+      const float m = fmaxf(z.m[t], w);
+      const float f = m == kNinf ? 1.0f : exp2_of(z.m[t] - m);
+      z.m[t] = m;
+      z.l[t] *= f;
+#pragma unroll
+      for (int i = 0; i < S::OT; ++i) z.o[t][i] *= f;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const float m = z.m[t] == kNinf ? 0.0f : z.m[t];
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i) {
+      x[t][i / 4][i % 4] = exp2_of(__builtin_fmaf(x[t][i / 4][i % 4], c, -m));
+      z.l[t] += x[t][i / 4][i % 4];
+    }
+  }
+}
+
+// z += V^T P^T for one piece of the tile's values.
+template <typename S, typename T, int MT>
+__device__ __forceinline__ void add_piece(const Frag<T, S::CW> (&v)[S::kSlots], int s, const f32x4 (&p)[MT][S::U],
+                                          Sums<S, MT>& z) {
+  if constexpr (S::kF32) {
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i)
+#pragma unroll
+      for (int j = 0; j < S::CW; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          z.o[t][s * S::CW + j] = mfma(__uint_as_float(v[i].w[j]), p[t][i / 4][i % 4], z.o[t][s * S::CW + j]);
+  } else {
+    uint32_t w[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[t][i] = pack2(p[t][i / 2][2 * i % 4], p[t][i / 2][2 * i % 4 + 1]);
+#pragma unroll
+    for (int j = 0; j < S::CW; ++j) {
+      uint32_t a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = halves(v[2 * i].w[j / 2], v[2 * i + 1].w[j / 2], j & 1);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) z.o[t][s * S::CW + j] = mfma(a, w[t], z.o[t][s * S::CW + j]);
+    }
+  }
+}
+
+// Bits of w that an infinity or NaN has, and w without such values.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (std::is_same<T, float>::value) return (w & 0x7f800000u) == 0x7f800000u ? 0xffffffffu : 0u;
+  else return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// ---- the kernel -----------------------------------------------------------------
+
+// Result of a row in shared memory: DP values, padded so that the sixteen rows
+// of a tile start in different banks.
+template <int DP>
+constexpr int kPad = DP + 4;
+
+template <typename T, bool kQ, int DP, int MT>
+__global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2) tree_attention_kernel(AttnArgs a) {
+  typedef Shape<T, kQ, DP, MT> S;
+  __shared__ uint64_t line_of[kMaxNodes];
+  __shared__ int depth_of[kMaxNodes];
+  __shared__ float2 stat[kWavesPerBlock][16 * MT];
+  __shared__ float part[kWavesPerBlock][16 * kPad<DP>];
+
+  // Blocks that share keys, one per group of rows, are eight apart: the same XCD.
+  const uint32_t eight = blockIdx.x / (8u * a.groups), rest = blockIdx.x % (8u * a.groups);
+  const uint32_t item = eight * 8 + rest % 8;
+  const int group = (int)(rest / 8);
+  if (item >= a.items) return;
+  const int split = (int)(item % (uint32_t)a.split);
+  const int h = (int)(item / (uint32_t)a.split % (uint32_t)a.Hkv);
+  const int b = (int)(item / (uint32_t)a.split / (uint32_t)a.Hkv);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, g = lane >> 4;
+  const int length = a.cache_len[b];
+  const bool valid = length >= 0 && length <= a.L;
+  const int n = valid ? length : 0;
+
+  if (wave == 0) {
+    const TreeNode t = tree_node(lane < a.N ? a.parents[(size_t)b * a.N + lane] : -2, lane, a.N);
+    line_of[lane] = t.line;
+    depth_of[lane] = t.depth;
+  }
+
+  // The rows' queries: row m is node m / G, head m % G of the KV head's G.
+  const int row0 = group * 16 * MT;
+  Frag<T, S::KW> q[MT][S::KS];
+  int node[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = row0 + t * 16 + (lane & 15);
+    node[t] = m < a.R ? m / a.G : 0;
+    const int head = h * a.G + (m < a.R ? m - node[t] * a.G : 0);
+    const uint8_t* p = static_cast<const uint8_t*>(a.q) + (((size_t)b * a.N + node[t]) * a.Hq + head) * (size_t)a.D * kEs<T>;
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s)
+#pragma unroll
+      for (int e = 0; e < S::KW; e += (S::KW > 8 ? 8 : S::KW)) {
+        constexpr int w = S::KW > 8 ? 8 : S::KW;
+        const int d = s * 4 * S::KW + g * S::KW + e;
+        Frag<T, w> f;
+        if (d < a.D) load_values<T, w>(p + d * kEs<T>, f);
+        else clear(f);
+#pragma unroll
+        for (int i = 0; i < Frag<T, w>::kWords; ++i) q[t][s].w[e * kEs<T> / 4 + i] = f.w[i];
+      }
+  }
+
+  // The keys: cache entries that every node sees before the window (none without
+  // one), those from the first that the window of any node reaches, and the
+  // tree's own.
+  int low = 0, first = 0;
+  if (a.window > 0) {
+    low = max(0, n - a.window + 1);
+    first = min(a.sinks, low);
+    if (first == low) first = low = 0;
+  }
+  constexpr int kKeys = S::kKeys;
+  const int tiles_first = (first + kKeys - 1) / kKeys, tiles_cache = tiles_first + (n - low + kKeys - 1) / kKeys;
+  const int tiles = valid ? tiles_cache + (a.N + kKeys - 1) / kKeys : 0;
+  const int from = (int)((long long)tiles * split / a.split), to = (int)((long long)tiles * (split + 1) / a.split);
+  const int edge = a.window > 0 ? n + a.N - 1 - a.window : -1;  // no window hides a later entry from any node
+  const size_t heads = (size_t)a.Hkv * a.D;                     // values per entry
+  const int head = h * a.D;
+  const bool one_scale = a.D % 128 == 0 ? head % 128 == 0 : head % 128 + a.D <= 128;
+
+  Sums<S, MT> z;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    z.m[t] = kNinf;
+    z.l[t] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S::OT; ++i) z.o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  __syncthreads();
+
+  // A tile of the cache: its first entry, and the tile's last key.
+  auto place = [&](int tile, int& j0) {
+    j0 = tile < tiles_first ? tile * kKeys : low + (tile - tiles_first) * kKeys;
+    return min(kKeys, (tile < tiles_first ? first : n) - j0) - 1;
+  };
+  auto rows_at = [&](const uint8_t* base, const uint8_t* scales, int j0) {
+    const size_t row = (size_t)b * a.L + j0;
+    Rows r;
+    r.base = base + (row * heads + head) * (kQ ? 1 : kEs<T>);
+    r.scales = kQ ? scales + row * (size_t)a.nb : nullptr;
+    r.stride = (uint32_t)heads * (kQ ? 1 : kEs<T>);
+    return r;
+  };
+  typedef typename std::conditional<kQ, KeyCodes<S>, typename S::Keys>::type CacheKeys;
+  CacheKeys k;
+  auto fetch_keys = [&](int tile) {
+    int j0;
+    const int last = place(tile, j0);
+    const Rows r = rows_at(a.k_cache, a.k_scales, j0);
+    if constexpr (kQ) load_key_codes<S>(r, a.nb, head, last, a.D, one_scale, lane, k);
+    else load_keys<S, T>(r, last, a.D, lane, k);
+  };
+  auto add_key = [&](Frag<T, S::KW>& f, int u, int s, f32x4 (&x)[MT][S::U]) {
+    if (a.D < DP) cut_key<S, T>(a.D, s, lane, f);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) x[t][u] = product<T, S::KW>(f, q[t][s], s == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[t][u]);
+  };
+  // Tiles that some row does not see all of: values that are not finite are taken out of the product (bits of the slots
+  // that had some), and added to the rows that see them: an infinity or NaN outweighs whatever its weight is.
+  // value(key, d): the CW values from d on.
+  auto take_out = [&](typename S::Values& v) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i)
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+        for (int w = 0; w < Frag<T, S::CW>::kWords; ++w) {
+          const uint32_t f = not_finite<T>(v[i][s].w[w]);
+          v[i][s].w[w] &= ~f;
+          bad |= f != 0 ? 1u << i : 0u;
+        }
+    return bad;
+  };
+  auto add_others = [&](uint32_t bad, const uint32_t (&seen)[MT], auto value) {
+    if (!__any(bad != 0)) return;
+#pragma unroll 1
+    for (int key = 0; key < kKeys; ++key) {
+      const int group16 = (key >> 2) & 3, slot = (key >> 4) * 4 + (key & 3);
+      if (!__any((lane >> 4) == group16 && (bad >> slot & 1))) continue;
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int d = s * 16 * S::CW + (g * 4 + r) * S::CW;
+          const Frag<T, S::CW> f = value(key, d < a.D ? d : 0);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const bool sees = __shfl(seen[t], group16 * 16 + (lane & 15)) >> slot & 1;
+#pragma unroll
+            for (int j = 0; j < S::CW; ++j) {
+              uint32_t w;
+              if constexpr (S::kF32) w = f.w[j];
+              else w = j & 1 ? f.w[j / 2] & 0xffff0000u : f.w[j / 2] << 16;
+              const bool add = sees && (w & 0x7f800000u) == 0x7f800000u;
+              z.o[t][s * S::CW + j][r] += add ? __uint_as_float(w) : 0.0f;
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers
+        }
+    }
+  };
+
+  if (from + wave < min(to, tiles_cache)) fetch_keys(from + wave);
+  for (int tile = from + wave; tile < min(to, tiles_cache); tile += kWavesPerBlock) {
+    int j0;
+    const int last = place(tile, j0);
+    const Rows rows = rows_at(a.v_cache, a.v_scales, j0);
+    typedef typename std::conditional<kQ, ValueCodes<S>, typename S::Values>::type CacheValues;
+    CacheValues raw;
+    if constexpr (kQ) load_row_codes<S>(rows, a.nb, head, last, a.D, lane, raw);
+    else load_rows<S, T>(rows, last, a.D, lane, raw);
+    f32x4 x[MT][S::U];
+#pragma unroll
+    for (int u = 0; u < S::U; ++u)
+#pragma unroll
+      for (int s = 0; s < S::KS; ++s) {
+        if constexpr (kQ) {
+          const float sc[2] = {scale_of(k.scale[u][s][0]), scale_of(k.scale[u][s][1])};
+          Frag<T, S::KW> f;
+          decode<T, S::KW>(k.w[u][s], sc, f);
+          add_key(f, u, s, x);
+        } else {
+          add_key(k[u][s], u, s, x);
+        }
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    if (tile + kWavesPerBlock < min(to, tiles_cache)) fetch_keys(tile + kWavesPerBlock);
+    const bool masked = last < kKeys - 1 || (tile >= tiles_first && j0 <= edge);
+    uint32_t seen[MT];
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;  // up to here, but for the first
+        seen[t] = 0;
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i) {
+          const int off = key_of(i, lane), j = j0 + off;
+          seen[t] |= off <= last && (j > hidden || j < a.sinks) ? 1u << i : 0u;
+        }
+      }
+      weigh<S, MT, true>(x, seen, a.c, z);
+    } else {
+      weigh<S, MT, false>(x, seen, a.c, z);
+    }
+    if constexpr (kQ) {
+      typename S::Values v;
+#pragma unroll
+      for (int i = 0; i < S::kSlots; ++i)
+#pragma unroll
+        for (int s = 0; s < S::VS; ++s) {
+          const float sc = scale_of(raw.scale[i][s]);
+          decode<T, S::CW>(raw.w[i][s], &sc, v[i][s]);
+        }
+      uint32_t bad = 0;
+      if (masked) bad = take_out(v);
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s) {
+        Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i) piece[i] = v[i][s];
+        add_piece<S, T, MT>(piece, s, x, z);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (masked)
+        add_others(bad, seen, [&](int key, int d) {
+          const uint32_t at = (uint32_t)min(key, last);
+          uint32_t w[S::CW / 4];
+          load_codes<S::CW>(rows.base + (at * rows.stride + (uint32_t)d), w);
+          const float sc = scale_of(rows.scales[at * (uint32_t)a.nb + (uint32_t)((head + d) >> 7)]);
+          Frag<T, S::CW> f;
+          decode<T, S::CW>(w, &sc, f);
+          return f;
+        });
+    } else {
+      uint32_t bad = 0;
+      if (masked) bad = take_out(raw);
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s) {
+        Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i) piece[i] = raw[i][s];
+        add_piece<S, T, MT>(piece, s, x, z);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (masked)
+        add_others(bad, seen, [&](int key, int d) {
+          Frag<T, S::CW> f;
+          load_values<T, S::CW>(rows.base + ((uint32_t)min(key, last) * rows.stride + (uint32_t)(d * kEs<T>)), f);
+          return f;
+        });
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // The tree's own entries: a node sees its ancestors and itself.
+#pragma unroll 1
+  for (int tile = from + wave; tile < to; tile += kWavesPerBlock) {
+    if (tile < tiles_cache) continue;
+    const int j0 = (tile - tiles_cache) * kKeys, last = min(kKeys, a.N - j0) - 1;
+    const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
+    const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
+    const Rows vr{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
+    typename S::Keys own;
+    load_keys<S, T>(kr, last, a.D, lane, own);
+    f32x4 x[MT][S::U];
+#pragma unroll
+    for (int u = 0; u < S::U; ++u)
+#pragma unroll
+      for (int s = 0; s < S::KS; ++s) add_key(own[u][s], u, s, x);
+    __builtin_amdgcn_sched_barrier(0);
+    typename S::Values v;
+    load_rows<S, T>(vr, last, a.D, lane, v);
+    uint32_t seen[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint64_t line = line_of[node[t]];
+      const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;
+      seen[t] = 0;
+#pragma unroll
+      for (int i = 0; i < S::kSlots; ++i) {
+        const int off = key_of(i, lane), j = j0 + off;
+        if (off > last || !(line >> j & 1)) continue;
+        const int position = n + depth_of[j];
+        seen[t] |= position > hidden || position < a.sinks ? 1u << i : 0u;
+      }
+    }
+    weigh<S, MT, true>(x, seen, a.c, z);
+    const uint32_t bad = take_out(v);
+#pragma unroll
+    for (int s = 0; s < S::VS; ++s) {
+      Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+      for (int i = 0; i < S::kSlots; ++i) piece[i] = v[i][s];
+      add_piece<S, T, MT>(piece, s, x, z);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    add_others(bad, seen, [&](int key, int d) {
+      Frag<T, S::CW> f;
+      load_values<T, S::CW>(vr.base + ((uint32_t)min(key, last) * vr.stride + (uint32_t)(d * kEs<T>)), f);
+      return f;
+    });
+  }
+
+  // The waves' results, 16 rows at a time.
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    z.l[t] += __shfl_xor(z.l[t], 16);
+    z.l[t] += __shfl_xor(z.l[t], 32);
+    if (g == 0) stat[wave][t * 16 + (lane & 15)] = float2{z.m[t], z.l[t]};
+  }
+  __syncthreads();
+  const size_t slot = ((size_t)item * a.groups + group) * (16 * MT);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    {
+      const int r = t * 16 + (lane & 15);
+      float m = stat[0][r].x;
+#pragma unroll
+      for (int w = 1; w < kWavesPerBlock; ++w) m = fmaxf(m, stat[w][r].x);
+      const float f = z.m[t] == kNinf ? 0.0f : exp2_of(z.m[t] - m);
+      float* to = &part[wave][(lane & 15) * kPad<DP>];
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+          for (int j = 0; j < S::CW; j += 4) {
+            f32x4 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = z.l[t] == 0.0f ? 0.0f : z.o[t][s * S::CW + j + i][r4] * f;
+            *reinterpret_cast<f32x4*>(to + s * 16 * S::CW + (g * 4 + r4) * S::CW + j) = y;
+          }
+    }
+    __syncthreads();
+    constexpr int kQuads = DP / 4;
+#pragma unroll
+    for (int k = 0; k < 16 * kQuads / kBlock; ++k) {
+      const int at = k * kBlock + threadIdx.x, r = at / kQuads, d = at % kQuads * 4;
+      const int m = row0 + t * 16 + r;
+      if (m >= a.R || d >= a.D) continue;
+      f32x4 y = *reinterpret_cast<const f32x4*>(&part[0][r * kPad<DP> + d]);
+#pragma unroll
+      for (int w = 1; w < kWavesPerBlock; ++w) y += *reinterpret_cast<const f32x4*>(&part[w][r * kPad<DP> + d]);
+      float ref = stat[0][t * 16 + r].x;
+#pragma unroll
+      for (int w = 1; w < kWavesPerBlock; ++w) ref = fmaxf(ref, stat[w][t * 16 + r].x);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWavesPerBlock; ++w) {
+        const float2 s = stat[w][t * 16 + r];
+        l += s.x == kNinf ? s.y : s.y * exp2_of(s.x - ref);
+      }
+      const int nd = m / a.G;
+      if (!valid) l = __builtin_nanf("");
+      if (line_of[nd] == 0) l = 0.0f;
+      if (a.split > 1) {
+        if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
+        if (d == 0) a.stats[slot + t * 16 + r] = float2{l == 0.0f ? kNinf : ref, l};
+        continue;
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = l == 0.0f ? 0.0f : y[i] * inv;
+      const size_t at_out = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
+      if constexpr (S::kF32) {
+        typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
+        *reinterpret_cast<quad*>(static_cast<float*>(a.out) + at_out) = quad{y[0], y[1], y[2], y[3]};
+      } else {
+        typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
+        *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + at_out) = pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The splits' results of a row: 64 lanes take its values, four each.
+template <typename T>
+__global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t rows, int rows_per_slot) {
+  const uint32_t row = blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & (kWave - 1), d = lane * 4;
+  const int m = (int)(row % (uint32_t)a.R);
+  const uint32_t pair = row / (uint32_t)a.R;  // b * Hkv + h
+  const int h = (int)(pair % (uint32_t)a.Hkv), b = (int)(pair / (uint32_t)a.Hkv);
+  const int group = m / rows_per_slot, r = m % rows_per_slot;
+  auto at = [&](int s) { return (((size_t)pair * a.split + s) * a.groups + group) * rows_per_slot + r; };
+  float ref = kNinf;
+  bool bad = false;
+  for (int s = 0; s < a.split; ++s) {
+    const float2 w = a.stats[at(s)];
+    bad |= w.y != w.y;
+    if (w.y != 0.0f) ref = fmaxf(ref, w.x);
+  }
+  float l = 0.0f;
+  f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < a.split; ++s) {
+    const float2 w = a.stats[at(s)];
+    if (w.y == 0.0f) continue;
+    const float f = w.x == kNinf ? 1.0f : exp2_of(w.x - ref);
+    l += w.y * f;
+    if (d < a.D && !bad) y += *reinterpret_cast<const f32x4*>(a.acc + at(s) * (size_t)a.D + d) * f;
+  }
+  if (d >= a.D) return;
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = bad ? __builtin_nanf("") : l == 0.0f ? 0.0f : y[i] * inv;
+  const int nd = m / a.G;
+  const size_t to = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
+  if constexpr (std::is_same<T, float>::value) {
+    typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
+    *reinterpret_cast<quad*>(static_cast<float*>(a.out) + to) = quad{y[0], y[1], y[2], y[3]};
+  } else {
+    typedef uint32_t pair2 __attribute__((ext_vector_type(2), aligned(2)));
+    *reinterpret_cast<pair2*>(static_cast<uint16_t*>(a.out) + to) = pair2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+  }
+}
+
+template <typename T, bool kQ, int DP, int MT>
+void start(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT>), dim3(p.grid), dim3(kBlock), 0, st, a);
+}
+
+template <typename T, bool kQ, int DP>
+void start_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if (p.mt == 1) start<T, kQ, DP, 1>(a, p, st);
+  else if constexpr (DP <= 128) start<T, kQ, DP, 2>(a, p, st);
+}
+
+template <typename T, bool kQ>
+hipError_t run(const AttnArgs& a, const AttnPlan& p, int B, hipStream_t st) {
+  if (p.dp == 64) start_rows<T, kQ, 64>(a, p, st);
+  else if (p.dp == 128) start_rows<T, kQ, 128>(a, p, st);
+  else start_rows<T, kQ, 256>(a, p, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.split == 1) return e;
+  const uint32_t rows = (uint32_t)B * a.Hkv * a.R;
+  hipLaunchKernelGGL((tree_join_kernel<T>), dim3((rows + kWavesPerBlock - 1) / kWavesPerBlock), dim3(kBlock), 0, st, a,
+                     rows, 16 * p.mt);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, int N, int Hq, int Hkv, int D, int L,
+                                 float scale, int window, int sinks, int dtype, const AttnPlan& plan, void* workspace,
+                                 hipStream_t st) {
+  AttnArgs a{};
+  a.q = io.q;
+  a.k_new = io.k_new;
+  a.v_new = io.v_new;
+  a.k_cache = static_cast<const uint8_t*>(io.k_cache);
+  a.v_cache = static_cast<const uint8_t*>(io.v_cache);
+  a.k_scales = static_cast<const uint8_t*>(io.k_scales);
+  a.v_scales = static_cast<const uint8_t*>(io.v_scales);
+  a.parents = io.parents;
+  a.cache_len = io.cache_len;
+  a.out = const_cast<void*>(io.out);
+  if (plan.split > 1) {
+    a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.stats);
+    a.acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.acc);
+  }
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.D = D;
+  a.L = L;
+  a.nb = quant_blocks(Hkv * D);
+  a.R = plan.R;
+  a.groups = plan.groups;
+  a.split = plan.split;
+  a.items = (uint32_t)B * Hkv * plan.split;
+  a.window = window;
+  a.sinks = sinks;
+  a.c = scale * 1.44269504088896340736f;
+  if (dtype == 1) return quantized ? run<uint16_t, true>(a, plan, B, st) : run<uint16_t, false>(a, plan, B, st);
+  return quantized ? run<float, true>(a, plan, B, st) : run<float, false>(a, plan, B, st);
+}
+
+}  // namespace sv

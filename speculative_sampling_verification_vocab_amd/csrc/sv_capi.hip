@@ -369,6 +369,101 @@ spec_status_t spec_token_logprobs(const void* logits, const int32_t* tokens, int
   return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
+namespace {
+
+spec_status_t tree_attention(const sv::AttnPointers& io, bool quantized, int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                             int32_t D, int32_t L_max, float scale, int32_t window, int32_t sinks, spec_dtype_t dtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  sv::AttnPlan plan{};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_attention(io, quantized, B, N, Hq, Hkv, D, L_max, scale, window, sinks, dtype,
+                                                  workspace, workspace_bytes, &plan, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_tree_attention(io, quantized, B, N, Hq, Hkv, D, L_max, scale, window, sinks,
+                                                 dtype == SPEC_BF16 ? 1 : 0, plan, workspace,
+                                                 static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+}  // namespace
+
+spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_new,
+                                  const void* v_new, const int32_t* parents, const int32_t* cache_len, int32_t B,
+                                  int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max, float scale,
+                                  int32_t window, int32_t sinks, spec_dtype_t dtype, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  const sv::AttnPointers io{q, k_cache, nullptr, v_cache, nullptr, k_new, v_new, parents, cache_len, out};
+  return tree_attention(io, false, B, N, Hq, Hkv, D, L_max, scale, window, sinks, dtype, workspace, workspace_bytes,
+                        stream);
+}
+
+spec_status_t spec_tree_attention_quantized(const void* q, const void* k_codes, const void* k_scales,
+                                            const void* v_codes, const void* v_scales, const void* k_new,
+                                            const void* v_new, const int32_t* parents, const int32_t* cache_len,
+                                            int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
+                                            float scale, int32_t window, int32_t sinks, spec_dtype_t dtype, void* out,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  const sv::AttnPointers io{q, k_codes, k_scales, v_codes, v_scales, k_new, v_new, parents, cache_len, out};
+  return tree_attention(io, true, B, N, Hq, Hkv, D, L_max, scale, window, sinks, dtype, workspace, workspace_bytes,
+                        stream);
+}
+
+size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
+                                           spec_dtype_t dtype) {
+  sv::AttnPlan plan{};
+  bool empty = false;
+  return sv::check_attention(B, N, Hq, Hkv, D, L_max, dtype, &plan, &empty) == SPEC_OK && !empty ? plan.total : 0;
+}
+
+spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int32_t R, int32_t V, spec_dtype_t dtype,
+                                 const float* temperature, float all_temperature, const int32_t* top_k,
+                                 int32_t all_top_k, const float* top_p, float all_top_p, const float* min_p,
+                                 float all_min_p, int32_t* tokens, void* stream) {
+  const sv::SampleSettings set{{temperature, all_temperature}, {top_k, all_top_k}, {top_p, all_top_p},
+                               {min_p, all_min_p}};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_sample(logits, uniforms, R, V, dtype, set, tokens, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_sample_tokens(logits, uniforms, R, V, dtype == SPEC_BF16 ? 1 : 0, set, tokens,
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+spec_status_t spec_tree_commit(void* cache, const void* staging, const int32_t* tokens, const int32_t* parents,
+                               const int32_t* sampled, const int32_t* cache_len, int32_t* new_len,
+                               int32_t* accepted_len, int32_t* out_tokens, int32_t* path, int32_t* status, int32_t P,
+                               int32_t B, int32_t N, int32_t L_max, int32_t E, spec_dtype_t dtype, void* stream) {
+  const sv::TreeCommitIO io{tokens, parents, sampled, cache_len, new_len, accepted_len, out_tokens, path, status};
+  sv::TreeCopyPlan plan{};
+  bool empty = false;
+  const spec_status_t sc = sv::validate_tree_commit(cache, staging, io, P, B, N, L_max, E, dtype, &plan, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_tree_commit(cache, staging, io, P, B, N, L_max, E, dtype == SPEC_BF16 ? 2 : 4, plan,
+                                              static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
+spec_status_t spec_tree_commit_quantized(void* codes, void* scales, const void* staging, const int32_t* tokens,
+                                         const int32_t* parents, const int32_t* sampled, const int32_t* cache_len,
+                                         int32_t* new_len, int32_t* accepted_len, int32_t* out_tokens, int32_t* path,
+                                         int32_t* status, int32_t P, int32_t B, int32_t N, int32_t L_max, int32_t E,
+                                         spec_dtype_t dtype, void* stream) {
+  const sv::TreeCommitIO io{tokens, parents, sampled, cache_len, new_len, accepted_len, out_tokens, path, status};
+  sv::KvQPlan plan{};
+  bool empty = false;
+  const spec_status_t sc =
+      sv::validate_tree_commit_quantized(codes, scales, staging, io, P, B, N, L_max, E, dtype, &plan, &empty);
+  if (sc != SPEC_OK || empty) return sc;
+  (void)hipGetLastError();
+  const hipError_t e = sv::launch_tree_commit_quantized(codes, scales, staging, io, P, B, N, L_max, E,
+                                                        dtype == SPEC_BF16 ? 1 : 0, plan,
+                                                        static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
+}
+
 spec_status_t spec_read_stream_probe(const void* src, size_t bytes, void* sink, void* stream) {
   if (!src || !sink || bytes == 0 || bytes % 32768 != 0 || (uintptr_t)src % 16 != 0 || (uintptr_t)sink % 4 != 0)
     return SPEC_ERR_INVALID_ARG;

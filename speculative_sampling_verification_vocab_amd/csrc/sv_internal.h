@@ -7,6 +7,8 @@
 
 #include "sv_host.h"
 #include "sv_host_quant.h"
+#include "sv_host_sample.h"
+#include "sv_host_tree.h"
 
 namespace sv {
 
@@ -72,5 +74,21 @@ hipError_t launch_kv_read_quantized(const void* codes, const void* scales, const
 hipError_t launch_logprobs(const LogprobsShape& s, const LogprobsWorkspace& w, const void* logits,
                            const int32_t* tokens, int dtype, float temperature, float* logprobs, float* entropy,
                            int32_t* top_ids, float* top_logprobs, void* workspace, hipStream_t st);
+
+// Attention of a tree over the cache: one launch, and with plan.split > 1 the
+// join of the splits.
+hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, int N, int Hq, int Hkv, int D, int L,
+                                 float scale, int window, int sinks, int dtype, const AttnPlan& plan, void* workspace,
+                                 hipStream_t st);
+
+// Walk along a tree and commit of its path: one launch, or two when new_len is cache_len.
+hipError_t launch_tree_commit(void* cache, const void* staging, const TreeCommitIO& io, int P, int B, int N, int L,
+                              int E, int elem_bytes, const TreeCopyPlan& plan, hipStream_t st);
+hipError_t launch_tree_commit_quantized(void* codes, void* scales, const void* staging, const TreeCommitIO& io, int P,
+                                        int B, int N, int L, int E, int dtype, const KvQPlan& plan, hipStream_t st);
+
+// Tokens drawn with request settings (one launch).
+hipError_t launch_sample_tokens(const void* logits, const float* uniforms, int R, int V, int dtype,
+                                const SampleSettings& set, int32_t* tokens, hipStream_t st);
 
 }  // namespace sv

@@ -84,6 +84,7 @@ __device__ __forceinline__ uint2 quantize8(float (&x)[kPerLaneQ], int* byte) {
 // and the compiler makes one access of each of these.
 typedef uint32_t u32x4_any2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_any4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any1 __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 template <typename T> struct AnyVector;
 template <> struct AnyVector<uint16_t> { typedef u32x4_any2 type; };

@@ -1,0 +1,229 @@
+// Commit of a tree's path.  From the root (node 0) the walk goes on to the
+// first child whose token is the one that was drawn at the node, until there is
+// none: the drawn tokens along the path are the step's output, whatever the
+// drafts were, and the path's entries move from staging to the cache.
+//
+// The walk is one wave's, a node per lane: a ballot finds the child, so a path
+// of d nodes costs d ballots after three loads.  Every block walks for itself
+// (a few hundred nanoseconds beside loads that it must wait for anyway), so the
+// copy needs no launch before it; the entries of a path are scattered in
+// staging and contiguous in the cache.
+
+#include <type_traits>
+
+#include "sv_internal.h"
+#include "sv_quant.h"
+#include "sv_tree.h"
+
+namespace sv {
+
+namespace {
+
+struct TreeCommitArgs {
+  TreeCommitIO io;
+  int B, N, L;
+  uint32_t chunks;
+  // values
+  uint8_t* cache;          // [P][B][L][row_bytes]
+  const uint8_t* staging;  // [P][B][N][row_bytes]
+  int64_t row_bytes;
+  int units;
+  // 8-bit
+  uint8_t *codes, *scales;  // [P][B][L][E], [P][B][L][nb]
+  const void* in;           // [P][B][N][E]
+  int E, nb;
+};
+
+struct Walk {
+  int count;   // nodes of the path, 0 for a faulty sequence
+  int len;     // cache_len
+  int status;  // 0 committed, 1 no room, 2 faulty
+};
+
+// The walk of sequence b, by the 64 lanes of a wave; path[i] is its node i.
+// out: the lane writes what it knows of the outputs too.
+__device__ __forceinline__ Walk walk_tree(const TreeCommitArgs& a, int b, int lane, int* path, bool out) {
+  const size_t at = (size_t)b * a.N + lane;
+  const bool in = lane < a.N;
+  const int parent = in ? a.io.parents[at] : -2, token = in ? a.io.tokens[at] : 0, drawn = in ? a.io.sampled[at] : 0;
+  Walk w;
+  w.len = a.io.cache_len[b];
+  w.count = 0;
+  int mine = -1, emitted = -1;  // the path's node `lane`, and the token drawn there
+  bool fault = __builtin_amdgcn_readlane(parent, 0) != -1;
+  int cur = 0;
+  while (!fault) {
+    const int t = __builtin_amdgcn_readlane(drawn, cur);
+    if (t < 0) {
+      fault = true;
+      break;
+    }
+    if (lane == w.count) mine = cur, emitted = t;
+    ++w.count;
+    const uint64_t next = __ballot(in && lane > cur && parent == cur && token == t);
+    if (next == 0) break;
+    cur = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)next) - 1);
+  }
+  if (fault) w.count = 0, mine = -1, emitted = -1;
+  w.status = fault ? 2 : w.len < 0 || w.len > a.L - w.count ? 1 : 0;
+  if (path) path[lane] = mine;
+  if (out) {
+    if (in) {
+      a.io.out_tokens[at] = emitted;
+      if (a.io.path) a.io.path[at] = mine;
+    }
+    if (lane == 0) {
+      a.io.accepted_len[b] = w.count - 1;
+      if (a.io.status) a.io.status[b] = w.status;
+      a.io.new_len[b] = w.status == 0 ? w.len + w.count : w.len;
+    }
+  }
+  return w;
+}
+
+// Block (plane, sequence, chunk): the path's units, chunk by chunk of four per
+// thread.  out: the first block of a sequence writes its outputs.
+template <int kUnit>
+__global__ void __launch_bounds__(kBlock) tree_commit_kernel(TreeCommitArgs a, int out) {
+  __shared__ int path[kMaxNodes];
+  __shared__ int head[3];
+  const uint32_t pb = blockIdx.x / a.chunks, chunk = blockIdx.x - pb * a.chunks;
+  const int b = (int)(pb % (uint32_t)a.B);
+  if (threadIdx.x < kWave) {
+    const Walk w = walk_tree(a, b, threadIdx.x, path, out && chunk == 0 && pb < (uint32_t)a.B);
+    if (threadIdx.x == 0) head[0] = w.count, head[1] = w.len, head[2] = w.status;
+  }
+  __syncthreads();
+  if (head[2] != 0) return;
+  constexpr int kU = 4;
+  const int total = head[0] * a.units;
+  using U = typename std::conditional<kUnit == 16, u32x4, typename std::conditional<kUnit == 4, uint32_t, uint16_t>::type>::type;
+  const U* s = reinterpret_cast<const U*>(a.staging + (size_t)pb * a.N * (size_t)a.row_bytes);
+  U* d = reinterpret_cast<U*>(a.cache + ((size_t)pb * a.L + (size_t)head[1]) * (size_t)a.row_bytes);
+  for (int i0 = (int)chunk * kBlock * kU + threadIdx.x; i0 < total; i0 += (int)a.chunks * kBlock * kU) {
+    U v[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int i = i0 + k * kBlock;
+      if (i < total) {
+        const int r = i / a.units;
+        v[k] = s[(size_t)path[r] * a.units + (i - r * a.units)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (i0 + k * kBlock < total) d[i0 + k * kBlock] = v[k];
+  }
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kBlock) tree_commit_quantized_kernel(TreeCommitArgs a, int out) {
+  __shared__ int path[kMaxNodes];
+  __shared__ int head[3];
+  const uint32_t pb = blockIdx.x / a.chunks, chunk = blockIdx.x - pb * a.chunks;
+  const int b = (int)(pb % (uint32_t)a.B);
+  if (threadIdx.x < kWave) {
+    const Walk w = walk_tree(a, b, threadIdx.x, path, out && chunk == 0 && pb < (uint32_t)a.B);
+    if (threadIdx.x == 0) head[0] = w.count, head[1] = w.len, head[2] = w.status;
+  }
+  __syncthreads();
+  if (head[2] != 0) return;
+  constexpr int kU = 4, kPer = kBlock / kLanesPerBlock;
+  const int total = head[0] * a.nb;  // blocks of the format, 16 lanes each
+  const int sub = threadIdx.x % kLanesPerBlock;
+  const T* src = static_cast<const T*>(a.in) + (size_t)pb * (size_t)a.N * (size_t)a.E;
+  const size_t row0 = (size_t)pb * (size_t)a.L + (size_t)head[1];
+  for (int base = (int)chunk * kPer * kU; base < total; base += (int)a.chunks * kPer * kU) {
+    const int first = base + threadIdx.x / kLanesPerBlock;
+    float v[kU][kPerLaneQ];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (base + k * kPer >= total) break;
+      const int i = min(first + k * kPer, total - 1);
+      const int r = i / a.nb;
+      const int at = (i - r * a.nb) * kQuantBlock + sub * kPerLaneQ;
+      load8<T, kVec, false>(src + (size_t)path[r] * (size_t)a.E + at, a.E - at, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (base + k * kPer >= total) break;
+      const int i = first + k * kPer;
+      int sb;
+      const uint2 q = quantize8(v[k], &sb);
+      if (i >= total) continue;
+      const int r = i / a.nb, blk = i - r * a.nb;
+      const int at = blk * kQuantBlock + sub * kPerLaneQ;
+      store_codes<kVec>(a.codes + (row0 + (size_t)r) * (size_t)a.E + at, a.E - at, q);
+      if (sub == 0) a.scales[(row0 + (size_t)r) * (size_t)a.nb + blk] = (uint8_t)sb;
+    }
+  }
+}
+
+// The outputs alone: a wave per sequence.
+__global__ void __launch_bounds__(kBlock) tree_walk_kernel(TreeCommitArgs a) {
+  const int b = blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
+  if (b < a.B) walk_tree(a, b, threadIdx.x & (kWave - 1), nullptr, true);
+}
+
+hipError_t finish(const TreeCommitArgs& a, bool copied, hipStream_t st) {
+  if (copied) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.io.new_len != a.io.cache_len) return e;
+  }
+  hipLaunchKernelGGL(tree_walk_kernel, dim3(((unsigned)a.B + kWavesPerBlock - 1) / kWavesPerBlock), dim3(kBlock), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_tree_commit(void* cache, const void* staging, const TreeCommitIO& io, int P, int B, int N, int L,
+                              int E, int elem_bytes, const TreeCopyPlan& plan, hipStream_t st) {
+  TreeCommitArgs a{};
+  a.io = io;
+  a.B = B;
+  a.N = N;
+  a.L = L;
+  a.chunks = plan.chunks;
+  a.cache = static_cast<uint8_t*>(cache);
+  a.staging = static_cast<const uint8_t*>(staging);
+  a.row_bytes = (int64_t)E * elem_bytes;
+  a.units = plan.units;
+  const bool copies = plan.chunks > 0;
+  if (copies) {
+    const dim3 grid((unsigned)((size_t)P * (size_t)B * plan.chunks));
+    const int out = io.new_len != io.cache_len;
+    if (plan.unit_bytes == 16) hipLaunchKernelGGL(tree_commit_kernel<16>, grid, dim3(kBlock), 0, st, a, out);
+    else if (plan.unit_bytes == 4) hipLaunchKernelGGL(tree_commit_kernel<4>, grid, dim3(kBlock), 0, st, a, out);
+    else hipLaunchKernelGGL(tree_commit_kernel<2>, grid, dim3(kBlock), 0, st, a, out);
+  }
+  return finish(a, copies, st);
+}
+
+hipError_t launch_tree_commit_quantized(void* codes, void* scales, const void* staging, const TreeCommitIO& io, int P,
+                                        int B, int N, int L, int E, int dtype, const KvQPlan& plan, hipStream_t st) {
+  TreeCommitArgs a{};
+  a.io = io;
+  a.B = B;
+  a.N = N;
+  a.L = L;
+  a.chunks = plan.chunks;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = static_cast<uint8_t*>(scales);
+  a.in = staging;
+  a.E = E;
+  a.nb = plan.nb;
+  if (plan.copies) {
+    const dim3 grid((unsigned)((size_t)P * (size_t)B * plan.chunks));
+    const int out = io.new_len != io.cache_len;
+    if (dtype == 1) {
+      if (plan.vec) hipLaunchKernelGGL((tree_commit_quantized_kernel<uint16_t, true>), grid, dim3(kBlock), 0, st, a, out);
+      else hipLaunchKernelGGL((tree_commit_quantized_kernel<uint16_t, false>), grid, dim3(kBlock), 0, st, a, out);
+    } else {
+      if (plan.vec) hipLaunchKernelGGL((tree_commit_quantized_kernel<float, true>), grid, dim3(kBlock), 0, st, a, out);
+      else hipLaunchKernelGGL((tree_commit_quantized_kernel<float, false>), grid, dim3(kBlock), 0, st, a, out);
+    }
+  }
+  return finish(a, plan.copies, st);
+}
+
+}  // namespace sv
