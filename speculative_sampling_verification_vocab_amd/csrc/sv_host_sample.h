@@ -19,7 +19,8 @@ struct SampleSettings {
   Setting<float> top_p, min_p;
 };
 
-constexpr int kSampleThreads = 1024;  // a row's block
+constexpr int kSampleThreads = 1024;  // a row's block at most
+constexpr int kSampleWideRows = 256;  // up to so many rows, one per CU, the blocks have 16 waves, else eight
 
 inline spec_status_t validate_sample(const void* logits, const float* uniforms, int32_t R, int32_t V,
                                      spec_dtype_t dtype, const SampleSettings& set, const int32_t* tokens,

@@ -22,10 +22,16 @@ namespace sv {
 
 namespace {
 
-constexpr int kT = kSampleThreads;
-constexpr int kSWaves = kT / kWave;
 constexpr int kBins = 2048;    // bins of a digit, and chunks of a row
 constexpr int kChunk = 512;    // tokens of a chunk, times a factor for rows beyond kBins chunks
+constexpr int kLoadsT = 4;     // 16-byte vectors of a thread's piece of a segment
+constexpr int kList = 4096;    // candidates
+// Values by their upper 16 bits (sign, exponent, seven bits of the mantissa: a
+// bf16 value itself): 30 octaves of either sign and zero, in ascending order, and
+// bins for what lies outside.
+constexpr int kOctaves = 30, kOctave0 = 107;  // from 2^-20 to 2^10
+constexpr int kSide = kOctaves * 128, kTable = 2 * kSide + 1;
+constexpr int kTiny = kTable, kLow = kTable + 1, kHigh = kTable + 2, kOdd = 3;
 constexpr float kNegInf = -__builtin_inff();
 
 struct SampleArgs {
@@ -52,9 +58,8 @@ __device__ __forceinline__ float order_value(uint32_t k) {
 struct Weight {
   double top, s;  // max x, log2(e) / T
   int F;
-  __device__ __forceinline__ uint64_t operator()(float x) const {
-    const double a = ((double)x - top) * s;
-    if (!(a > -(double)(F + 2))) return 0;  // below half a unit
+  // 2^(a + e), a >= -1020.
+  static __device__ __forceinline__ double power(double a, int e) {
     const double n = __builtin_rint(a);
     const double t = (a - n) * 0.69314718055994530942;
     double y = 1.0 / 39916800.0;
@@ -69,7 +74,13 @@ struct Weight {
     y = __builtin_fma(y, t, 0.5);
     y = __builtin_fma(y, t, 1.0);
     y = __builtin_fma(y, t, 1.0);
-    const double v = __builtin_ldexp(y, (int)n + F) + 4503599627370496.0;  // 2^52: the sum's low bits are v
+    return __builtin_ldexp(y, (int)n + e);
+  }
+  __device__ __forceinline__ double exponent(float x) const { return ((double)x - top) * s; }
+  __device__ __forceinline__ uint64_t operator()(float x) const {
+    const double a = exponent(x);
+    if (!(a > -(double)(F + 2))) return 0;  // below half a unit
+    const double v = power(a, F) + 4503599627370496.0;  // 2^52: the sum's low bits are the power's nearest
     return (uint64_t)__double_as_longlong(v) - 0x4330000000000000ull;
   }
 };
@@ -81,12 +92,21 @@ struct Shared {
       uint32_t count[kBins];
       uint64_t mass[kBins];
     } bin;
-    uint64_t sum[kBins];  // of a row's chunks
+    struct {
+      uint64_t sum[kBins];   // of a row's chunks
+      uint32_t tie[kBins];   // and their tokens at the cut
+    };
+    uint64_t list[kList];    // candidates
+    uint32_t table[kTable + kOdd];
   };
-  uint64_t wave[kSWaves];
+  uint64_t wave[16];
   uint64_t found[4];
-  float top[kSWaves];
-  int bad;
+  uint64_t votes[2][16];
+  double tail[16];
+  float top[2][16];
+  uint64_t best;
+  alignas(16) uint32_t end[4];
+  int bad, count, cut;
 };
 
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
@@ -105,6 +125,7 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t v, int lane) {
 }
 
 // Sum over the block; every thread gets it.
+template <int kT>
 __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   v = wave_sum64(v);
   __syncthreads();
@@ -112,11 +133,12 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
   __syncthreads();
   uint64_t r = 0;
 #pragma unroll
-  for (int i = 0; i < kSWaves; ++i) r += sh.wave[i];
+  for (int i = 0; i < kT / kWave; ++i) r += sh.wave[i];
   return r;
 }
 
 // Sum of the threads before this one.
+template <int kT>
 __device__ __forceinline__ uint64_t block_before64(uint64_t v, Shared& sh) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const uint64_t up_to = wave_scan64(v, lane);
@@ -146,7 +168,7 @@ __device__ __forceinline__ void load_row(const T* row, int V, int id, float (&x)
 }
 
 // f(x, id) for every token, a vector per thread at a time.
-template <typename T, typename Fn>
+template <typename T, int kT, typename Fn>
 __device__ __forceinline__ void for_row(const T* row, int V, Fn f) {
   constexpr int n = Elem<T>::kVec;
   for (int id = threadIdx.x * n; id < V; id += kT * n) {
@@ -155,88 +177,6 @@ __device__ __forceinline__ void for_row(const T* row, int V, Fn f) {
 #pragma unroll
     for (int i = 0; i < n; ++i) f(x[i], id + i);
   }
-}
-
-// Sums of f(x, id) over the row's chunks of kChunk * factor tokens, in sh.sum, and over the row.
-template <typename T, typename Fn>
-__device__ __forceinline__ uint64_t chunk_sums(const T* row, int V, int factor, Shared& sh, Fn f) {
-  constexpr int n = Elem<T>::kVec;
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const int size = kChunk * factor, chunks = (V + size - 1) / size;
-  __syncthreads();
-  uint64_t total = 0;
-  for (int c = w; c < chunks; c += kSWaves) {
-    uint64_t s = 0;
-    const int end = min((long long)V, (long long)(c + 1) * size);
-    for (int id = c * size + lane * n; id < end; id += kWave * n) {
-      float x[n];
-      load_row(row, V, id, x);
-#pragma unroll
-      for (int i = 0; i < n; ++i) s += id + i < V ? f(x[i], id + i) : 0;
-    }
-    s = wave_sum64(s);
-    if (lane == 0) sh.sum[c] = s;
-    total += s;
-  }
-  return block_sum64(lane == 0 ? total : 0, sh);
-}
-
-// The smallest token up to which f sums to more than `target` (less than the row's sum), by the chunks' sums.
-template <typename T, typename Fn>
-__device__ __forceinline__ int locate(const T* row, int V, int factor, uint64_t target, Shared& sh, Fn f) {
-  constexpr int n = Elem<T>::kVec;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int size = kChunk * factor, chunks = (V + size - 1) / size;
-  uint64_t own[kBins / kT], mine = 0;
-#pragma unroll
-  for (int i = 0; i < kBins / kT; ++i) {
-    const int c = threadIdx.x * (kBins / kT) + i;
-    own[i] = c < chunks ? sh.sum[c] : 0;
-    mine += own[i];
-  }
-  uint64_t before = block_before64(mine, sh);
-#pragma unroll
-  for (int i = 0; i < kBins / kT; ++i) {
-    if (before <= target && target < before + own[i]) {
-      sh.found[0] = threadIdx.x * (kBins / kT) + i;
-      sh.found[1] = before;
-    }
-    before += own[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < kWave) {
-    const int c = (int)sh.found[0];
-    uint64_t at = sh.found[1];
-    for (int id0 = c * size; id0 < V; id0 += kWave * n) {
-      const int id = id0 + lane * n;
-      float x[n];
-      uint64_t v[n], s = 0;
-      load_row(row, V, min(id, V - 1), x);
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        v[i] = id + i < V ? f(x[i], id + i) : 0;
-        s += v[i];
-      }
-      const uint64_t up_to = at + wave_scan64(s, lane);
-      const uint64_t hit = __ballot(up_to > target);
-      if (hit != 0) {
-        if (lane == __ffsll((unsigned long long)hit) - 1) {
-          uint64_t y = up_to - s;
-          int token = id;
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            y += v[i];
-            if (y <= target) token = id + i + 1;
-          }
-          sh.found[2] = token;
-        }
-        break;
-      }
-      at = __shfl((unsigned long long)up_to, kWave - 1);
-    }
-  }
-  __syncthreads();
-  return (int)sh.found[2];
 }
 
 // A cut in the ranking: tokens above `key`, and the first `ties` by id at it.
@@ -249,7 +189,7 @@ struct Cut {
 // The cut at which the ranked counts (by_mass false) or weights reach target.  Three
 // passes over the row, each a digit of the keys that share the digits before.
 // share >= 0: the target is that share of the row's weight, known after the first.
-template <typename T>
+template <typename T, int kT>
 __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weight, bool by_mass, uint64_t target,
                                         double share, Shared& sh) {
   uint32_t prefix = 0;
@@ -261,7 +201,7 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kT) sh.bin.count[i] = 0, sh.bin.mass[i] = 0;
     __syncthreads();
-    for_row(row, V, [&](float x, int id) {
+    for_row<T, kT>(row, V, [&](float x, int id) {
       const uint32_t k = order_bits(x);
       if (id < V && (level == 0 || k >> (shift + (level == 1 ? 11 : 10)) == prefix)) {
         const uint32_t b = k >> shift & (digits - 1);
@@ -283,10 +223,10 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
       m_all += m[i];
     }
     if (level == 0 && share >= 0.0) {
-      const double t = __builtin_ceil(share * (double)block_sum64(m_all, sh));
+      const double t = __builtin_ceil(share * (double)block_sum64<kT>(m_all, sh));
       target = t < 1.0 ? 1 : (uint64_t)t;
     }
-    uint64_t n_before = above_n + block_before64(n_all, sh), m_before = above_m + block_before64(m_all, sh);
+    uint64_t n_before = above_n + block_before64<kT>(n_all, sh), m_before = above_m + block_before64<kT>(m_all, sh);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint64_t lo = by_mass ? m_before : n_before, hi = lo + (by_mass ? m[i] : n[i]);
@@ -313,10 +253,248 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
   return c;
 }
 
+// ---- the draw -------------------------------------------------------------------
+
+// The token of a row that a cut leaves: one pass for the chunks' weights above the cut and
+// their ties at it, a scan, and one chunk again.
+template <typename T, int kT>
+__device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
+                                    Shared& sh) {
+  constexpr int n = Elem<T>::kVec, kPer = kBins / kT;
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int size = kChunk * factor, chunks = (V + size - 1) / size;
+  const float value = order_value(cut.key);
+  const uint64_t at_cut = cut.key == 0 ? 0 : weight(value);
+  __syncthreads();
+  for (int c = w; c < chunks; c += kT / kWave) {
+    uint64_t s = 0;
+    uint32_t ties = 0;
+    const int end = min((long long)V, (long long)(c + 1) * size);
+    for (int id = c * size + lane * n; id < end; id += kWave * n) {
+      float x[n];
+      load_row(row, V, id, x);
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const uint32_t key = order_bits(x[i]);
+        const bool more = key > cut.key && x[i] > kNegInf;
+        if (__any(more)) s += more ? weight(x[i]) : 0;
+        ties += key == cut.key && id + i < V ? 1 : 0;
+        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+      }
+    }
+    s = wave_sum64(s);
+    ties = (uint32_t)wave_sum64(ties);
+    if (lane == 0) sh.sum[c] = s, sh.tie[c] = ties;
+  }
+  __syncthreads();
+  // Thread t has the chunks kPer t and on; ties are kept up to cut.ties of them.
+  uint64_t own[kPer], tied[kPer], ties = 0, sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = (int)threadIdx.x * kPer + i;
+    own[i] = c < chunks ? sh.sum[c] : 0;
+    tied[i] = c < chunks ? sh.tie[c] : 0;
+    ties += tied[i];
+  }
+  uint64_t ties_before = block_before64<kT>(ties, sh);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint64_t room = cut.ties > ties_before ? cut.ties - ties_before : 0;
+    own[i] += (tied[i] < room ? tied[i] : room) * at_cut;
+    ties_before += tied[i];
+    sum += own[i];
+  }
+  ties_before -= ties;
+  const uint64_t total = block_sum64<kT>(sum, sh);
+  const uint64_t target = (uint64_t)((double)u * (double)total);
+  uint64_t before = block_before64<kT>(sum, sh);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (before <= target && target < before + own[i]) {
+      sh.found[0] = threadIdx.x * kPer + i;
+      sh.found[1] = before;
+      sh.found[2] = ties_before;
+    }
+    before += own[i];
+    ties_before += tied[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    uint64_t at = sh.found[1], tie_at = sh.found[2];
+    for (int id0 = (int)sh.found[0] * size; id0 < V; id0 += kWave * n) {
+      const int id = id0 + lane * n;
+      float x[n];
+      load_row(row, V, min(id, V - 1), x);
+      uint64_t v[n], t = 0, s = 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) t += id + i < V && order_bits(x[i]) == cut.key ? 1 : 0;
+      const uint64_t ties_to = tie_at + wave_scan64(t, lane);
+      uint64_t rank = ties_to - t;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const uint32_t key = order_bits(x[i]);
+        const bool in = id + i < V;
+        v[i] = in && key > cut.key ? weight(x[i]) : in && key == cut.key && rank++ < cut.ties ? at_cut : 0;
+        s += v[i];
+        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+      }
+      const uint64_t up_to = at + wave_scan64(s, lane);
+      const uint64_t hit = __ballot(up_to > target);
+      if (hit != 0) {
+        if (lane == __ffsll((unsigned long long)hit) - 1) {
+          uint64_t y = up_to - s;
+          int token = id;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            y += v[i];
+            if (y <= target) token = id + i + 1;
+          }
+          sh.found[3] = token;
+        }
+        break;
+      }
+      at = __shfl((unsigned long long)up_to, kWave - 1);
+      tie_at = __shfl((unsigned long long)ties_to, kWave - 1);
+    }
+  }
+  __syncthreads();
+  return (int)sh.found[3];
+}
+
+// ---- the table ------------------------------------------------------------------
+
+// Bin of a value by its upper 16 bits.
+__device__ __forceinline__ int table_bin(uint32_t b) {
+  const int m = (int)(b & 0x7fffu), t = m - kOctave0 * 128;
+  const bool minus = (b & 0x8000u) != 0;
+  const int odd = m == 0 ? kSide : t < 0 ? kTiny : minus ? kLow : kHigh;
+  return (uint32_t)t < (uint32_t)kSide ? minus ? kSide - 1 - t : kSide + 1 + t : odd;
+}
+
+// The upper 16 bits that a bin stands for.
+__device__ __forceinline__ uint32_t table_value(int bin) {
+  return bin == kSide ? 0u : bin > kSide ? (uint32_t)(bin - kSide - 1 + kOctave0 * 128)
+                                         : (uint32_t)(kSide - 1 - bin + kOctave0 * 128) | 0x8000u;
+}
+
+// A border in the table: its bin, what lies above it, and (by count or weight) the row's total.
+struct Border {
+  int bin;
+  uint64_t above_n, above_m, total_m;
+};
+
+// The bin, from the highest down, at which counts (by_mass false) or weights reach target, or with share >=
+// 0 that share of the total weight.  count(bin) and mass(bin, count) give a bin's; at most `target` must be there.
+template <int kT, typename Mass>
+__device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, double share, Shared& sh, Mass mass) {
+  constexpr int kPer = (kTable + kT - 1) / kT;
+  uint64_t n = 0, m = 0;
+  const int first = kTable - 1 - (int)threadIdx.x * kPer;
+#pragma unroll 1
+  for (int i = 0; i < kPer; ++i) {
+    const int bin = first - i;
+    const uint32_t c = bin >= 0 ? sh.table[bin] : 0;
+    n += c;
+    m += c != 0 ? mass(bin, c) : 0;
+  }
+  Border b;
+  b.total_m = block_sum64<kT>(m, sh);
+  if (share >= 0.0) {
+    const double t = __builtin_ceil(share * (double)b.total_m);
+    target = t < 1.0 ? 1 : (uint64_t)t;
+  }
+  uint64_t n_before = block_before64<kT>(n, sh), m_before = block_before64<kT>(m, sh);
+  const uint64_t lo = by_mass ? m_before : n_before, hi = lo + (by_mass ? m : n);
+  if (lo < target && target <= hi) {
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+      const int bin = first - i;
+      const uint32_t c = bin >= 0 ? sh.table[bin] : 0;
+      const uint64_t w = c != 0 ? mass(bin, c) : 0;
+      if ((by_mass ? m_before + w : n_before + c) >= target) {
+        sh.found[0] = bin;
+        sh.found[1] = n_before;
+        sh.found[2] = m_before;
+        break;
+      }
+      n_before += c;
+      m_before += w;
+    }
+  }
+  __syncthreads();
+  b.bin = (int)sh.found[0];
+  b.above_n = sh.found[1];
+  b.above_m = sh.found[2];
+  __syncthreads();
+  return b;
+}
+
+// ---- candidates -----------------------------------------------------------------
+
+// The largest 16-bit prefix p of ordered bits with at least k threads whose `own` has a prefix >= p (0
+// if there are fewer than k).  Two bits at a time.
+template <int kT>
+__device__ __forceinline__ uint32_t kth_prefix(uint32_t own, uint32_t k, Shared& sh) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  own >>= 16;
+  uint32_t p = 0;
+#pragma unroll 1
+  for (int shift = 14; shift >= 0; shift -= 2) {
+    uint64_t votes = 0;
+#pragma unroll
+    for (int i = 1; i <= 3; ++i)
+      votes |= (uint64_t)__popcll(__ballot(own >= (p | (uint32_t)i << shift))) << (16 * (i - 1));
+    uint64_t* at = sh.votes[shift >> 1 & 1];
+    if (lane == 0) at[w] = votes;
+    __syncthreads();
+    votes = 0;
+#pragma unroll
+    for (int i = 0; i < kT / kWave; ++i) votes += at[i];
+#pragma unroll
+    for (int i = 3; i >= 1; --i)
+      if ((votes >> (16 * (i - 1)) & 0xffff) >= k) {
+        p |= (uint32_t)i << shift;
+        break;
+      }
+  }
+  return p;
+}
+
+// The list's first n (a power of two) in ascending order.
+template <int kT>
+__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
+  for (int size = 2; size <= n; size *= 2)
+    for (int step = size / 2; step > 0; step /= 2) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n / 2; i += kT) {
+        const int lo = (i & ~(step - 1)) * 2 | (i & (step - 1)), hi = lo | step;
+        const uint64_t x = list[lo], y = list[hi];
+        if ((x > y) == ((lo & size) == 0)) list[lo] = y, list[hi] = x;
+      }
+    }
+  __syncthreads();
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kT) sample_tokens_kernel(SampleArgs a) {
+__device__ __forceinline__ T ninf_of() {
+  if constexpr (sizeof(T) == 2) return 0xff80;
+  else return kNegInf;
+}
+
+template <typename T>
+__device__ __forceinline__ float raw_max(const u32x4 (&raw)[kLoadsT], int v) {
+  constexpr int n = Elem<T>::kVec;
+  float m = raw_elem<T>(raw, v * n);
+#pragma unroll
+  for (int i = 1; i < n; ++i) m = fmaxf(m, raw_elem<T>(raw, v * n + i));
+  return m;
+}
+
+template <typename T, int kT>
+__global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
+  constexpr int V8 = Elem<T>::kVec, kWaves = kT / kWave;
   __shared__ Shared sh;
-  const int r = blockIdx.x, V = a.V;
+  const int r = blockIdx.x, V = a.V, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * (size_t)V;
   const float temperature = a.set.temperature.rows ? a.set.temperature.rows[r] : a.set.temperature.all;
   const int k = a.set.top_k.rows ? a.set.top_k.rows[r] : a.set.top_k.all;
@@ -324,39 +502,158 @@ __global__ void __launch_bounds__(kT) sample_tokens_kernel(SampleArgs a) {
   const float m = a.set.min_p.rows ? a.set.min_p.rows[r] : a.set.min_p.all;
   const float u = a.uniforms[r];
   const int factor = (int)(((long long)V + (long long)kChunk * kBins - 1) / ((long long)kChunk * kBins));
+  const bool greedy = temperature == 0.0f, by_k = k >= 1 && k < V, by_p = p < 1.0f, by_m = m > 0.0f;
+  const double s64 = 1.4426950408889634074 / (double)temperature;
+  // Few tokens and min-p alone: what a cut can keep is known while the row is read, and listed.  Other cuts
+  // need the row's values first, in a table.
+  const bool lists = !greedy && (by_k ? k <= kT : by_m && !by_p);
+  const bool tables = !greedy && (by_k ? k > kT : by_p);
+  const double span_m = by_m ? (double)temperature * log((double)fminf(m, 1.0f)) : 0.0;
+  // The least float at or above the min-p cut.
+  auto least_kept = [&](float top) {
+    const double least = (double)top + span_m;
+    const float f = (float)least;
+    return (double)f < least ? order_value(order_bits(f) + 1) : f;
+  };
 
-  if (threadIdx.x == 0) sh.bad = 0, sh.found[0] = sh.found[1] = sh.found[2] = 0;
+  if (threadIdx.x == 0) sh.bad = sh.count = 0, sh.best = ~0ull, sh.found[0] = sh.found[1] = sh.found[2] = sh.found[3] = 0;
+  if (tables)
+    for (int i = threadIdx.x; i < kTable + kOdd; i += kT) sh.table[i] = 0;
+  float top = kNegInf, bound = kNegInf, largest_own = kNegInf;
+  uint32_t largest = 0;  // magnitude bits
+  double tail = 0.0;
+  // The row's last vector, where it is not whole, with -inf behind its end.
+  constexpr uint32_t kNinf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  if (threadIdx.x < V8) {
+    const int id = V / V8 * V8 + (int)threadIdx.x;
+    reinterpret_cast<T*>(sh.end)[threadIdx.x] = id < V ? row[id] : ninf_of<T>();
+  }
   __syncthreads();
-  float top = kNegInf;
-  bool bad = false;
-  for_row(row, V, [&](float x, int) {
-    top = fmaxf(top, x);
-    bad |= x != x;
-  });
+  u32x4 next[kLoadsT];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int v = 0; v < kLoadsT; ++v) {
+      const int id = base + (v * kT + (int)threadIdx.x) * V8;
+      if (id + V8 <= V) next[v] = load16<T, false, false>(row + id);
+      else next[v] = id < V ? *reinterpret_cast<const u32x4*>(sh.end) : u32x4{kNinf, kNinf, kNinf, kNinf};
+    }
+  };
+  constexpr int kSegment = kT * V8 * kLoadsT;
+  // Tokens at or above the bound to the list.
+  auto list_those = [&](const u32x4 (&raw)[kLoadsT], int v, int base) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < V8; ++i) {
+      const float x = raw_elem<T>(raw, v * V8 + i);
+      hits |= x >= bound && x > kNegInf ? 1u << i : 0u;
+    }
+    if (hits == 0) return;
+    int at = atomicAdd(&sh.count, __popc(hits));
+#pragma unroll
+    for (int i = 0; i < V8; ++i)
+      if (hits >> i & 1) {
+        if (at < kList)
+          sh.list[at] = (uint64_t)~order_bits(raw_elem<T>(raw, v * V8 + i)) << 32 |
+                        (uint32_t)(base + (v * kT + (int)threadIdx.x) * V8 + i);
+        ++at;
+      }
+  };
+  fetch(0);
+  int turn = 0, segment = 0;
+#pragma unroll 1
+  for (int base = 0; base < V; base += kSegment, turn ^= 1, ++segment) {
+    u32x4 raw[kLoadsT];
+    float most[kLoadsT], own = kNegInf;
+#pragma unroll
+    for (int v = 0; v < kLoadsT; ++v) raw[v] = next[v];
+    if (V - base > kSegment) fetch(base + kSegment);
+#pragma unroll
+    for (int v = 0; v < kLoadsT; ++v) {
+      most[v] = raw_elem<T>(raw, v * V8);
+#pragma unroll
+      for (int i = 1; i < V8; ++i) most[v] = fmaxf(most[v], raw_elem<T>(raw, v * V8 + i));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (sizeof(T) == 2) {
+          typedef uint16_t halves __attribute__((ext_vector_type(2)));
+          largest = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(halves, largest),
+                                                                           __builtin_bit_cast(halves, raw[v][q] & 0x7fff7fffu)));
+        } else {
+          largest = max(largest, raw[v][q] & 0x7fffffffu);
+        }
+      }
+      own = fmaxf(own, most[v]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[v][q]));  // unpacked again where they are used again: registers
+    }
+    if (!lists && !greedy) top = fmaxf(top, own);  // of the thread; the others' follow behind the loop
+    if (tables) {
+#pragma unroll
+      for (int v = 0; v < kLoadsT; ++v) {
+        const int id = base + (v * kT + (int)threadIdx.x) * V8;
+        if (id >= V) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (sizeof(T) == 2) {
+            atomicAdd(&sh.table[table_bin(raw[v][q] & 0xffffu)], 1u);
+            atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
+          } else {
+            const uint32_t b = raw[v][q];
+            // the least values that are not zero are no zeros, whatever their upper bits
+            atomicAdd(&sh.table[table_bin(b >> 16 | ((b & 0x7fffffffu) - 1u < 0xffffu ? 1u : 0u))], 1u);
+          }
+        }
+      }
+      continue;
+    }
+    if (!lists && !greedy) continue;
+    const float mine = wave_max(own);
+    if (lane == 0) sh.top[turn][wave] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sh.top[turn][i]);
+    if (top == kNegInf) continue;
+    if (greedy) {
+      // The lowest id of the largest value: the least of (value's complement, id).
+      if (own == top) {
+        int id = 0;
+#pragma unroll
+        for (int v = kLoadsT - 1; v >= 0; --v)
+#pragma unroll
+          for (int i = V8 - 1; i >= 0; --i)
+            id = raw_elem<T>(raw, v * V8 + i) == top ? base + (v * kT + (int)threadIdx.x) * V8 + i : id;
+        atomicMin((unsigned long long*)&sh.best, (unsigned long long)~order_bits(top) << 32 | (uint32_t)id);
+      }
+    } else if (lists) {
+      // k threads' largest so far are k tokens of the row; taken anew when as much again was read.
+      largest_own = fmaxf(largest_own, own);
+      if (by_k && (segment & (segment + 1)) == 0)
+        bound = fmaxf(bound, order_value(max(kth_prefix<kT>(order_bits(largest_own), (uint32_t)k, sh), 0x80u) << 16));
+      if (by_m && !(by_k && by_p)) bound = fmaxf(bound, least_kept(top));  // top-p of the top k: all of their weight
+#pragma unroll
+      for (int v = 0; v < kLoadsT; ++v)
+        if (__any(most[v] >= bound)) list_those(raw, v, base);
+    }
+  }
+  // A fault of the row or of its settings: comparisons that NaN fails.
+  const bool nan = sizeof(T) == 2 ? (largest & 0xffffu) > 0x7f80u || largest >> 16 > 0x7f80u : largest > 0x7f800000u;
+  if (nan) sh.bad = 1;
   top = wave_max(top);
-  if ((threadIdx.x & (kWave - 1)) == 0) sh.top[threadIdx.x / kWave] = top;
-  if (bad) sh.bad = 1;
+  if (lane == 0) sh.top[turn][wave] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSWaves; ++i) top = fmaxf(top, sh.top[i]);
-  // A fault of the row or of its settings: comparisons that NaN fails.
+  for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sh.top[turn][i]);
   if (sh.bad || !(fabsf(top) < __builtin_inff()) || !(temperature >= 0.0f && temperature < __builtin_inff()) || p != p ||
       m != m || !(u >= 0.0f && u < 1.0f)) {
     if (threadIdx.x == 0) a.tokens[r] = -1;
     return;
   }
-  if (temperature == 0.0f) {
-    auto is_top = [&](float x, int) -> uint64_t { return x == top; };
-    chunk_sums(row, V, factor, sh, is_top);
-    const int token = locate(row, V, factor, 0, sh, is_top);
-    if (threadIdx.x == 0) a.tokens[r] = token;
+  if (greedy) {
+    if (threadIdx.x == 0) a.tokens[r] = (int)(uint32_t)sh.best;
     return;
   }
-  Weight weight;
-  weight.top = top;
-  weight.s = 1.4426950408889634074 / (double)temperature;
-  weight.F = a.F;
-  const bool by_k = k >= 1 && k < V, by_p = p < 1.0f, by_m = m > 0.0f;
+  const Weight weight{(double)top, s64, a.F};
+  const float least = by_m ? least_kept(top) : kNegInf;
   Cut cut;
   cut.key = 0;
   cut.ties = ~0ull;
@@ -364,39 +661,200 @@ __global__ void __launch_bounds__(kT) sample_tokens_kernel(SampleArgs a) {
     if (c.key > cut.key) cut = c;
     else if (c.key == cut.key && c.ties < cut.ties) cut.ties = c.ties;
   };
+  bool done = !tables && !lists, listed = lists;
+  if (tables) {
+    // Values outside the table that have weight, or that a cut may meet, leave the row to its digits.
+    const bool weightless = top > -1024.0f && weight(-1024.0f) == 0;
+    const bool plain = sh.table[kHigh] == 0 && sh.table[kTiny] == 0 && (sh.table[kLow] == 0 || weightless) &&
+                       (!by_k || (uint64_t)k <= (uint64_t)V - sh.table[kLow]);
+    if (plain && sizeof(T) == 2) {
+      // A bin is a value: the cuts are known.
+      auto mass = [&](int bin, uint32_t c) { return (uint64_t)c * weight(__uint_as_float(table_value(bin) << 16)); };
+      uint64_t all = 0;
+      if (by_k) {
+        const Border b = find_border<kT>(false, (uint64_t)k, -1.0, sh, mass);
+        Cut c;
+        const float x = __uint_as_float(table_value(b.bin) << 16);
+        c.key = order_bits(x);
+        c.ties = (uint64_t)k - b.above_n;
+        all = c.mass = b.above_m + c.ties * weight(x);
+        narrow(c);
+      }
+      if (by_p) {
+        const double t = __builtin_ceil((double)p * (double)all);
+        const Border b = find_border<kT>(true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh, mass);
+        Cut c;
+        const float x = __uint_as_float(table_value(b.bin) << 16);
+        const uint64_t w = weight(x);
+        const double tt = by_k ? t : __builtin_ceil((p > 0.0f ? (double)p : 0.0) * (double)b.total_m);
+        const uint64_t goal = tt < 1.0 ? 1 : (uint64_t)tt;
+        c.key = order_bits(x);
+        c.ties = (goal - b.above_m + w - 1) / w;
+        c.mass = 0;
+        narrow(c);
+      }
+      done = true;
+    } else if (plain) {
+      // A bin's values share 16 bits.  Down to which bin the cut can lie: where the least weight that the bins above can
+      // have reaches the share of the most that the row can.
+      auto edge = [&](int bin, bool far) {
+        return __uint_as_float(table_value(bin) << 16 | ((bin > kSide) == far && bin != kSide ? 0xffffu : 0u));
+      };
+      int bin;
+      uint64_t count;
+      if (by_k) {
+        const Border b = find_border<kT>(false, (uint64_t)k, -1.0, sh, [](int, uint32_t) { return (uint64_t)0; });
+        bin = b.bin;
+        count = b.above_n + sh.table[bin];
+      } else {
+        const Border hi = find_border<kT>(true, 1, -1.0, sh, [&](int bin, uint32_t c) { return (uint64_t)c * weight(edge(bin, true)); });
+        const double t = __builtin_ceil((p > 0.0f ? (double)p : 0.0) * (double)hi.total_m);
+        const uint64_t goal = t < 1.0 ? 1 : (uint64_t)t;
+        if (threadIdx.x == 0) sh.found[0] = 0, sh.found[1] = ~0ull >> 1;
+        __syncthreads();
+        const Border b = find_border<kT>(true, goal, -1.0, sh, [&](int bin, uint32_t c) { return (uint64_t)c * weight(edge(bin, false)); });
+        bin = b.bin;
+        count = b.above_n + sh.table[bin];
+      }
+      __syncthreads();
+      if (count <= kList) {
+        listed = true;
+        bound = edge(bin, false);
+        Weight w{(double)top, s64, 0};
+        fetch(0);
+#pragma unroll 1
+        for (int base = 0; base < V; base += kSegment) {
+          u32x4 raw[kLoadsT];
+#pragma unroll
+          for (int v = 0; v < kLoadsT; ++v) raw[v] = next[v];
+          if (V - base > kSegment) fetch(base + kSegment);
+#pragma unroll
+          for (int v = 0; v < kLoadsT; ++v) {
+            if (__any(raw_max<T>(raw, v) >= bound)) list_those(raw, v, base);
+            if (!by_k) {
+#pragma unroll
+              for (int i = 0; i < V8; ++i) {
+                const float x = raw_elem<T>(raw, v * V8 + i);
+                const double e = w.exponent(x);
+                tail += x < bound && e > -70.0 ? Weight::power(fmax(e, -70.0), 0) : 0.0;
+                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+  }
+  const int n = sh.count;
+  if (listed && n <= kList) {
+    // Ranked: the bits' complements ascend where the logits descend.
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + (int)threadIdx.x; i < size; i += kT) sh.list[i] = ~0ull;
+    sort_list<kT>(sh.list, size);
+    const int per = (size + kT - 1) / kT;  // 8 at most
+    constexpr int kPer = kList / kT;
+    uint64_t own[kPer], sum = 0;
+    float value[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (int)threadIdx.x * per + i;
+      const uint64_t e = i < per && at < n ? sh.list[at] : ~0ull;
+      value[i] = e == ~0ull ? kNegInf : order_value(~(uint32_t)(e >> 32));
+      own[i] = e == ~0ull ? 0 : weight(value[i]);
+      sum += own[i];
+      __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
+    }
+    double all_tail = wave_sum(tail);
+    if (lane == 0) sh.tail[wave] = all_tail;
+    if (threadIdx.x == 0) sh.cut = n, sh.found[0] = 0;
+    const uint64_t before = block_before64<kT>(sum, sh);
+    uint64_t up_to = before;
+    const int nk = by_k ? min(k, n) : n;
+    if (by_k && by_p) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        up_to += own[i];
+        if (i < per && (int)threadIdx.x * per + i == nk - 1) sh.found[0] = up_to;
+      }
+    } else if (by_p) {
+      all_tail = 0.0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) all_tail += sh.tail[i];
+      if (threadIdx.x == kT - 1) sh.found[0] = before + sum + (uint64_t)__builtin_rint(__builtin_ldexp(all_tail, a.F));
+    }
+    __syncthreads();
+    const double share = __builtin_ceil((double)fmaxf(p, 0.0f) * (double)sh.found[0]);
+    const uint64_t target = share < 1.0 ? 1 : (uint64_t)share;
+    // The first index that is not kept.
+    up_to = before;
+    int mine = nk;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (int)threadIdx.x * per + i;
+      up_to += own[i];
+      if (i >= per || at >= n) continue;
+      if (by_p && up_to >= target) mine = min(mine, at + 1);
+      if (by_m && value[i] < least) mine = min(mine, at);
+    }
+    mine = wave_min(mine);
+    if (lane == 0) atomicMin(&sh.cut, mine);
+    __syncthreads();
+    const int kept = sh.cut;
+    {
+      // The kept ones by id.
+      __syncthreads();
+      size = 2;
+      while (size < kept) size *= 2;
+      for (int i = threadIdx.x; i < size; i += kT) {
+        const uint64_t e = sh.list[i];
+        sh.list[i] = i < kept ? e << 32 | e >> 32 : ~0ull;
+      }
+      sort_list<kT>(sh.list, size);
+      const int per = (size + kT - 1) / kT;
+      sum = 0;
+      uint32_t id[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = (int)threadIdx.x * per + i;
+        const uint64_t e = i < per && at < kept ? sh.list[at] : ~0ull;
+        id[i] = (uint32_t)(e >> 32);
+        own[i] = e == ~0ull ? 0 : weight(order_value(~(uint32_t)e));
+        sum += own[i];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const uint64_t total = block_sum64<kT>(sum, sh);
+      const uint64_t goal = (uint64_t)((double)u * (double)total);
+      uint64_t from = block_before64<kT>(sum, sh);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (from <= goal && goal < from + own[i]) a.tokens[r] = (int)id[i];
+        from += own[i];
+      }
+      return;
+    }
+  }
+
+  // Cuts that neither the list nor the table gave: digit by digit.
   uint64_t mass = 0;
-  if (by_k) {
-    const Cut c = find_cut(row, V, weight, false, (uint64_t)k, -1.0, sh);
+  if (by_k && !done) {
+    const Cut c = find_cut<T, kT>(row, V, weight, false, (uint64_t)k, -1.0, sh);
     mass = c.mass;
     narrow(c);
   }
-  if (by_p) {
+  if (by_p && !done) {
     const double t = by_k ? __builtin_ceil((double)p * (double)mass) : 0.0;
-    narrow(find_cut(row, V, weight, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh));
+    narrow(find_cut<T, kT>(row, V, weight, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh));
   }
   if (by_m) {
-    // w >= m: x >= max + T ln m, as the least float that is.
-    const double least = (double)top + (double)temperature * log((double)fminf(m, 1.0f));
-    float f = (float)least;
-    if ((double)f < least) f = order_value(order_bits(f) + 1);
     Cut c;
-    c.key = order_bits(f);
+    c.key = order_bits(least);
     c.ties = ~0ull;
     c.mass = 0;
     narrow(c);
   }
-  int last_tie = V;  // tokens at the cut's key are kept up to this one
-  if (cut.ties != ~0ull) {
-    auto tie = [&](float x, int) -> uint64_t { return order_bits(x) == cut.key; };
-    const uint64_t n = chunk_sums(row, V, factor, sh, tie);
-    if (cut.ties < n) last_tie = locate(row, V, factor, cut.ties - 1, sh, tie);
-  }
-  auto kept = [&](float x, int id) -> uint64_t {
-    const uint32_t key = order_bits(x);
-    return key > cut.key || (key == cut.key && id <= last_tie) ? weight(x) : 0;
-  };
-  const uint64_t total = chunk_sums(row, V, factor, sh, kept);
-  const int token = locate(row, V, factor, (uint64_t)((double)u * (double)total), sh, kept);
+  const int token = draw<T, kT>(row, V, factor, weight, cut, u, sh);
   if (threadIdx.x == 0) a.tokens[r] = token;
 }
 
@@ -413,8 +871,14 @@ hipError_t launch_sample_tokens(const void* logits, const float* uniforms, int R
   int bits = 0;
   while ((1ll << bits) < V) ++bits;
   a.F = 62 - bits < 50 ? 62 - bits : 50;
-  if (dtype == 1) hipLaunchKernelGGL(sample_tokens_kernel<uint16_t>, dim3((unsigned)R), dim3(kT), 0, st, a);
-  else hipLaunchKernelGGL(sample_tokens_kernel<float>, dim3((unsigned)R), dim3(kT), 0, st, a);
+  const dim3 grid((unsigned)R);
+  if (R <= kSampleWideRows) {
+    if (dtype == 1) hipLaunchKernelGGL((sample_tokens_kernel<uint16_t, 1024>), grid, dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL((sample_tokens_kernel<float, 1024>), grid, dim3(1024), 0, st, a);
+  } else {
+    if (dtype == 1) hipLaunchKernelGGL((sample_tokens_kernel<uint16_t, 512>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((sample_tokens_kernel<float, 512>), grid, dim3(512), 0, st, a);
+  }
   return hipGetLastError();
 }
 
