@@ -23,15 +23,14 @@ namespace sv {
 namespace {
 
 constexpr int kBins = 2048;    // bins of a digit, and chunks of a row
-constexpr int kChunk = 512;    // tokens of a chunk, times a factor for rows beyond kBins chunks
+constexpr int kChunk = 2048;   // tokens of a chunk, times a factor for rows beyond kBins chunks
 constexpr int kLoadsT = 4;     // 16-byte vectors of a thread's piece of a segment
 constexpr int kList = 4096;    // candidates
-// Values by their upper 16 bits (sign, exponent, seven bits of the mantissa: a
-// bf16 value itself): 30 octaves of either sign and zero, in ascending order, and
-// bins for what lies outside.
+// Values by sign and magnitude, in their upper 16 bits (a bf16 value itself): 30
+// octaves, a bin for zero and what is smaller, and one for what is larger.
 constexpr int kOctaves = 30, kOctave0 = 107;  // from 2^-20 to 2^10
-constexpr int kSide = kOctaves * 128, kTable = 2 * kSide + 1;
-constexpr int kTiny = kTable, kLow = kTable + 1, kHigh = kTable + 2, kOdd = 3;
+constexpr int kLeast = kOctave0 * 128;        // upper bits of 2^-20
+constexpr int kHuge = kOctaves * 128 + 1, kHalf = kHuge + 1, kTable = 2 * kHalf;
 constexpr float kNegInf = -__builtin_inff();
 
 struct SampleArgs {
@@ -97,7 +96,7 @@ struct Shared {
       uint32_t tie[kBins];   // and their tokens at the cut
     };
     uint64_t list[kList];    // candidates
-    uint32_t table[kTable + kOdd];
+    uint32_t table[kTable];
   };
   uint64_t wave[16];
   uint64_t found[4];
@@ -106,7 +105,7 @@ struct Shared {
   float top[2][16];
   uint64_t best;
   alignas(16) uint32_t end[4];
-  int bad, count, cut;
+  int bad, tiny, count, cut;
 };
 
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
@@ -263,8 +262,9 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
   constexpr int n = Elem<T>::kVec, kPer = kBins / kT;
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const int size = kChunk * factor, chunks = (V + size - 1) / size;
-  const float value = order_value(cut.key);
-  const uint64_t at_cut = cut.key == 0 ? 0 : weight(value);
+  const bool all = cut.key == 0;
+  const float value = all ? kNegInf : order_value(cut.key);
+  const uint64_t at_cut = all ? 0 : weight(value);
   __syncthreads();
   for (int c = w; c < chunks; c += kT / kWave) {
     uint64_t s = 0;
@@ -273,13 +273,28 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
     for (int id = c * size + lane * n; id < end; id += kWave * n) {
       float x[n];
       load_row(row, V, id, x);
+      if (all) {
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const uint32_t key = order_bits(x[i]);
-        const bool more = key > cut.key && x[i] > kNegInf;
-        if (__any(more)) s += more ? weight(x[i]) : 0;
-        ties += key == cut.key && id + i < V ? 1 : 0;
-        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+        for (int i = 0; i < n; ++i) {
+          s += weight(x[i]);
+          if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+        }
+        continue;
+      }
+      // Few are kept: the lanes' next ones together, until no lane has one.
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) hits |= x[i] >= value && id + i < V ? 1u << i : 0u;
+      while (__any(hits != 0)) {
+        const int at = __ffs(hits) - 1;
+        float y = x[0];
+#pragma unroll
+        for (int i = 1; i < n; ++i) y = at == i ? x[i] : y;
+        if (hits != 0) {
+          if (y == value) ++ties;
+          else s += weight(y);
+        }
+        hits &= hits - 1;
       }
     }
     s = wave_sum64(s);
@@ -327,14 +342,13 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
       load_row(row, V, min(id, V - 1), x);
       uint64_t v[n], t = 0, s = 0;
 #pragma unroll
-      for (int i = 0; i < n; ++i) t += id + i < V && order_bits(x[i]) == cut.key ? 1 : 0;
+      for (int i = 0; i < n; ++i) t += id + i < V && x[i] == value ? 1 : 0;
       const uint64_t ties_to = tie_at + wave_scan64(t, lane);
       uint64_t rank = ties_to - t;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
-        const uint32_t key = order_bits(x[i]);
         const bool in = id + i < V;
-        v[i] = in && key > cut.key ? weight(x[i]) : in && key == cut.key && rank++ < cut.ties ? at_cut : 0;
+        v[i] = in && x[i] > value ? weight(x[i]) : in && x[i] == value && rank++ < cut.ties ? at_cut : 0;
         s += v[i];
         if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
       }
@@ -363,19 +377,29 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
 
 // ---- the table ------------------------------------------------------------------
 
-// Bin of a value by its upper 16 bits.
+// Bin of a value by its upper 16 bits: zero first, then magnitudes, of either sign.
 __device__ __forceinline__ int table_bin(uint32_t b) {
-  const int m = (int)(b & 0x7fffu), t = m - kOctave0 * 128;
-  const bool minus = (b & 0x8000u) != 0;
-  const int odd = m == 0 ? kSide : t < 0 ? kTiny : minus ? kLow : kHigh;
-  return (uint32_t)t < (uint32_t)kSide ? minus ? kSide - 1 - t : kSide + 1 + t : odd;
+  const int m = (int)(b & 0x7fffu);
+  return min(max(m, kLeast - 1), kLeast - 1 + kHuge) - (kLeast - 1) + (b & 0x8000u ? kHalf : 0);
 }
 
-// The upper 16 bits that a bin stands for.
-__device__ __forceinline__ uint32_t table_value(int bin) {
-  return bin == kSide ? 0u : bin > kSide ? (uint32_t)(bin - kSide - 1 + kOctave0 * 128)
-                                         : (uint32_t)(kSide - 1 - bin + kOctave0 * 128) | 0x8000u;
+// The same for two bf16 values at once, as byte offsets.
+__device__ __forceinline__ uint32_t table_offsets(uint32_t w) {
+  typedef uint16_t halves __attribute__((ext_vector_type(2)));
+  const halves m = __builtin_bit_cast(halves, w & 0x7fff7fffu), sign = __builtin_bit_cast(halves, w) >> 15;
+  const halves lo = {kLeast - 1, kLeast - 1}, hi = {kLeast - 1 + kHuge, kLeast - 1 + kHuge};
+  const halves half = {4 * kHalf, 4 * kHalf};
+  const halves t = __builtin_elementwise_min(__builtin_elementwise_max(m, lo), hi) - lo;
+  return __builtin_bit_cast(uint32_t, (halves)((t << 2) + sign * half));
 }
+
+// The upper 16 bits that a bin stands for, and the bin at a place in descending order of values (zeros of both
+// signs are counted in the first of their two).
+__device__ __forceinline__ uint32_t table_value(int bin) {
+  const int t = bin < kHalf ? bin : bin - kHalf;
+  return (uint32_t)(t == 0 ? 0 : kLeast - 1 + t) | (bin < kHalf ? 0u : 0x8000u);
+}
+__device__ __forceinline__ int table_at(int place) { return place < kHalf ? kHuge - place : place; }
 
 // A border in the table: its bin, what lies above it, and (by count or weight) the row's total.
 struct Border {
@@ -389,11 +413,11 @@ template <int kT, typename Mass>
 __device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, double share, Shared& sh, Mass mass) {
   constexpr int kPer = (kTable + kT - 1) / kT;
   uint64_t n = 0, m = 0;
-  const int first = kTable - 1 - (int)threadIdx.x * kPer;
+  const int first = (int)threadIdx.x * kPer;
 #pragma unroll 1
   for (int i = 0; i < kPer; ++i) {
-    const int bin = first - i;
-    const uint32_t c = bin >= 0 ? sh.table[bin] : 0;
+    const int bin = table_at(first + i);
+    const uint32_t c = first + i < kTable ? sh.table[bin] : 0;
     n += c;
     m += c != 0 ? mass(bin, c) : 0;
   }
@@ -408,8 +432,8 @@ __device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, dou
   if (lo < target && target <= hi) {
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
-      const int bin = first - i;
-      const uint32_t c = bin >= 0 ? sh.table[bin] : 0;
+      const int bin = table_at(first + i);
+      const uint32_t c = first + i < kTable ? sh.table[bin] : 0;
       const uint64_t w = c != 0 ? mass(bin, c) : 0;
       if ((by_mass ? m_before + w : n_before + c) >= target) {
         sh.found[0] = bin;
@@ -495,6 +519,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   constexpr int V8 = Elem<T>::kVec, kWaves = kT / kWave;
   __shared__ Shared sh;
   const int r = blockIdx.x, V = a.V, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  typedef uint16_t halves __attribute__((ext_vector_type(2)));
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * (size_t)V;
   const float temperature = a.set.temperature.rows ? a.set.temperature.rows[r] : a.set.temperature.all;
   const int k = a.set.top_k.rows ? a.set.top_k.rows[r] : a.set.top_k.all;
@@ -516,11 +541,11 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     return (double)f < least ? order_value(order_bits(f) + 1) : f;
   };
 
-  if (threadIdx.x == 0) sh.bad = sh.count = 0, sh.best = ~0ull, sh.found[0] = sh.found[1] = sh.found[2] = sh.found[3] = 0;
+  if (threadIdx.x == 0) sh.bad = sh.tiny = sh.count = 0, sh.best = ~0ull, sh.found[0] = sh.found[1] = sh.found[2] = sh.found[3] = 0;
   if (tables)
-    for (int i = threadIdx.x; i < kTable + kOdd; i += kT) sh.table[i] = 0;
+    for (int i = threadIdx.x; i < kTable; i += kT) sh.table[i] = 0;
   float top = kNegInf, bound = kNegInf, largest_own = kNegInf;
-  uint32_t largest = 0;  // magnitude bits
+  uint32_t largest = 0, smallest = ~0u;  // magnitude bits; the least, less one, that are not zero
   double tail = 0.0;
   // The row's last vector, where it is not whole, with -inf behind its end.
   constexpr uint32_t kNinf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
@@ -569,24 +594,16 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     if (V - base > kSegment) fetch(base + kSegment);
 #pragma unroll
     for (int v = 0; v < kLoadsT; ++v) {
-      most[v] = raw_elem<T>(raw, v * V8);
-#pragma unroll
-      for (int i = 1; i < V8; ++i) most[v] = fmaxf(most[v], raw_elem<T>(raw, v * V8 + i));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if constexpr (sizeof(T) == 2) {
-          typedef uint16_t halves __attribute__((ext_vector_type(2)));
-          largest = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(halves, largest),
-                                                                           __builtin_bit_cast(halves, raw[v][q] & 0x7fff7fffu)));
+          const halves m = __builtin_bit_cast(halves, raw[v][q] & 0x7fff7fffu);
+          largest = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(halves, largest), m));
         } else {
           largest = max(largest, raw[v][q] & 0x7fffffffu);
         }
       }
-      own = fmaxf(own, most[v]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[v][q]));  // unpacked again where they are used again: registers
     }
-    if (!lists && !greedy) top = fmaxf(top, own);  // of the thread; the others' follow behind the loop
     if (tables) {
 #pragma unroll
       for (int v = 0; v < kLoadsT; ++v) {
@@ -595,17 +612,29 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (sizeof(T) == 2) {
-            atomicAdd(&sh.table[table_bin(raw[v][q] & 0xffffu)], 1u);
-            atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
+            const halves one = {1, 1};
+            smallest = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
+                __builtin_bit_cast(halves, smallest), (halves)(__builtin_bit_cast(halves, raw[v][q] & 0x7fff7fffu) - one)));
+            const uint32_t at = table_offsets(raw[v][q]);
+            atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sh.table) + (at & 0xffffu)), 1u);
+            atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sh.table) + (at >> 16)), 1u);
           } else {
-            const uint32_t b = raw[v][q];
-            // the least values that are not zero are no zeros, whatever their upper bits
-            atomicAdd(&sh.table[table_bin(b >> 16 | ((b & 0x7fffffffu) - 1u < 0xffffu ? 1u : 0u))], 1u);
+            smallest = min(smallest, (raw[v][q] & 0x7fffffffu) - 1u);
+            atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
           }
         }
+        if constexpr (sizeof(T) == 4) top = fmaxf(top, raw_max<T>(raw, v));
       }
       continue;
     }
+#pragma unroll
+    for (int v = 0; v < kLoadsT; ++v) {
+      most[v] = raw_max<T>(raw, v);
+      own = fmaxf(own, most[v]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[v][q]));  // unpacked again where they are used again: registers
+    }
+    if (!lists && !greedy) top = fmaxf(top, own);  // of the thread; the others' follow behind the loop
     if (!lists && !greedy) continue;
     const float mine = wave_max(own);
     if (lane == 0) sh.top[turn][wave] = mine;
@@ -638,6 +667,22 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   // A fault of the row or of its settings: comparisons that NaN fails.
   const bool nan = sizeof(T) == 2 ? (largest & 0xffffu) > 0x7f80u || largest >> 16 > 0x7f80u : largest > 0x7f800000u;
   if (nan) sh.bad = 1;
+  const bool tiny = sizeof(T) == 2 ? (smallest & 0xffffu) < kLeast - 1 || smallest >> 16 < kLeast - 1
+                                   : smallest < ((uint32_t)kLeast << 16) - 1;
+  if (tables && tiny) sh.tiny = 1;
+  if (tables) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.table[0] += sh.table[kHalf], sh.table[kHalf] = 0;
+    __syncthreads();
+    // The largest value of bf16 rows.
+    for (int i = (int)threadIdx.x; sizeof(T) == 2 && i < kTable && top == kNegInf; i += kT)
+      if (sh.table[table_at(i)] != 0) top = __uint_as_float(table_value(table_at(i)) << 16);
+    if (sizeof(T) == 2 && (sh.table[kHuge] != 0 || sh.tiny || sh.table[kTable - 1] >= (uint32_t)V)) {
+      // A value that the table does not tell.
+      top = kNegInf;
+      for_row<T, kT>(row, V, [&](float x, int) { top = fmaxf(top, x); });
+    }
+  }
   top = wave_max(top);
   if (lane == 0) sh.top[turn][wave] = top;
   __syncthreads();
@@ -665,8 +710,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   if (tables) {
     // Values outside the table that have weight, or that a cut may meet, leave the row to its digits.
     const bool weightless = top > -1024.0f && weight(-1024.0f) == 0;
-    const bool plain = sh.table[kHigh] == 0 && sh.table[kTiny] == 0 && (sh.table[kLow] == 0 || weightless) &&
-                       (!by_k || (uint64_t)k <= (uint64_t)V - sh.table[kLow]);
+    const uint32_t low = sh.table[kTable - 1];  // values of -2^10 and below, masked ones among them
+    const bool plain = sh.table[kHuge] == 0 && !sh.tiny && (low == 0 || weightless) && (!by_k || k <= V - (int)low);
     if (plain && sizeof(T) == 2) {
       // A bin is a value: the cuts are known.
       auto mass = [&](int bin, uint32_t c) { return (uint64_t)c * weight(__uint_as_float(table_value(bin) << 16)); };
@@ -698,7 +743,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       // A bin's values share 16 bits.  Down to which bin the cut can lie: where the least weight that the bins above can
       // have reaches the share of the most that the row can.
       auto edge = [&](int bin, bool far) {
-        return __uint_as_float(table_value(bin) << 16 | ((bin > kSide) == far && bin != kSide ? 0xffffu : 0u));
+        return __uint_as_float(table_value(bin) << 16 | ((bin < kHalf) == far && bin != 0 ? 0xffffu : 0u));
       };
       int bin;
       uint64_t count;
