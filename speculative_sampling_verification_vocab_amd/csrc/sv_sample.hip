@@ -32,6 +32,8 @@ constexpr int kOctaves = 30, kOctave0 = 107;  // from 2^-20 to 2^10
 constexpr int kLeast = kOctave0 * 128;        // upper bits of 2^-20
 constexpr int kHuge = kOctaves * 128 + 1, kHalf = kHuge + 1, kTable = 2 * kHalf;
 constexpr float kNegInf = -__builtin_inff();
+template <typename T>
+constexpr uint32_t kNinfOf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
 
 struct SampleArgs {
   const void* logits;      // [R][V]
@@ -260,41 +262,61 @@ template <typename T, int kT>
 __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
                                     Shared& sh) {
   constexpr int n = Elem<T>::kVec, kPer = kBins / kT;
+  constexpr uint32_t kNinf = kNinfOf<T>;
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const int size = kChunk * factor, chunks = (V + size - 1) / size;
   const bool all = cut.key == 0;
   const float value = all ? kNegInf : order_value(cut.key);
   const uint64_t at_cut = all ? 0 : weight(value);
   __syncthreads();
+  // A wave's chunks, kGroup vectors at a time, the next ones on their way.
+  constexpr int kGroup = 4;
+  const int steps = (size + kWave * n * kGroup - 1) / (kWave * n * kGroup);  // of a chunk
+  u32x4 next[kGroup];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int id = base + (g * kWave + lane) * n;
+      if (id + n <= V) next[g] = load16<T, false, false>(row + id);
+      else next[g] = id < V ? *reinterpret_cast<const u32x4*>(sh.end) : u32x4{kNinf, kNinf, kNinf, kNinf};
+    }
+  };
+  if (w < chunks) fetch(w * size);
   for (int c = w; c < chunks; c += kT / kWave) {
     uint64_t s = 0;
     uint32_t ties = 0;
-    const int end = min((long long)V, (long long)(c + 1) * size);
-    for (int id = c * size + lane * n; id < end; id += kWave * n) {
-      float x[n];
-      load_row(row, V, id, x);
-      if (all) {
+    for (int step = 0; step < steps; ++step) {
+      u32x4 raw[kGroup];
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          s += weight(x[i]);
-          if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+      for (int g = 0; g < kGroup; ++g) raw[g] = next[g];
+      const bool more = step + 1 < steps;
+      const long long base = more ? (long long)c * size + (step + 1) * (kWave * n * kGroup) : (long long)(c + kT / kWave) * size;
+      if (more || base < V) fetch((int)base);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            s += weight(raw_elem<T>(raw, g * n + i));
+            if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+          }
+          continue;
         }
-        continue;
-      }
-      // Few are kept: the lanes' next ones together, until no lane has one.
-      uint32_t hits = 0;
+        // Few are kept: the lanes' next ones together, until no lane has one.
+        uint32_t hits = 0;
 #pragma unroll
-      for (int i = 0; i < n; ++i) hits |= x[i] >= value && id + i < V ? 1u << i : 0u;
-      while (__any(hits != 0)) {
-        const int at = __ffs(hits) - 1;
-        float y = x[0];
+        for (int i = 0; i < n; ++i) hits |= raw_elem<T>(raw, g * n + i) >= value ? 1u << i : 0u;
+        while (__any(hits != 0)) {
+          const int at = __ffs(hits) - 1;
+          float y = raw_elem<T>(raw, g * n);
 #pragma unroll
-        for (int i = 1; i < n; ++i) y = at == i ? x[i] : y;
-        if (hits != 0) {
-          if (y == value) ++ties;
-          else s += weight(y);
+          for (int i = 1; i < n; ++i) y = at == i ? raw_elem<T>(raw, g * n + i) : y;
+          if (hits != 0) {
+            if (y == value) ++ties;
+            else s += weight(y);
+          }
+          hits &= hits - 1;
         }
-        hits &= hits - 1;
       }
     }
     s = wave_sum64(s);
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   uint32_t largest = 0, smallest = ~0u;  // magnitude bits; the least, less one, that are not zero
   double tail = 0.0;
   // The row's last vector, where it is not whole, with -inf behind its end.
-  constexpr uint32_t kNinf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  constexpr uint32_t kNinf = kNinfOf<T>;
   if (threadIdx.x < V8) {
     const int id = V / V8 * V8 + (int)threadIdx.x;
     reinterpret_cast<T*>(sh.end)[threadIdx.x] = id < V ? row[id] : ninf_of<T>();
