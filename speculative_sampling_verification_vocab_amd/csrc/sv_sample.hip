@@ -26,6 +26,7 @@ constexpr int kBins = 2048;    // bins of a digit, and chunks of a row
 constexpr int kChunk = 2048;   // tokens of a chunk, times a factor for rows beyond kBins chunks
 constexpr int kLoadsT = 4;     // 16-byte vectors of a thread's piece of a segment
 constexpr int kList = 4096;    // candidates
+constexpr int kRanked = 512;   // so many are ranked by counting
 // Values by sign and magnitude, in their upper 16 bits (a bf16 value itself): 30
 // octaves, a bin for zero and what is smaller, and one for what is larger.
 constexpr int kOctaves = 30, kOctave0 = 107;  // from 2^-20 to 2^10
@@ -54,39 +55,38 @@ __device__ __forceinline__ float order_value(uint32_t k) {
 }
 
 // The weight of logit x, w 2^F to the nearest whole number: 2^a in 64 bits with a =
-// (x - max) log2(e) / T, by the exponential series of the fraction's
-// natural logarithm (|t| <= 0.35, twelve terms: 6e-15).
+// (x - max) log2(e) / T, as 2^n (1 + r q(r)), n the nearest whole number to a and q the
+// polynomial that takes the values of (2^r - 1) / r at ten Chebyshev points of [-1/2, 1/2]
+// (relative error of the power 5.7e-16; 1 at r = 0).  Equal logits have equal
+// weights wherever they are computed, and the largest has 2^F exactly.
 struct Weight {
   double top, s;  // max x, log2(e) / T
   int F;
-  // 2^(a + e), a >= -1020.
-  static __device__ __forceinline__ double power(double a, int e) {
-    const double n = __builtin_rint(a);
-    const double t = (a - n) * 0.69314718055994530942;
-    double y = 1.0 / 39916800.0;
-    y = __builtin_fma(y, t, 1.0 / 3628800.0);
-    y = __builtin_fma(y, t, 1.0 / 362880.0);
-    y = __builtin_fma(y, t, 1.0 / 40320.0);
-    y = __builtin_fma(y, t, 1.0 / 5040.0);
-    y = __builtin_fma(y, t, 1.0 / 720.0);
-    y = __builtin_fma(y, t, 1.0 / 120.0);
-    y = __builtin_fma(y, t, 1.0 / 24.0);
-    y = __builtin_fma(y, t, 1.0 / 6.0);
-    y = __builtin_fma(y, t, 0.5);
-    y = __builtin_fma(y, t, 1.0);
-    y = __builtin_fma(y, t, 1.0);
-    return __builtin_ldexp(y, (int)n + e);
-  }
-  __device__ __forceinline__ double exponent(float x) const { return ((double)x - top) * s; }
   __device__ __forceinline__ uint64_t operator()(float x) const {
-    const double a = exponent(x);
-    if (!(a > -(double)(F + 2))) return 0;  // below half a unit
-    const double v = power(a, F) + 4503599627370496.0;  // 2^52: the sum's low bits are the power's nearest
-    return (uint64_t)__double_as_longlong(v) - 0x4330000000000000ull;
+    const double a = ((double)x - top) * s;
+    const double n = a + 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits are the whole number
+    const double r = a - (n - 6755399441055744.0);
+    double y = 7.070977866508139e-09;
+    y = __builtin_fma(y, r, 1.0205905413765595e-07);
+    y = __builtin_fma(y, r, 1.3215451633221434e-06);
+    y = __builtin_fma(y, r, 1.5252672924850737e-05);
+    y = __builtin_fma(y, r, 1.5403530424776529e-04);
+    y = __builtin_fma(y, r, 1.3333558200794592e-03);
+    y = __builtin_fma(y, r, 9.618129107618665e-03);
+    y = __builtin_fma(y, r, 5.550410866465167e-02);
+    y = __builtin_fma(y, r, 2.4022650695910075e-01);
+    y = __builtin_fma(y, r, 6.931471805599462e-01);
+    y = __builtin_fma(y, r, 1.0);
+    // Times 2^(n + F) in the exponent; added to 2^52, the low bits are the nearest whole number.
+    const int hi = __double2hiint(y) + ((__double2loint(n) + F) << 20);
+    const double v = __hiloint2double(hi, __double2loint(y)) + 4503599627370496.0;
+    const uint64_t w = (uint64_t)(uint32_t)(__double2hiint(v) - 0x43300000) << 32 | (uint32_t)__double2loint(v);
+    return a > -(double)(F + 2) ? w : 0;  // less than a quarter of a unit otherwise
   }
 };
 
 // What a block shares.
+template <typename T>
 struct Shared {
   union {
     struct {
@@ -99,15 +99,16 @@ struct Shared {
     };
     uint64_t list[kList];    // candidates
     uint32_t table[kTable];
+    uint64_t mass[sizeof(T) == 4 ? kTable : 1];  // fp32: the table's weights
   };
   uint64_t wave[16];
   uint64_t found[4];
   uint64_t votes[2][16];
-  double tail[16];
+  float lanes[16][kWave];
   float top[2][16];
   uint64_t best;
   alignas(16) uint32_t end[4];
-  int bad, tiny, count, cut;
+  int bad, tiny, low, count, cut;
 };
 
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
@@ -126,8 +127,8 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t v, int lane) {
 }
 
 // Sum over the block; every thread gets it.
-template <int kT>
-__device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
+template <int kT, typename T>
+__device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared<T>& sh) {
   v = wave_sum64(v);
   __syncthreads();
   if ((threadIdx.x & (kWave - 1)) == 0) sh.wave[threadIdx.x / kWave] = v;
@@ -139,8 +140,8 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared& sh) {
 }
 
 // Sum of the threads before this one.
-template <int kT>
-__device__ __forceinline__ uint64_t block_before64(uint64_t v, Shared& sh) {
+template <int kT, typename T>
+__device__ __forceinline__ uint64_t block_before64(uint64_t v, Shared<T>& sh) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const uint64_t up_to = wave_scan64(v, lane);
   __syncthreads();
@@ -192,7 +193,7 @@ struct Cut {
 // share >= 0: the target is that share of the row's weight, known after the first.
 template <typename T, int kT>
 __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weight, bool by_mass, uint64_t target,
-                                        double share, Shared& sh) {
+                                        double share, Shared<T>& sh) {
   uint32_t prefix = 0;
   uint64_t above_n = 0, above_m = 0;
   int shift = 21;
@@ -260,7 +261,7 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
 // their ties at it, a scan, and one chunk again.
 template <typename T, int kT>
 __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
-                                    Shared& sh) {
+                                    Shared<T>& sh) {
   constexpr int n = Elem<T>::kVec, kPer = kBins / kT;
   constexpr uint32_t kNinf = kNinfOf<T>;
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
@@ -306,6 +307,8 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
         uint32_t hits = 0;
 #pragma unroll
         for (int i = 0; i < n; ++i) hits |= raw_elem<T>(raw, g * n + i) >= value ? 1u << i : 0u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[g][q]));  // unpacked again where one is picked: registers
         while (__any(hits != 0)) {
           const int at = __ffs(hits) - 1;
           float y = raw_elem<T>(raw, g * n);
@@ -431,15 +434,15 @@ struct Border {
 
 // The bin, from the highest down, at which counts (by_mass false) or weights reach target, or with share >=
 // 0 that share of the total weight.  count(bin) and mass(bin, count) give a bin's; at most `target` must be there.
-template <int kT, typename Mass>
-__device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, double share, Shared& sh, Mass mass) {
+template <int kT, typename T, typename Bin, typename Mass>
+__device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, uint64_t target, double share, Shared<T>& sh, Mass mass) {
   constexpr int kPer = (kTable + kT - 1) / kT;
   uint64_t n = 0, m = 0;
   const int first = (int)threadIdx.x * kPer;
 #pragma unroll 1
   for (int i = 0; i < kPer; ++i) {
     const int bin = table_at(first + i);
-    const uint32_t c = first + i < kTable ? sh.table[bin] : 0;
+    const auto c = first + i < kTable ? table[bin] : 0;
     n += c;
     m += c != 0 ? mass(bin, c) : 0;
   }
@@ -455,7 +458,7 @@ __device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, dou
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
       const int bin = table_at(first + i);
-      const uint32_t c = first + i < kTable ? sh.table[bin] : 0;
+      const auto c = first + i < kTable ? table[bin] : 0;
       const uint64_t w = c != 0 ? mass(bin, c) : 0;
       if ((by_mass ? m_before + w : n_before + c) >= target) {
         sh.found[0] = bin;
@@ -479,8 +482,8 @@ __device__ __forceinline__ Border find_border(bool by_mass, uint64_t target, dou
 
 // The largest 16-bit prefix p of ordered bits with at least k threads whose `own` has a prefix >= p (0
 // if there are fewer than k).  Two bits at a time.
-template <int kT>
-__device__ __forceinline__ uint32_t kth_prefix(uint32_t own, uint32_t k, Shared& sh) {
+template <int kT, typename T>
+__device__ __forceinline__ uint32_t kth_prefix(uint32_t own, uint32_t k, Shared<T>& sh) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   own >>= 16;
   uint32_t p = 0;
@@ -504,6 +507,49 @@ __device__ __forceinline__ uint32_t kth_prefix(uint32_t own, uint32_t k, Shared&
       }
   }
   return p;
+}
+
+// Up to so many, 64 disjoint sets of tokens give the bound: lane l's of every wave.  k
+// of them that reach it are then among the first 64 ln(64 / (64 - k)) or so (k = 52: 107).
+constexpr int kFewer = 52;
+
+// The largest 16-bit prefix that at least k of those sets reach, one barrier and 16 votes of the wave.
+template <int kT, typename T>
+__device__ __forceinline__ uint32_t kth_of_lanes(float own, int k, Shared<T>& sh) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  sh.lanes[w][lane] = own;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kT / kWave; ++i) own = fmaxf(own, sh.lanes[i][lane]);
+  const uint32_t key = order_bits(own) >> 16;
+  uint32_t p = 0;
+#pragma unroll
+  for (int shift = 15; shift >= 0; --shift)
+    if (__popcll(__ballot(key >= (p | 1u << shift))) >= k) p |= 1u << shift;
+  return p;
+}
+
+// Each of up to 512 listed tokens' ranks by (value, id) and by id, in the low and high half of ranks[i]: pairs of 64,
+// a quarter of the pairs' second at a time.
+template <int kT>
+__device__ __forceinline__ void rank_list(const uint64_t* list, uint32_t* ranks, int n) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int groups = (n + kWave - 1) / kWave;
+  for (int i = threadIdx.x; i < n; i += kT) ranks[i] = 0;
+  __syncthreads();
+  for (int unit = threadIdx.x / kWave; unit < groups * groups * 4; unit += kT / kWave) {
+    const int mine = unit / (groups * 4) * kWave + lane, theirs = unit / 4 % groups * kWave + unit % 4 * 16;
+    const uint64_t e = mine < n ? list[mine] : 0, f = theirs + (lane & 15) < n ? list[theirs + (lane & 15)] : ~0ull;
+    uint32_t r = 0, by_id = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t lo = __builtin_amdgcn_readlane((int)f, j), hi = __builtin_amdgcn_readlane((int)(f >> 32), j);
+      r += ((uint64_t)hi << 32 | lo) < e ? 1 : 0;
+      by_id += lo < (uint32_t)e ? 1 : 0;
+    }
+    if (mine < n) atomicAdd(&ranks[mine], r | by_id << 16);
+  }
+  __syncthreads();
 }
 
 // The list's first n (a power of two) in ascending order.
@@ -539,7 +585,7 @@ __device__ __forceinline__ float raw_max(const u32x4 (&raw)[kLoadsT], int v) {
 template <typename T, int kT>
 __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   constexpr int V8 = Elem<T>::kVec, kWaves = kT / kWave;
-  __shared__ Shared sh;
+  __shared__ Shared<T> sh;
   const int r = blockIdx.x, V = a.V, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   typedef uint16_t halves __attribute__((ext_vector_type(2)));
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * (size_t)V;
@@ -555,6 +601,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   // need the row's values first, in a table.
   const bool lists = !greedy && (by_k ? k <= kT : by_m && !by_p);
   const bool tables = !greedy && (by_k ? k > kT : by_p);
+  const bool counts = tables && (sizeof(T) == 2 || by_k);
   const double span_m = by_m ? (double)temperature * log((double)fminf(m, 1.0f)) : 0.0;
   // The least float at or above the min-p cut.
   auto least_kept = [&](float top) {
@@ -563,12 +610,11 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     return (double)f < least ? order_value(order_bits(f) + 1) : f;
   };
 
-  if (threadIdx.x == 0) sh.bad = sh.tiny = sh.count = 0, sh.best = ~0ull, sh.found[0] = sh.found[1] = sh.found[2] = sh.found[3] = 0;
-  if (tables)
+  if (threadIdx.x == 0) sh.bad = sh.tiny = sh.low = sh.count = 0, sh.best = ~0ull, sh.found[0] = sh.found[1] = sh.found[2] = sh.found[3] = 0;
+  if (counts)
     for (int i = threadIdx.x; i < kTable; i += kT) sh.table[i] = 0;
   float top = kNegInf, bound = kNegInf, largest_own = kNegInf;
   uint32_t largest = 0, smallest = ~0u;  // magnitude bits; the least, less one, that are not zero
-  double tail = 0.0;
   // The row's last vector, where it is not whole, with -inf behind its end.
   constexpr uint32_t kNinf = kNinfOf<T>;
   if (threadIdx.x < V8) {
@@ -587,12 +633,12 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   };
   constexpr int kSegment = kT * V8 * kLoadsT;
   // Tokens at or above the bound to the list.
-  auto list_those = [&](const u32x4 (&raw)[kLoadsT], int v, int base) {
+  auto list_those = [&](const u32x4 (&raw)[kLoadsT], int v, int base, float most) {
     uint32_t hits = 0;
 #pragma unroll
     for (int i = 0; i < V8; ++i) {
       const float x = raw_elem<T>(raw, v * V8 + i);
-      hits |= x >= bound && x > kNegInf ? 1u << i : 0u;
+      hits |= x >= bound && x > kNegInf && x <= most ? 1u << i : 0u;
     }
     if (hits == 0) return;
     int at = atomicAdd(&sh.count, __popc(hits));
@@ -642,7 +688,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
             atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sh.table) + (at >> 16)), 1u);
           } else {
             smallest = min(smallest, (raw[v][q] & 0x7fffffffu) - 1u);
-            atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
+            if (counts) atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
           }
         }
         if constexpr (sizeof(T) == 4) top = fmaxf(top, raw_max<T>(raw, v));
@@ -679,11 +725,12 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       // k threads' largest so far are k tokens of the row; taken anew when as much again was read.
       largest_own = fmaxf(largest_own, own);
       if (by_k && (segment & (segment + 1)) == 0)
-        bound = fmaxf(bound, order_value(max(kth_prefix<kT>(order_bits(largest_own), (uint32_t)k, sh), 0x80u) << 16));
+        bound = fmaxf(bound, order_value(max(k <= kFewer ? kth_of_lanes<kT>(largest_own, k, sh)
+                                                         : kth_prefix<kT>(order_bits(largest_own), (uint32_t)k, sh), 0x80u) << 16));
       if (by_m && !(by_k && by_p)) bound = fmaxf(bound, least_kept(top));  // top-p of the top k: all of their weight
 #pragma unroll
       for (int v = 0; v < kLoadsT; ++v)
-        if (__any(most[v] >= bound)) list_those(raw, v, base);
+        if (__any(most[v] >= bound)) list_those(raw, v, base, __builtin_inff());
     }
   }
   // A fault of the row or of its settings: comparisons that NaN fails.
@@ -692,7 +739,9 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   const bool tiny = sizeof(T) == 2 ? (smallest & 0xffffu) < kLeast - 1 || smallest >> 16 < kLeast - 1
                                    : smallest < ((uint32_t)kLeast << 16) - 1;
   if (tables && tiny) sh.tiny = 1;
-  if (tables) {
+  if (tables && (sizeof(T) == 2 ? (largest & 0xffffu) >= 0x4480u || largest >> 16 >= 0x4480u : largest >= 0x44800000u))
+    sh.low = 1;  // a magnitude of 2^10 or more; of the largest, or below
+  if (counts) {
     __syncthreads();
     if (threadIdx.x == 0) sh.table[0] += sh.table[kHalf], sh.table[kHalf] = 0;
     __syncthreads();
@@ -729,17 +778,18 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     else if (c.key == cut.key && c.ties < cut.ties) cut.ties = c.ties;
   };
   bool done = !tables && !lists, listed = lists;
+  uint64_t row_mass = 0;
   if (tables) {
     // Values outside the table that have weight, or that a cut may meet, leave the row to its digits.
     const bool weightless = top > -1024.0f && weight(-1024.0f) == 0;
-    const uint32_t low = sh.table[kTable - 1];  // values of -2^10 and below, masked ones among them
-    const bool plain = sh.table[kHuge] == 0 && !sh.tiny && (low == 0 || weightless) && (!by_k || k <= V - (int)low);
+    const int low = counts ? (int)sh.table[kTable - 1] : sh.low;  // values of -2^10 and below, masked ones among them
+    const bool plain = top < 1024.0f && !sh.tiny && (low == 0 || weightless) && (!by_k || k <= V - low);
     if (plain && sizeof(T) == 2) {
       // A bin is a value: the cuts are known.
       auto mass = [&](int bin, uint32_t c) { return (uint64_t)c * weight(__uint_as_float(table_value(bin) << 16)); };
       uint64_t all = 0;
       if (by_k) {
-        const Border b = find_border<kT>(false, (uint64_t)k, -1.0, sh, mass);
+        const Border b = find_border<kT>(sh.table, false, (uint64_t)k, -1.0, sh, mass);
         Cut c;
         const float x = __uint_as_float(table_value(b.bin) << 16);
         c.key = order_bits(x);
@@ -749,7 +799,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       }
       if (by_p) {
         const double t = __builtin_ceil((double)p * (double)all);
-        const Border b = find_border<kT>(true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh, mass);
+        const Border b = find_border<kT>(sh.table, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh, mass);
         Cut c;
         const float x = __uint_as_float(table_value(b.bin) << 16);
         const uint64_t w = weight(x);
@@ -761,33 +811,16 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         narrow(c);
       }
       done = true;
-    } else if (plain) {
-      // A bin's values share 16 bits.  Down to which bin the cut can lie: where the least weight that the bins above can
-      // have reaches the share of the most that the row can.
-      auto edge = [&](int bin, bool far) {
-        return __uint_as_float(table_value(bin) << 16 | ((bin < kHalf) == far && bin != 0 ? 0xffffu : 0u));
-      };
-      int bin;
-      uint64_t count;
-      if (by_k) {
-        const Border b = find_border<kT>(false, (uint64_t)k, -1.0, sh, [](int, uint32_t) { return (uint64_t)0; });
-        bin = b.bin;
-        count = b.above_n + sh.table[bin];
-      } else {
-        const Border hi = find_border<kT>(true, 1, -1.0, sh, [&](int bin, uint32_t c) { return (uint64_t)c * weight(edge(bin, true)); });
-        const double t = __builtin_ceil((p > 0.0f ? (double)p : 0.0) * (double)hi.total_m);
-        const uint64_t goal = t < 1.0 ? 1 : (uint64_t)t;
-        if (threadIdx.x == 0) sh.found[0] = 0, sh.found[1] = ~0ull >> 1;
+    } else if (plain && sizeof(T) == 4) {
+      // A bin's values share 16 bits: the cut's bin is known, and its tokens, or with the ones above all that can be
+      // kept, are listed.
+      auto least_of = [&](int bin) { return __uint_as_float(table_value(bin) << 16 | (bin >= kHalf ? 0xffffu : 0u)); };
+      auto most_of = [&](int bin) { return __uint_as_float(table_value(bin) << 16 | (bin < kHalf && bin != 0 ? 0xffffu : 0u)); };
+      auto list_between = [&](float lo, float hi) {
         __syncthreads();
-        const Border b = find_border<kT>(true, goal, -1.0, sh, [&](int bin, uint32_t c) { return (uint64_t)c * weight(edge(bin, false)); });
-        bin = b.bin;
-        count = b.above_n + sh.table[bin];
-      }
-      __syncthreads();
-      if (count <= kList) {
-        listed = true;
-        bound = edge(bin, false);
-        Weight w{(double)top, s64, 0};
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+        bound = lo;
         fetch(0);
 #pragma unroll 1
         for (int base = 0; base < V; base += kSegment) {
@@ -796,30 +829,102 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
           for (int v = 0; v < kLoadsT; ++v) raw[v] = next[v];
           if (V - base > kSegment) fetch(base + kSegment);
 #pragma unroll
-          for (int v = 0; v < kLoadsT; ++v) {
-            if (__any(raw_max<T>(raw, v) >= bound)) list_those(raw, v, base);
-            if (!by_k) {
-#pragma unroll
-              for (int i = 0; i < V8; ++i) {
-                const float x = raw_elem<T>(raw, v * V8 + i);
-                const double e = w.exponent(x);
-                tail += x < bound && e > -70.0 ? Weight::power(fmax(e, -70.0), 0) : 0.0;
-                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
-              }
-            }
-          }
+          for (int v = 0; v < kLoadsT; ++v)
+            if (__any(raw_max<T>(raw, v) >= lo)) list_those(raw, v, base, hi);
         }
         __syncthreads();
+        return sh.count;
+      };
+      Border b;
+      uint64_t goal = (uint64_t)k;
+      if (by_k) {
+        b = find_border<kT>(sh.table, false, goal, -1.0, sh, [](int, uint32_t) { return (uint64_t)0; });
+      } else {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTable; i += kT) sh.mass[i] = 0;
+        __syncthreads();
+        fetch(0);
+#pragma unroll 1
+        for (int base = 0; base < V; base += kSegment) {
+          u32x4 raw[kLoadsT];
+#pragma unroll
+          for (int v = 0; v < kLoadsT; ++v) raw[v] = next[v];
+          if (V - base > kSegment) fetch(base + kSegment);
+#pragma unroll
+          for (int v = 0; v < kLoadsT; ++v)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t w = weight(__uint_as_float(raw[v][q]));
+              if (w != 0) atomicAdd((unsigned long long*)&sh.mass[table_bin(raw[v][q] >> 16)], (unsigned long long)w);
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) sh.mass[0] += sh.mass[kHalf], sh.mass[kHalf] = 0;
+        __syncthreads();
+        const double share = p > 0.0f ? (double)p : 0.0;
+        b = find_border<kT>(sh.mass, true, 1, share, sh, [](int, uint64_t m) { return m; });
+        row_mass = b.total_m;
+        const double t = __builtin_ceil(share * (double)row_mass);
+        goal = t < 1.0 ? 1 : (uint64_t)t;
+      }
+      __syncthreads();
+      if (list_between(least_of(b.bin), __builtin_inff()) <= kList) {
+        listed = true;
+      } else if (!(by_k && by_p)) {
+        const int in_bin = list_between(least_of(b.bin), most_of(b.bin));
+        if (in_bin <= kList) {
+          int size = 2;
+          while (size < in_bin) size *= 2;
+          for (int i = in_bin + (int)threadIdx.x; i < size; i += kT) sh.list[i] = ~0ull;
+          sort_list<kT>(sh.list, size);
+          const int per = (size + kT - 1) / kT;
+          uint64_t own[kList / kT], sum = 0;
+#pragma unroll
+          for (int i = 0; i < kList / kT; ++i) {
+            const int at = (int)threadIdx.x * per + i;
+            own[i] = i < per && at < in_bin ? by_k ? 1 : weight(order_value(~(uint32_t)(sh.list[at] >> 32))) : 0;
+            sum += own[i];
+          }
+          uint64_t before = (by_k ? b.above_n : b.above_m) + block_before64<kT>(sum, sh);
+#pragma unroll
+          for (int i = 0; i < kList / kT; ++i) {
+            if (before < goal && goal <= before + own[i]) sh.cut = (int)threadIdx.x * per + i;
+            before += own[i];
+          }
+          __syncthreads();
+          const int at = sh.cut;
+          Cut c;
+          c.key = ~(uint32_t)(sh.list[at] >> 32);
+          int ties = 1;
+          while (ties <= at && ~(uint32_t)(sh.list[at - ties] >> 32) == c.key) ++ties;
+          c.ties = (uint64_t)ties;
+          c.mass = 0;
+          narrow(c);
+          done = true;
+        }
       }
     }
   }
   const int n = sh.count;
   if (listed && n <= kList) {
-    // Ranked: the bits' complements ascend where the logits descend.
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int i = n + (int)threadIdx.x; i < size; i += kT) sh.list[i] = ~0ull;
-    sort_list<kT>(sh.list, size);
+    // Ranked: the bits' complements ascend where the logits descend.  Few are ranked by counting, more are sorted.
+    const bool few = n <= kRanked;
+    int size = n;
+    uint64_t own_entry = 0;
+    uint32_t own_ranks = 0;
+    if (few) {
+      uint32_t* ranks = reinterpret_cast<uint32_t*>(sh.list + kRanked);
+      rank_list<kT>(sh.list, ranks, n);
+      if ((int)threadIdx.x < n) own_entry = sh.list[threadIdx.x], own_ranks = ranks[threadIdx.x];
+      __syncthreads();
+      if ((int)threadIdx.x < n) sh.list[own_ranks & 0xffffu] = own_entry;
+      __syncthreads();
+    } else {
+      size = 2;
+      while (size < n) size *= 2;
+      for (int i = n + (int)threadIdx.x; i < size; i += kT) sh.list[i] = ~0ull;
+      sort_list<kT>(sh.list, size);
+    }
     const int per = (size + kT - 1) / kT;  // 8 at most
     constexpr int kPer = kList / kT;
     uint64_t own[kPer], sum = 0;
@@ -833,9 +938,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       sum += own[i];
       __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
     }
-    double all_tail = wave_sum(tail);
-    if (lane == 0) sh.tail[wave] = all_tail;
-    if (threadIdx.x == 0) sh.cut = n, sh.found[0] = 0;
+    if (threadIdx.x == 0) sh.cut = n, sh.found[0] = row_mass;
     const uint64_t before = block_before64<kT>(sum, sh);
     uint64_t up_to = before;
     const int nk = by_k ? min(k, n) : n;
@@ -845,11 +948,6 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         up_to += own[i];
         if (i < per && (int)threadIdx.x * per + i == nk - 1) sh.found[0] = up_to;
       }
-    } else if (by_p) {
-      all_tail = 0.0;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) all_tail += sh.tail[i];
-      if (threadIdx.x == kT - 1) sh.found[0] = before + sum + (uint64_t)__builtin_rint(__builtin_ldexp(all_tail, a.F));
     }
     __syncthreads();
     const double share = __builtin_ceil((double)fmaxf(p, 0.0f) * (double)sh.found[0]);
@@ -872,20 +970,28 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     {
       // The kept ones by id.
       __syncthreads();
-      size = 2;
-      while (size < kept) size *= 2;
-      for (int i = threadIdx.x; i < size; i += kT) {
-        const uint64_t e = sh.list[i];
-        sh.list[i] = i < kept ? e << 32 | e >> 32 : ~0ull;
+      int count = kept;
+      if (few) {
+        if ((int)threadIdx.x < n)
+          sh.list[own_ranks >> 16] = (int)(own_ranks & 0xffffu) < kept ? own_entry << 32 | own_entry >> 32 : ~0ull;
+        count = size = n;
+        __syncthreads();
+      } else {
+        size = 2;
+        while (size < kept) size *= 2;
+        for (int i = threadIdx.x; i < size; i += kT) {
+          const uint64_t e = sh.list[i];
+          sh.list[i] = i < kept ? e << 32 | e >> 32 : ~0ull;
+        }
+        sort_list<kT>(sh.list, size);
       }
-      sort_list<kT>(sh.list, size);
       const int per = (size + kT - 1) / kT;
       sum = 0;
       uint32_t id[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int at = (int)threadIdx.x * per + i;
-        const uint64_t e = i < per && at < kept ? sh.list[at] : ~0ull;
+        const uint64_t e = i < per && at < count ? sh.list[at] : ~0ull;
         id[i] = (uint32_t)(e >> 32);
         own[i] = e == ~0ull ? 0 : weight(order_value(~(uint32_t)e));
         sum += own[i];
