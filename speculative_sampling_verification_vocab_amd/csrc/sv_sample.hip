@@ -22,11 +22,14 @@ namespace sv {
 
 namespace {
 
-constexpr int kBins = 2048;    // bins of a digit, and chunks of a row
-constexpr int kChunk = 2048;   // tokens of a chunk, times a factor for rows beyond kBins chunks
+constexpr int kBins = 2048;    // bins of a digit
+constexpr int kChunk = 2048;   // tokens of a chunk, times a factor for rows of more than
+constexpr int kChunks = 512;   // chunks
 constexpr int kLoadsT = 4;     // 16-byte vectors of a thread's piece of a segment
 constexpr int kList = 4096;    // candidates
 constexpr int kRanked = 512;   // so many are ranked by counting
+// Where less than one token in so many is kept, weights are computed for those alone.
+constexpr int kSparse = 256;
 // Values by sign and magnitude, in their upper 16 bits (a bf16 value itself): 30
 // octaves, a bin for zero and what is smaller, and one for what is larger.
 constexpr int kOctaves = 30, kOctave0 = 107;  // from 2^-20 to 2^10
@@ -85,6 +88,12 @@ struct Weight {
   }
 };
 
+// A value that all lanes have, in scalar registers.
+__device__ __forceinline__ float uniform(float x) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
+__device__ __forceinline__ double uniform(double x) {
+  return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(x)), __builtin_amdgcn_readfirstlane(__double2loint(x)));
+}
+
 // What a block shares.
 template <typename T>
 struct Shared {
@@ -93,14 +102,12 @@ struct Shared {
       uint32_t count[kBins];
       uint64_t mass[kBins];
     } bin;
-    struct {
-      uint64_t sum[kBins];   // of a row's chunks
-      uint32_t tie[kBins];   // and their tokens at the cut
-    };
     uint64_t list[kList];    // candidates
     uint32_t table[kTable];
-    uint64_t mass[sizeof(T) == 4 ? kTable : 1];  // fp32: the table's weights
+    uint64_t mass[kTable];   // fp32: the weights in the table's bins; bf16: the weights of its values
   };
+  uint64_t chunk_sum[kChunks];   // weights above the cut
+  uint32_t chunk_tie[kChunks];   // and tokens at it
   uint64_t wave[16];
   uint64_t found[4];
   uint64_t votes[2][16];
@@ -111,19 +118,24 @@ struct Shared {
   int bad, tiny, low, count, cut;
 };
 
-__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor((unsigned long long)v, d);
-  return v;
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+  return (uint64_t)(uint32_t)dpp::mov<kCtrl, kRowMask>(0, (int)(v >> 32)) << 32 | (uint32_t)dpp::mov<kCtrl, kRowMask>(0, (int)v);
 }
 
-__device__ __forceinline__ uint64_t wave_scan64(uint64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const uint64_t w = __shfl_up((unsigned long long)v, d);
-    if (lane >= d) v += w;
-  }
+// Inclusive sums over the lanes, as in wave_inclusive_scan, and their total.
+__device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
+  v += moved<dpp::kShr1, 0xf>(v);
+  v += moved<dpp::kShr2, 0xf>(v);
+  v += moved<dpp::kShr4, 0xf>(v);
+  v += moved<dpp::kShr8, 0xf>(v);
+  v += moved<dpp::kBcast15, 0xa>(v);
+  v += moved<dpp::kBcast31, 0xc>(v);
   return v;
+}
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
+  v = wave_scan64(v);
+  return (uint64_t)(uint32_t)dpp::lane63((int)(v >> 32)) << 32 | (uint32_t)dpp::lane63((int)v);
 }
 
 // Sum over the block; every thread gets it.
@@ -143,7 +155,7 @@ __device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared<T>& sh) {
 template <int kT, typename T>
 __device__ __forceinline__ uint64_t block_before64(uint64_t v, Shared<T>& sh) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const uint64_t up_to = wave_scan64(v, lane);
+  const uint64_t up_to = wave_scan64(v);
   __syncthreads();
   if (lane == kWave - 1) sh.wave[w] = up_to;
   __syncthreads();
@@ -255,151 +267,6 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
   return c;
 }
 
-// ---- the draw -------------------------------------------------------------------
-
-// The token of a row that a cut leaves: one pass for the chunks' weights above the cut and
-// their ties at it, a scan, and one chunk again.
-template <typename T, int kT>
-__device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
-                                    Shared<T>& sh) {
-  constexpr int n = Elem<T>::kVec, kPer = kBins / kT;
-  constexpr uint32_t kNinf = kNinfOf<T>;
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const int size = kChunk * factor, chunks = (V + size - 1) / size;
-  const bool all = cut.key == 0;
-  const float value = all ? kNegInf : order_value(cut.key);
-  const uint64_t at_cut = all ? 0 : weight(value);
-  __syncthreads();
-  // A wave's chunks, kGroup vectors at a time, the next ones on their way.
-  constexpr int kGroup = 4;
-  const int steps = (size + kWave * n * kGroup - 1) / (kWave * n * kGroup);  // of a chunk
-  u32x4 next[kGroup];
-  auto fetch = [&](int base) {
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      const int id = base + (g * kWave + lane) * n;
-      if (id + n <= V) next[g] = load16<T, false, false>(row + id);
-      else next[g] = id < V ? *reinterpret_cast<const u32x4*>(sh.end) : u32x4{kNinf, kNinf, kNinf, kNinf};
-    }
-  };
-  if (w < chunks) fetch(w * size);
-  for (int c = w; c < chunks; c += kT / kWave) {
-    uint64_t s = 0;
-    uint32_t ties = 0;
-    for (int step = 0; step < steps; ++step) {
-      u32x4 raw[kGroup];
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) raw[g] = next[g];
-      const bool more = step + 1 < steps;
-      const long long base = more ? (long long)c * size + (step + 1) * (kWave * n * kGroup) : (long long)(c + kT / kWave) * size;
-      if (more || base < V) fetch((int)base);
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) {
-        if (all) {
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            s += weight(raw_elem<T>(raw, g * n + i));
-            if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
-          }
-          continue;
-        }
-        // Few are kept: the lanes' next ones together, until no lane has one.
-        uint32_t hits = 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) hits |= raw_elem<T>(raw, g * n + i) >= value ? 1u << i : 0u;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[g][q]));  // unpacked again where one is picked: registers
-        while (__any(hits != 0)) {
-          const int at = __ffs(hits) - 1;
-          float y = raw_elem<T>(raw, g * n);
-#pragma unroll
-          for (int i = 1; i < n; ++i) y = at == i ? raw_elem<T>(raw, g * n + i) : y;
-          if (hits != 0) {
-            if (y == value) ++ties;
-            else s += weight(y);
-          }
-          hits &= hits - 1;
-        }
-      }
-    }
-    s = wave_sum64(s);
-    ties = (uint32_t)wave_sum64(ties);
-    if (lane == 0) sh.sum[c] = s, sh.tie[c] = ties;
-  }
-  __syncthreads();
-  // Thread t has the chunks kPer t and on; ties are kept up to cut.ties of them.
-  uint64_t own[kPer], tied[kPer], ties = 0, sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = (int)threadIdx.x * kPer + i;
-    own[i] = c < chunks ? sh.sum[c] : 0;
-    tied[i] = c < chunks ? sh.tie[c] : 0;
-    ties += tied[i];
-  }
-  uint64_t ties_before = block_before64<kT>(ties, sh);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const uint64_t room = cut.ties > ties_before ? cut.ties - ties_before : 0;
-    own[i] += (tied[i] < room ? tied[i] : room) * at_cut;
-    ties_before += tied[i];
-    sum += own[i];
-  }
-  ties_before -= ties;
-  const uint64_t total = block_sum64<kT>(sum, sh);
-  const uint64_t target = (uint64_t)((double)u * (double)total);
-  uint64_t before = block_before64<kT>(sum, sh);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (before <= target && target < before + own[i]) {
-      sh.found[0] = threadIdx.x * kPer + i;
-      sh.found[1] = before;
-      sh.found[2] = ties_before;
-    }
-    before += own[i];
-    ties_before += tied[i];
-  }
-  __syncthreads();
-  if (threadIdx.x < kWave) {
-    uint64_t at = sh.found[1], tie_at = sh.found[2];
-    for (int id0 = (int)sh.found[0] * size; id0 < V; id0 += kWave * n) {
-      const int id = id0 + lane * n;
-      float x[n];
-      load_row(row, V, min(id, V - 1), x);
-      uint64_t v[n], t = 0, s = 0;
-#pragma unroll
-      for (int i = 0; i < n; ++i) t += id + i < V && x[i] == value ? 1 : 0;
-      const uint64_t ties_to = tie_at + wave_scan64(t, lane);
-      uint64_t rank = ties_to - t;
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const bool in = id + i < V;
-        v[i] = in && x[i] > value ? weight(x[i]) : in && x[i] == value && rank++ < cut.ties ? at_cut : 0;
-        s += v[i];
-        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
-      }
-      const uint64_t up_to = at + wave_scan64(s, lane);
-      const uint64_t hit = __ballot(up_to > target);
-      if (hit != 0) {
-        if (lane == __ffsll((unsigned long long)hit) - 1) {
-          uint64_t y = up_to - s;
-          int token = id;
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            y += v[i];
-            if (y <= target) token = id + i + 1;
-          }
-          sh.found[3] = token;
-        }
-        break;
-      }
-      at = __shfl((unsigned long long)up_to, kWave - 1);
-      tie_at = __shfl((unsigned long long)ties_to, kWave - 1);
-    }
-  }
-  __syncthreads();
-  return (int)sh.found[3];
-}
-
 // ---- the table ------------------------------------------------------------------
 
 // Bin of a value by its upper 16 bits: zero first, then magnitudes, of either sign.
@@ -408,14 +275,16 @@ __device__ __forceinline__ int table_bin(uint32_t b) {
   return min(max(m, kLeast - 1), kLeast - 1 + kHuge) - (kLeast - 1) + (b & 0x8000u ? kHalf : 0);
 }
 
-// The same for two bf16 values at once, as byte offsets.
+// The same for two bf16 values at once, as byte offsets of bins of `size` bytes.
+template <int size>
 __device__ __forceinline__ uint32_t table_offsets(uint32_t w) {
+  static_assert(size * kTable < 65536, "16 bits");
   typedef uint16_t halves __attribute__((ext_vector_type(2)));
   const halves m = __builtin_bit_cast(halves, w & 0x7fff7fffu), sign = __builtin_bit_cast(halves, w) >> 15;
   const halves lo = {kLeast - 1, kLeast - 1}, hi = {kLeast - 1 + kHuge, kLeast - 1 + kHuge};
-  const halves half = {4 * kHalf, 4 * kHalf};
+  const halves half = {size * kHalf, size * kHalf}, bytes = {size, size};
   const halves t = __builtin_elementwise_min(__builtin_elementwise_max(m, lo), hi) - lo;
-  return __builtin_bit_cast(uint32_t, (halves)((t << 2) + sign * half));
+  return __builtin_bit_cast(uint32_t, (halves)(t * bytes + sign * half));
 }
 
 // The upper 16 bits that a bin stands for, and the bin at a place in descending order of values (zeros of both
@@ -476,6 +345,177 @@ __device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, ui
   b.above_m = sh.found[2];
   __syncthreads();
   return b;
+}
+
+// ---- the draw -------------------------------------------------------------------
+
+// The token of a row that a cut leaves: one pass for the chunks' weights above the cut and
+// their ties at it, a scan, and one chunk again.  tabled (bf16, all values with weight in the table, the cut's not
+// zero): many are kept, and the weights of values above the cut come from the table, others' as 0.
+template <typename T, int kT>
+__device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
+                                    bool tabled, Shared<T>& sh) {
+  constexpr int n = Elem<T>::kVec, kPer = kChunks > kT ? kChunks / kT : 1;
+  constexpr uint32_t kNinf = kNinfOf<T>;
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int size = kChunk * factor, chunks = (V + size - 1) / size;
+  const bool all = cut.key == 0;
+  const float value = all ? kNegInf : order_value(cut.key);
+  const uint64_t at_cut = all ? 0 : weight(value);
+  __syncthreads();
+  if constexpr (sizeof(T) == 2) {
+    if (tabled) {
+      for (int i = threadIdx.x; i < kTable; i += kT) {
+        const float x = __uint_as_float(table_value(i) << 16);
+        const bool in = i != kHuge && i != kTable - 1;  // beyond the table: none, or without weight
+        sh.mass[i] = in && x > value && x <= (float)weight.top ? weight(x) : 0;
+      }
+      __syncthreads();
+    }
+  }
+  // Ties' place in the table; a cut at no bf16 value (min-p's) has none.
+  const uint32_t tie_at = all || (__float_as_uint(value) & 0xffffu) ? ~0u : 8u * (uint32_t)table_bin(__float_as_uint(value) >> 16);
+  // A wave's chunks, two vectors at a time, the next ones on their way.
+  constexpr int kGroup = 2;
+  const int steps = (size + kWave * n * kGroup - 1) / (kWave * n * kGroup);  // of a chunk
+  u32x4 next[kGroup];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int id = base + (g * kWave + lane) * n;
+      if (id + n <= V) next[g] = load16<T, false, false>(row + id);
+      else next[g] = id < V ? *reinterpret_cast<const u32x4*>(sh.end) : u32x4{kNinf, kNinf, kNinf, kNinf};
+    }
+  };
+  if (w < chunks) fetch(w * size);
+  for (int c = w; c < chunks; c += kT / kWave) {
+    uint64_t s = 0;
+    uint32_t ties = 0;
+    for (int step = 0; step < steps; ++step) {
+      u32x4 raw[kGroup];
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) raw[g] = next[g];
+      const bool more = step + 1 < steps;
+      const long long base = more ? (long long)c * size + (step + 1) * (kWave * n * kGroup) : (long long)(c + kT / kWave) * size;
+      if (more || base < V) fetch((int)base);
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+        if constexpr (sizeof(T) == 2) {
+          if (tabled) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t at = table_offsets<8>(raw[g][q]), lo = at & 0xffffu, hi = at >> 16;
+              const uint8_t* table = reinterpret_cast<const uint8_t*>(sh.mass);
+              s += *reinterpret_cast<const uint64_t*>(table + lo) + *reinterpret_cast<const uint64_t*>(table + hi);
+              ties += (lo == tie_at ? 1 : 0) + (hi == tie_at ? 1 : 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // a vector at a time: registers
+            continue;
+          }
+        }
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            s += weight(raw_elem<T>(raw, g * n + i));
+            if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+          }
+          continue;
+        }
+        // Few are kept: the lanes' next ones together, until no lane has one.
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) hits |= raw_elem<T>(raw, g * n + i) >= value ? 1u << i : 0u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[g][q]));  // unpacked again where one is picked: registers
+        while (__any(hits != 0)) {
+          const int at = __ffs(hits) - 1;
+          float y = raw_elem<T>(raw, g * n);
+#pragma unroll
+          for (int i = 1; i < n; ++i) y = at == i ? raw_elem<T>(raw, g * n + i) : y;
+          if (hits != 0) {
+            if (y == value) ++ties;
+            else s += weight(y);
+          }
+          hits &= hits - 1;
+        }
+      }
+    }
+    s = wave_sum64(s);
+    ties = (uint32_t)wave_sum64(ties);
+    if (lane == 0) sh.chunk_sum[c] = s, sh.chunk_tie[c] = ties;
+  }
+  __syncthreads();
+  // Thread t has the chunks kPer t and on; ties are kept up to cut.ties of them.
+  uint64_t own[kPer], tied[kPer], ties = 0, sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = (int)threadIdx.x * kPer + i;
+    own[i] = c < chunks ? sh.chunk_sum[c] : 0;
+    tied[i] = c < chunks ? sh.chunk_tie[c] : 0;
+    ties += tied[i];
+  }
+  uint64_t ties_before = block_before64<kT>(ties, sh);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint64_t room = cut.ties > ties_before ? cut.ties - ties_before : 0;
+    own[i] += (tied[i] < room ? tied[i] : room) * at_cut;
+    ties_before += tied[i];
+    sum += own[i];
+  }
+  ties_before -= ties;
+  const uint64_t total = block_sum64<kT>(sum, sh);
+  const uint64_t target = (uint64_t)((double)u * (double)total);
+  uint64_t before = block_before64<kT>(sum, sh);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (before <= target && target < before + own[i]) {
+      sh.found[0] = threadIdx.x * kPer + i;
+      sh.found[1] = before;
+      sh.found[2] = ties_before;
+    }
+    before += own[i];
+    ties_before += tied[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    uint64_t at = sh.found[1], tie_at = sh.found[2];
+    for (int id0 = (int)sh.found[0] * size; id0 < V; id0 += kWave * n) {
+      const int id = id0 + lane * n;
+      float x[n];
+      load_row(row, V, min(id, V - 1), x);
+      uint64_t v[n], t = 0, s = 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) t += id + i < V && x[i] == value ? 1 : 0;
+      const uint64_t ties_to = tie_at + wave_scan64(t);
+      uint64_t rank = ties_to - t;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool in = id + i < V;
+        v[i] = in && x[i] > value ? weight(x[i]) : in && x[i] == value && rank++ < cut.ties ? at_cut : 0;
+        s += v[i];
+        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+      }
+      const uint64_t up_to = at + wave_scan64(s);
+      const uint64_t hit = __ballot(up_to > target);
+      if (hit != 0) {
+        if (lane == __ffsll((unsigned long long)hit) - 1) {
+          uint64_t y = up_to - s;
+          int token = id;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            y += v[i];
+            if (y <= target) token = id + i + 1;
+          }
+          sh.found[3] = token;
+        }
+        break;
+      }
+      at = __shfl((unsigned long long)up_to, kWave - 1);
+      tie_at = __shfl((unsigned long long)ties_to, kWave - 1);
+    }
+  }
+  __syncthreads();
+  return (int)sh.found[3];
 }
 
 // ---- candidates -----------------------------------------------------------------
@@ -594,15 +634,15 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   const float p = a.set.top_p.rows ? a.set.top_p.rows[r] : a.set.top_p.all;
   const float m = a.set.min_p.rows ? a.set.min_p.rows[r] : a.set.min_p.all;
   const float u = a.uniforms[r];
-  const int factor = (int)(((long long)V + (long long)kChunk * kBins - 1) / ((long long)kChunk * kBins));
+  const int factor = (int)(((long long)V + (long long)kChunk * kChunks - 1) / ((long long)kChunk * kChunks));
   const bool greedy = temperature == 0.0f, by_k = k >= 1 && k < V, by_p = p < 1.0f, by_m = m > 0.0f;
-  const double s64 = 1.4426950408889634074 / (double)temperature;
+  const double s64 = uniform(1.4426950408889634074 / (double)temperature);
   // Few tokens and min-p alone: what a cut can keep is known while the row is read, and listed.  Other cuts
   // need the row's values first, in a table.
   const bool lists = !greedy && (by_k ? k <= kT : by_m && !by_p);
-  const bool tables = !greedy && (by_k ? k > kT : by_p);
-  const bool counts = tables && (sizeof(T) == 2 || by_k);
-  const double span_m = by_m ? (double)temperature * log((double)fminf(m, 1.0f)) : 0.0;
+  const bool tables = !greedy && !lists;
+  const bool counts = tables && (by_k || (by_p && sizeof(T) == 2));
+  const double span_m = uniform(by_m ? (double)temperature * log((double)fminf(m, 1.0f)) : 0.0);
   // The least float at or above the min-p cut.
   auto least_kept = [&](float top) {
     const double least = (double)top + span_m;
@@ -683,7 +723,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
             const halves one = {1, 1};
             smallest = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
                 __builtin_bit_cast(halves, smallest), (halves)(__builtin_bit_cast(halves, raw[v][q] & 0x7fff7fffu) - one)));
-            const uint32_t at = table_offsets(raw[v][q]);
+            if (!counts) continue;
+            const uint32_t at = table_offsets<4>(raw[v][q]);
             atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sh.table) + (at & 0xffffu)), 1u);
             atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sh.table) + (at >> 16)), 1u);
           } else {
@@ -691,7 +732,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
             if (counts) atomicAdd(&sh.table[table_bin(raw[v][q] >> 16)], 1u);
           }
         }
-        if constexpr (sizeof(T) == 4) top = fmaxf(top, raw_max<T>(raw, v));
+        if (sizeof(T) == 4 || !counts) top = fmaxf(top, raw_max<T>(raw, v));
       }
       continue;
     }
@@ -702,8 +743,6 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) asm("" : "+v"(raw[v][q]));  // unpacked again where they are used again: registers
     }
-    if (!lists && !greedy) top = fmaxf(top, own);  // of the thread; the others' follow behind the loop
-    if (!lists && !greedy) continue;
     const float mine = wave_max(own);
     if (lane == 0) sh.top[turn][wave] = mine;
     __syncthreads();
@@ -768,8 +807,9 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     if (threadIdx.x == 0) a.tokens[r] = (int)(uint32_t)sh.best;
     return;
   }
-  const Weight weight{(double)top, s64, a.F};
-  const float least = by_m ? least_kept(top) : kNegInf;
+  top = uniform(top);
+  const Weight weight{uniform((double)top), s64, a.F};
+  const float least = uniform(by_m ? least_kept(top) : kNegInf);
   Cut cut;
   cut.key = 0;
   cut.ties = ~0ull;
@@ -777,14 +817,15 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     if (c.key > cut.key) cut = c;
     else if (c.key == cut.key && c.ties < cut.ties) cut.ties = c.ties;
   };
-  bool done = !tables && !lists, listed = lists;
+  bool done = !by_k && !by_p, listed = lists, tabled = false;
   uint64_t row_mass = 0;
   if (tables) {
     // Values outside the table that have weight, or that a cut may meet, leave the row to its digits.
     const bool weightless = top > -1024.0f && weight(-1024.0f) == 0;
     const int low = counts ? (int)sh.table[kTable - 1] : sh.low;  // values of -2^10 and below, masked ones among them
     const bool plain = top < 1024.0f && !sh.tiny && (low == 0 || weightless) && (!by_k || k <= V - low);
-    if (plain && sizeof(T) == 2) {
+    uint64_t kept = (uint64_t)V;  // at most
+    if (plain && sizeof(T) == 2 && !done) {
       // A bin is a value: the cuts are known.
       auto mass = [&](int bin, uint32_t c) { return (uint64_t)c * weight(__uint_as_float(table_value(bin) << 16)); };
       uint64_t all = 0;
@@ -794,6 +835,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         const float x = __uint_as_float(table_value(b.bin) << 16);
         c.key = order_bits(x);
         c.ties = (uint64_t)k - b.above_n;
+        kept = (uint64_t)k;
         all = c.mass = b.above_m + c.ties * weight(x);
         narrow(c);
       }
@@ -808,10 +850,13 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         c.key = order_bits(x);
         c.ties = (goal - b.above_m + w - 1) / w;
         c.mass = 0;
+        kept = b.above_n + c.ties < kept ? b.above_n + c.ties : kept;
         narrow(c);
       }
       done = true;
-    } else if (plain && sizeof(T) == 4) {
+    }
+    tabled = plain && sizeof(T) == 2 && kept > (uint64_t)V / kSparse;
+    if (plain && sizeof(T) == 4 && !done) {
       // A bin's values share 16 bits: the cut's bin is known, and its tokens, or with the ones above all that can be
       // kept, are listed.
       auto least_of = [&](int bin) { return __uint_as_float(table_value(bin) << 16 | (bin >= kHalf ? 0xffffu : 0u)); };
@@ -1027,7 +1072,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     c.mass = 0;
     narrow(c);
   }
-  const int token = draw<T, kT>(row, V, factor, weight, cut, u, sh);
+  if (cut.key == order_bits(0.0f)) tabled = false;  // zeros of both signs are its ties
+  const int token = draw<T, kT>(row, V, factor, weight, cut, u, tabled, sh);
   if (threadIdx.x == 0) a.tokens[r] = token;
 }
 
