@@ -108,7 +108,7 @@ struct Shared {
   };
   uint64_t chunk_sum[kChunks];   // weights above the cut
   uint32_t chunk_tie[kChunks];   // and tokens at it
-  uint64_t wave[16];
+  uint64_t wave[2][16];
   uint64_t found[4];
   uint64_t votes[2][16];
   float lanes[16][kWave];
@@ -138,30 +138,22 @@ __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
   return (uint64_t)(uint32_t)dpp::lane63((int)(v >> 32)) << 32 | (uint32_t)dpp::lane63((int)v);
 }
 
-// Sum over the block; every thread gets it.
+// Sum of the threads before this one, and of all.  The waves' sums alternate between two buffers (turn), so that one
+// barrier is enough.
 template <int kT, typename T>
-__device__ __forceinline__ uint64_t block_sum64(uint64_t v, Shared<T>& sh) {
-  v = wave_sum64(v);
-  __syncthreads();
-  if ((threadIdx.x & (kWave - 1)) == 0) sh.wave[threadIdx.x / kWave] = v;
-  __syncthreads();
-  uint64_t r = 0;
-#pragma unroll
-  for (int i = 0; i < kT / kWave; ++i) r += sh.wave[i];
-  return r;
-}
-
-// Sum of the threads before this one.
-template <int kT, typename T>
-__device__ __forceinline__ uint64_t block_before64(uint64_t v, Shared<T>& sh) {
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+__device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t& total, int& turn, Shared<T>& sh) {
+  constexpr int kWaves = kT / kWave;
+  const int lane = threadIdx.x & (kWave - 1), w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const uint64_t up_to = wave_scan64(v);
+  if (lane == kWave - 1) sh.wave[turn][w] = up_to;
   __syncthreads();
-  if (lane == kWave - 1) sh.wave[w] = up_to;
-  __syncthreads();
-  uint64_t r = up_to - v;
-  for (int i = 0; i < w; ++i) r += sh.wave[i];
-  return r;
+  const uint64_t all = wave_scan64(lane < kWaves ? sh.wave[turn][lane] : 0);
+  turn ^= 1;
+  auto at = [&](int i) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(all >> 32), i) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)all, i);
+  };
+  total = at(kWaves - 1);
+  return (w > 0 ? at(w - 1) : 0) + up_to - v;
 }
 
 // The vector of tokens id .. id + n - 1 of a row; -inf past its end.
@@ -205,7 +197,7 @@ struct Cut {
 // share >= 0: the target is that share of the row's weight, known after the first.
 template <typename T, int kT>
 __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weight, bool by_mass, uint64_t target,
-                                        double share, Shared<T>& sh) {
+                                        double share, int& turn, Shared<T>& sh) {
   uint32_t prefix = 0;
   uint64_t above_n = 0, above_m = 0;
   int shift = 21;
@@ -236,11 +228,13 @@ __device__ __forceinline__ Cut find_cut(const T* row, int V, const Weight& weigh
       n_all += n[i];
       m_all += m[i];
     }
+    uint64_t row_n, row_m;
+    uint64_t n_before = above_n + block_scan64<kT>(n_all, row_n, turn, sh);
+    uint64_t m_before = above_m + block_scan64<kT>(m_all, row_m, turn, sh);
     if (level == 0 && share >= 0.0) {
-      const double t = __builtin_ceil(share * (double)block_sum64<kT>(m_all, sh));
+      const double t = __builtin_ceil(share * (double)row_m);
       target = t < 1.0 ? 1 : (uint64_t)t;
     }
-    uint64_t n_before = above_n + block_before64<kT>(n_all, sh), m_before = above_m + block_before64<kT>(m_all, sh);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint64_t lo = by_mass ? m_before : n_before, hi = lo + (by_mass ? m[i] : n[i]);
@@ -304,7 +298,7 @@ struct Border {
 // The bin, from the highest down, at which counts (by_mass false) or weights reach target, or with share >=
 // 0 that share of the total weight.  count(bin) and mass(bin, count) give a bin's; at most `target` must be there.
 template <int kT, typename T, typename Bin, typename Mass>
-__device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, uint64_t target, double share, Shared<T>& sh, Mass mass) {
+__device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, uint64_t target, double share, int& turn, Shared<T>& sh, Mass mass) {
   constexpr int kPer = (kTable + kT - 1) / kT;
   uint64_t n = 0, m = 0;
   const int first = (int)threadIdx.x * kPer;
@@ -316,12 +310,12 @@ __device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, ui
     m += c != 0 ? mass(bin, c) : 0;
   }
   Border b;
-  b.total_m = block_sum64<kT>(m, sh);
+  uint64_t row_n;
+  uint64_t n_before = block_scan64<kT>(n, row_n, turn, sh), m_before = block_scan64<kT>(m, b.total_m, turn, sh);
   if (share >= 0.0) {
     const double t = __builtin_ceil(share * (double)b.total_m);
     target = t < 1.0 ? 1 : (uint64_t)t;
   }
-  uint64_t n_before = block_before64<kT>(n, sh), m_before = block_before64<kT>(m, sh);
   const uint64_t lo = by_mass ? m_before : n_before, hi = lo + (by_mass ? m : n);
   if (lo < target && target <= hi) {
 #pragma unroll 1
@@ -354,7 +348,7 @@ __device__ __forceinline__ Border find_border(const Bin* table, bool by_mass, ui
 // zero): many are kept, and the weights of values above the cut come from the table, others' as 0.
 template <typename T, int kT>
 __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weight& weight, const Cut& cut, float u,
-                                    bool tabled, Shared<T>& sh) {
+                                    bool tabled, int& turn, Shared<T>& sh) {
   constexpr int n = Elem<T>::kVec, kPer = kChunks > kT ? kChunks / kT : 1;
   constexpr uint32_t kNinf = kNinfOf<T>;
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
@@ -454,7 +448,8 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
     tied[i] = c < chunks ? sh.chunk_tie[c] : 0;
     ties += tied[i];
   }
-  uint64_t ties_before = block_before64<kT>(ties, sh);
+  uint64_t row_ties, total;
+  uint64_t ties_before = block_scan64<kT>(ties, row_ties, turn, sh);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const uint64_t room = cut.ties > ties_before ? cut.ties - ties_before : 0;
@@ -463,9 +458,8 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
     sum += own[i];
   }
   ties_before -= ties;
-  const uint64_t total = block_sum64<kT>(sum, sh);
+  uint64_t before = block_scan64<kT>(sum, total, turn, sh);
   const uint64_t target = (uint64_t)((double)u * (double)total);
-  uint64_t before = block_before64<kT>(sum, sh);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (before <= target && target < before + own[i]) {
@@ -477,42 +471,38 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
     ties_before += tied[i];
   }
   __syncthreads();
-  if (threadIdx.x < kWave) {
-    uint64_t at = sh.found[1], tie_at = sh.found[2];
-    for (int id0 = (int)sh.found[0] * size; id0 < V; id0 += kWave * n) {
-      const int id = id0 + lane * n;
-      float x[n];
-      load_row(row, V, min(id, V - 1), x);
-      uint64_t v[n], t = 0, s = 0;
+  // That chunk's tokens, a vector per thread at a time.
+  const int first = (int)sh.found[0] * size, end = (int)min((long long)V, (long long)first + size);
+  uint64_t at = sh.found[1], ties_at = sh.found[2];
+#pragma unroll 1
+  for (int base = first; base < end; base += kT * n) {
+    const int id = base + (int)threadIdx.x * n;
+    const bool mine = id < end;
+    float x[n];
+    load_row(row, V, min(id, V - 1), x);
+    uint64_t v[n], t = 0, s = 0, all_ties, all_mass;
 #pragma unroll
-      for (int i = 0; i < n; ++i) t += id + i < V && x[i] == value ? 1 : 0;
-      const uint64_t ties_to = tie_at + wave_scan64(t);
-      uint64_t rank = ties_to - t;
+    for (int i = 0; i < n; ++i) t += mine && id + i < V && x[i] == value ? 1 : 0;
+    uint64_t rank = ties_at + block_scan64<kT>(t, all_ties, turn, sh);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool in = mine && id + i < V;
+      v[i] = in && x[i] > value ? weight(x[i]) : in && x[i] == value && rank++ < cut.ties ? at_cut : 0;
+      s += v[i];
+      if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+    }
+    uint64_t y = at + block_scan64<kT>(s, all_mass, turn, sh);
+    if (y <= target && target < y + s) {
+      int token = id;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
-        const bool in = id + i < V;
-        v[i] = in && x[i] > value ? weight(x[i]) : in && x[i] == value && rank++ < cut.ties ? at_cut : 0;
-        s += v[i];
-        if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // two weights at a time: registers
+        y += v[i];
+        if (y <= target) token = id + i + 1;
       }
-      const uint64_t up_to = at + wave_scan64(s);
-      const uint64_t hit = __ballot(up_to > target);
-      if (hit != 0) {
-        if (lane == __ffsll((unsigned long long)hit) - 1) {
-          uint64_t y = up_to - s;
-          int token = id;
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            y += v[i];
-            if (y <= target) token = id + i + 1;
-          }
-          sh.found[3] = token;
-        }
-        break;
-      }
-      at = __shfl((unsigned long long)up_to, kWave - 1);
-      tie_at = __shfl((unsigned long long)ties_to, kWave - 1);
+      sh.found[3] = token;
     }
+    at += all_mass;
+    ties_at += all_ties;
   }
   __syncthreads();
   return (int)sh.found[3];
@@ -830,7 +820,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       auto mass = [&](int bin, uint32_t c) { return (uint64_t)c * weight(__uint_as_float(table_value(bin) << 16)); };
       uint64_t all = 0;
       if (by_k) {
-        const Border b = find_border<kT>(sh.table, false, (uint64_t)k, -1.0, sh, mass);
+        const Border b = find_border<kT>(sh.table, false, (uint64_t)k, -1.0, turn, sh, mass);
         Cut c;
         const float x = __uint_as_float(table_value(b.bin) << 16);
         c.key = order_bits(x);
@@ -841,7 +831,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       }
       if (by_p) {
         const double t = __builtin_ceil((double)p * (double)all);
-        const Border b = find_border<kT>(sh.table, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh, mass);
+        const Border b = find_border<kT>(sh.table, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, turn, sh, mass);
         Cut c;
         const float x = __uint_as_float(table_value(b.bin) << 16);
         const uint64_t w = weight(x);
@@ -883,7 +873,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       Border b;
       uint64_t goal = (uint64_t)k;
       if (by_k) {
-        b = find_border<kT>(sh.table, false, goal, -1.0, sh, [](int, uint32_t) { return (uint64_t)0; });
+        b = find_border<kT>(sh.table, false, goal, -1.0, turn, sh, [](int, uint32_t) { return (uint64_t)0; });
       } else {
         __syncthreads();
         for (int i = threadIdx.x; i < kTable; i += kT) sh.mass[i] = 0;
@@ -907,7 +897,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         if (threadIdx.x == 0) sh.mass[0] += sh.mass[kHalf], sh.mass[kHalf] = 0;
         __syncthreads();
         const double share = p > 0.0f ? (double)p : 0.0;
-        b = find_border<kT>(sh.mass, true, 1, share, sh, [](int, uint64_t m) { return m; });
+        b = find_border<kT>(sh.mass, true, 1, share, turn, sh, [](int, uint64_t m) { return m; });
         row_mass = b.total_m;
         const double t = __builtin_ceil(share * (double)row_mass);
         goal = t < 1.0 ? 1 : (uint64_t)t;
@@ -930,7 +920,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
             own[i] = i < per && at < in_bin ? by_k ? 1 : weight(order_value(~(uint32_t)(sh.list[at] >> 32))) : 0;
             sum += own[i];
           }
-          uint64_t before = (by_k ? b.above_n : b.above_m) + block_before64<kT>(sum, sh);
+          uint64_t in_all;
+          uint64_t before = (by_k ? b.above_n : b.above_m) + block_scan64<kT>(sum, in_all, turn, sh);
 #pragma unroll
           for (int i = 0; i < kList / kT; ++i) {
             if (before < goal && goal <= before + own[i]) sh.cut = (int)threadIdx.x * per + i;
@@ -984,7 +975,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
       __builtin_amdgcn_sched_barrier(0);  // one at a time: registers
     }
     if (threadIdx.x == 0) sh.cut = n, sh.found[0] = row_mass;
-    const uint64_t before = block_before64<kT>(sum, sh);
+    uint64_t all;
+    const uint64_t before = block_scan64<kT>(sum, all, turn, sh);
     uint64_t up_to = before;
     const int nk = by_k ? min(k, n) : n;
     if (by_k && by_p) {
@@ -1042,9 +1034,9 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
         sum += own[i];
         __builtin_amdgcn_sched_barrier(0);
       }
-      const uint64_t total = block_sum64<kT>(sum, sh);
+      uint64_t total;
+      uint64_t from = block_scan64<kT>(sum, total, turn, sh);
       const uint64_t goal = (uint64_t)((double)u * (double)total);
-      uint64_t from = block_before64<kT>(sum, sh);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         if (from <= goal && goal < from + own[i]) a.tokens[r] = (int)id[i];
@@ -1057,13 +1049,13 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   // Cuts that neither the list nor the table gave: digit by digit.
   uint64_t mass = 0;
   if (by_k && !done) {
-    const Cut c = find_cut<T, kT>(row, V, weight, false, (uint64_t)k, -1.0, sh);
+    const Cut c = find_cut<T, kT>(row, V, weight, false, (uint64_t)k, -1.0, turn, sh);
     mass = c.mass;
     narrow(c);
   }
   if (by_p && !done) {
     const double t = by_k ? __builtin_ceil((double)p * (double)mass) : 0.0;
-    narrow(find_cut<T, kT>(row, V, weight, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, sh));
+    narrow(find_cut<T, kT>(row, V, weight, true, t < 1.0 ? 1 : (uint64_t)t, by_k ? -1.0 : p > 0.0f ? (double)p : 0.0, turn, sh));
   }
   if (by_m) {
     Cut c;
@@ -1073,7 +1065,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
     narrow(c);
   }
   if (cut.key == order_bits(0.0f)) tabled = false;  // zeros of both signs are its ties
-  const int token = draw<T, kT>(row, V, factor, weight, cut, u, tabled, sh);
+  const int token = draw<T, kT>(row, V, factor, weight, cut, u, tabled, turn, sh);
   if (threadIdx.x == 0) a.tokens[r] = token;
 }
 
