@@ -134,9 +134,10 @@ struct Rows {
 };
 
 // The shape of a kernel's operands.
-template <typename T, bool kQ, int DP, int MT>
+template <typename T, bool kQ, int DP, int MT, bool kWhole>
 struct Shape {
   static constexpr bool kF32 = std::is_same<T, float>::value;
+  static constexpr bool kAll = kWhole;                   // heads of DP values, no less
   static constexpr int U = kF32 && DP == 256 ? 1 : 2;    // keys / 16 of a tile (registers)
   static constexpr int kKeys = 16 * U;
   static constexpr int kSlots = 4 * U;                   // keys of a tile that a lane holds weights of
@@ -165,7 +166,7 @@ __device__ __forceinline__ void load_keys(const Rows& r, int last, int D, int la
       for (int e = 0; e < S::KW; e += n) {
         const int d = s * 4 * S::KW + (lane >> 4) * S::KW + e;
         Frag<T, n> f;
-        load_values<T, n>(r.base + (row + (uint32_t)((d < D ? d : 0) * kEs<T>)), f);
+        load_values<T, n>(r.base + (row + (uint32_t)((S::kAll || d < D ? d : 0) * kEs<T>)), f);
 #pragma unroll
         for (int i = 0; i < Frag<T, n>::kWords; ++i) k[u][s].w[e * kEs<T> / 4 + i] = f.w[i];
       }
@@ -181,7 +182,7 @@ __device__ __forceinline__ void load_rows(const Rows& r, int last, int D, int la
 #pragma unroll
     for (int s = 0; s < S::VS; ++s) {
       const int d = s * 16 * S::CW + (lane & 15) * S::CW;
-      load_values<T, S::CW>(r.base + (row + (uint32_t)((d < D ? d : 0) * kEs<T>)), v[i][s]);
+      load_values<T, S::CW>(r.base + (row + (uint32_t)((S::kAll || d < D ? d : 0) * kEs<T>)), v[i][s]);
     }
   }
 }
@@ -210,8 +211,8 @@ __device__ __forceinline__ void load_key_codes(const Rows& r, int nb, int head, 
 #pragma unroll
     for (int s = 0; s < S::KS; ++s) {
       const int d = s * 64 + (lane >> 4) * 16;
-      if (D % 16 == 0) {
-        const u32x4 v = *reinterpret_cast<const u32x4_any1*>(r.base + (row + (uint32_t)(d < D ? d : 0)));
+      if (S::kAll || D % 16 == 0) {
+        const u32x4 v = *reinterpret_cast<const u32x4_any1*>(r.base + (row + (uint32_t)(S::kAll || d < D ? d : 0)));
 #pragma unroll
         for (int q = 0; q < 4; ++q) c.w[u][s][q] = v[q];
       } else {
@@ -258,7 +259,7 @@ __device__ __forceinline__ void load_row_codes(const Rows& r, int nb, int head, 
 #pragma unroll
     for (int s = 0; s < S::VS; ++s) {
       const int d = s * 16 * S::CW + (lane & 15) * S::CW;
-      const int at = d < D ? d : 0;
+      const int at = S::kAll || d < D ? d : 0;
       load_codes<S::CW>(r.base + (key * r.stride + (uint32_t)at), c.w[i][s]);
       c.scale[i][s] = r.scales[key * (uint32_t)nb + (uint32_t)((head + at) >> 7)];
     }
@@ -411,9 +412,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 template <int DP>
 constexpr int kPad = DP + 4;
 
-template <typename T, bool kQ, int DP, int MT>
+template <typename T, bool kQ, int DP, int MT, bool kWhole>
 __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2) tree_attention_kernel(AttnArgs a) {
-  typedef Shape<T, kQ, DP, MT> S;
+  typedef Shape<T, kQ, DP, MT, kWhole> S;
   __shared__ uint64_t line_of[kMaxNodes];
   __shared__ int depth_of[kMaxNodes];
   __shared__ float2 stat[kWavesPerBlock][16 * MT];
@@ -427,7 +428,8 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
   const int split = (int)(item % (uint32_t)a.split);
   const int h = (int)(item / (uint32_t)a.split % (uint32_t)a.Hkv);
   const int b = (int)(item / (uint32_t)a.split / (uint32_t)a.Hkv);
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, g = lane >> 4;
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);  // scalar, and with it the tiles' addresses
   const int length = a.cache_len[b];
   const bool valid = length >= 0 && length <= a.L;
   const int n = valid ? length : 0;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
         constexpr int w = S::KW > 8 ? 8 : S::KW;
         const int d = s * 4 * S::KW + g * S::KW + e;
         Frag<T, w> f;
-        if (d < a.D) load_values<T, w>(p + d * kEs<T>, f);
+        if (kWhole || d < a.D) load_values<T, w>(p + d * kEs<T>, f);
         else clear(f);
 #pragma unroll
         for (int i = 0; i < Frag<T, w>::kWords; ++i) q[t][s].w[e * kEs<T> / 4 + i] = f.w[i];
@@ -507,13 +509,13 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
   CacheKeys k;
   auto fetch_keys = [&](int tile) {
     int j0;
-    const int last = place(tile, j0);
+    const int last = kWhole ? (place(tile, j0), kKeys - 1) : place(tile, j0);  // a constant leaves the offsets in registers
     const Rows r = rows_at(a.k_cache, a.k_scales, j0);
     if constexpr (kQ) load_key_codes<S>(r, a.nb, head, last, a.D, one_scale, lane, k);
     else load_keys<S, T>(r, last, a.D, lane, k);
   };
   auto add_key = [&](Frag<T, S::KW>& f, int u, int s, f32x4 (&x)[MT][S::U]) {
-    if (a.D < DP) cut_key<S, T>(a.D, s, lane, f);
+    if constexpr (!kWhole) cut_key<S, T>(a.D, s, lane, f);
 #pragma unroll
     for (int t = 0; t < MT; ++t) x[t][u] = product<T, S::KW>(f, q[t][s], s == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[t][u]);
   };
@@ -563,10 +565,16 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
     }
   };
 
-  if (from + wave < min(to, tiles_cache)) fetch_keys(from + wave);
-  for (int tile = from + wave; tile < min(to, tiles_cache); tile += kWavesPerBlock) {
+  // Tiles that every row sees whole: of the first entries, and behind the window's edge.
+  const int edge_tiles = edge >= low ? (edge - low) / kKeys + 1 : 0;
+  const int first_end = max(from, min(to, first / kKeys));
+  const int later = min(max(from, tiles_first + edge_tiles), to), later_end = max(later, min(to, tiles_first + (n - low) / kKeys));
+  const int count = first_end - from + later_end - later;
+  auto whole_tile = [&](int i) { return i < first_end - from ? from + i : later + i - (first_end - from); };
+  if (wave < count) fetch_keys(whole_tile(wave));
+  for (int i = wave; i < count; i += kWavesPerBlock) {
     int j0;
-    const int last = place(tile, j0);
+    const int last = kWhole ? (place(whole_tile(i), j0), kKeys - 1) : place(whole_tile(i), j0);
     const Rows rows = rows_at(a.v_cache, a.v_scales, j0);
     typedef typename std::conditional<kQ, ValueCodes<S>, typename S::Values>::type CacheValues;
     CacheValues raw;
@@ -587,104 +595,89 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
         }
       }
     __builtin_amdgcn_sched_barrier(0);
-    if (tile + kWavesPerBlock < min(to, tiles_cache)) fetch_keys(tile + kWavesPerBlock);
-    const bool masked = last < kKeys - 1 || (tile >= tiles_first && j0 <= edge);
-    uint32_t seen[MT];
-    if (masked) {
+    if (i + kWavesPerBlock < count) fetch_keys(whole_tile(i + kWavesPerBlock));
+    const uint32_t none[MT] = {};
+    weigh<S, MT, false>(x, none, a.c, z);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;  // up to here, but for the first
-        seen[t] = 0;
+    for (int s = 0; s < S::VS; ++s) {
+      Frag<T, S::CW> piece[S::kSlots];
 #pragma unroll
-        for (int i = 0; i < S::kSlots; ++i) {
-          const int off = key_of(i, lane), j = j0 + off;
-          seen[t] |= off <= last && (j > hidden || j < a.sinks) ? 1u << i : 0u;
+      for (int i8 = 0; i8 < S::kSlots; ++i8) {
+        if constexpr (kQ) {
+          const float sc = scale_of(raw.scale[i8][s]);
+          decode<T, S::CW>(raw.w[i8][s], &sc, piece[i8]);
+        } else {
+          piece[i8] = raw[i8][s];
         }
       }
-      weigh<S, MT, true>(x, seen, a.c, z);
-    } else {
-      weigh<S, MT, false>(x, seen, a.c, z);
-    }
-    if constexpr (kQ) {
-      typename S::Values v;
-#pragma unroll
-      for (int i = 0; i < S::kSlots; ++i)
-#pragma unroll
-        for (int s = 0; s < S::VS; ++s) {
-          const float sc = scale_of(raw.scale[i][s]);
-          decode<T, S::CW>(raw.w[i][s], &sc, v[i][s]);
-        }
-      uint32_t bad = 0;
-      if (masked) bad = take_out(v);
-#pragma unroll
-      for (int s = 0; s < S::VS; ++s) {
-        Frag<T, S::CW> piece[S::kSlots];
-#pragma unroll
-        for (int i = 0; i < S::kSlots; ++i) piece[i] = v[i][s];
-        add_piece<S, T, MT>(piece, s, x, z);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (masked)
-        add_others(bad, seen, [&](int key, int d) {
-          const uint32_t at = (uint32_t)min(key, last);
-          uint32_t w[S::CW / 4];
-          load_codes<S::CW>(rows.base + (at * rows.stride + (uint32_t)d), w);
-          const float sc = scale_of(rows.scales[at * (uint32_t)a.nb + (uint32_t)((head + d) >> 7)]);
-          Frag<T, S::CW> f;
-          decode<T, S::CW>(w, &sc, f);
-          return f;
-        });
-    } else {
-      uint32_t bad = 0;
-      if (masked) bad = take_out(raw);
-#pragma unroll
-      for (int s = 0; s < S::VS; ++s) {
-        Frag<T, S::CW> piece[S::kSlots];
-#pragma unroll
-        for (int i = 0; i < S::kSlots; ++i) piece[i] = raw[i][s];
-        add_piece<S, T, MT>(piece, s, x, z);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (masked)
-        add_others(bad, seen, [&](int key, int d) {
-          Frag<T, S::CW> f;
-          load_values<T, S::CW>(rows.base + ((uint32_t)min(key, last) * rows.stride + (uint32_t)(d * kEs<T>)), f);
-          return f;
-        });
+      add_piece<S, T, MT>(piece, s, x, z);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // The tree's own entries: a node sees its ancestors and itself.
+  // The others: ends, entries at the window's edge, and the tree's own, of which a node sees its ancestors and itself.
 #pragma unroll 1
   for (int tile = from + wave; tile < to; tile += kWavesPerBlock) {
-    if (tile < tiles_cache) continue;
-    const int j0 = (tile - tiles_cache) * kKeys, last = min(kKeys, a.N - j0) - 1;
-    const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
-    const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
-    const Rows vr{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
-    typename S::Keys own;
-    load_keys<S, T>(kr, last, a.D, lane, own);
+    if (tile < first_end || (tile >= later && tile < later_end)) continue;
+    const bool own = tile >= tiles_cache;
+    int j0, last;
+    typename S::Keys key;
+    typename S::Values v;
     f32x4 x[MT][S::U];
+    Rows vr;
+    if (own) {
+      j0 = (tile - tiles_cache) * kKeys;
+      last = min(kKeys, a.N - j0) - 1;
+      const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
+      const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
+      vr = Rows{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
+      load_keys<S, T>(kr, last, a.D, lane, key);
+      load_rows<S, T>(vr, last, a.D, lane, v);
+    } else {
+      last = place(tile, j0);
+      const Rows kr = rows_at(a.k_cache, a.k_scales, j0);
+      vr = rows_at(a.v_cache, a.v_scales, j0);
+      if constexpr (kQ) {
+        KeyCodes<S> kc;
+        ValueCodes<S> vc;
+        load_key_codes<S>(kr, a.nb, head, last, a.D, one_scale, lane, kc);
+        load_row_codes<S>(vr, a.nb, head, last, a.D, lane, vc);
+#pragma unroll
+        for (int u = 0; u < S::U; ++u)
+#pragma unroll
+          for (int s = 0; s < S::KS; ++s) {
+            const float sc[2] = {scale_of(kc.scale[u][s][0]), scale_of(kc.scale[u][s][1])};
+            decode<T, S::KW>(kc.w[u][s], sc, key[u][s]);
+          }
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i)
+#pragma unroll
+          for (int s = 0; s < S::VS; ++s) {
+            const float sc = scale_of(vc.scale[i][s]);
+            decode<T, S::CW>(vc.w[i][s], &sc, v[i][s]);
+          }
+      } else {
+        load_keys<S, T>(kr, last, a.D, lane, key);
+        load_rows<S, T>(vr, last, a.D, lane, v);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < S::U; ++u)
 #pragma unroll
-      for (int s = 0; s < S::KS; ++s) add_key(own[u][s], u, s, x);
+      for (int s = 0; s < S::KS; ++s) add_key(key[u][s], u, s, x);
     __builtin_amdgcn_sched_barrier(0);
-    typename S::Values v;
-    load_rows<S, T>(vr, last, a.D, lane, v);
     uint32_t seen[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const uint64_t line = line_of[node[t]];
-      const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;
+      const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;  // up to here, but for the first
       seen[t] = 0;
 #pragma unroll
       for (int i = 0; i < S::kSlots; ++i) {
-        const int off = key_of(i, lane), j = j0 + off;
-        if (off > last || !(line >> j & 1)) continue;
-        const int position = n + depth_of[j];
-        seen[t] |= position > hidden || position < a.sinks ? 1u << i : 0u;
+        const int off = key_of(i, lane), j = min(j0 + off, own ? kMaxNodes - 1 : n);
+        const int position = own ? n + depth_of[j & (kMaxNodes - 1)] : j;
+        const bool sees = off <= last && (!own || (line >> (j & 63) & 1)) && (position > hidden || position < a.sinks);
+        seen[t] |= sees ? 1u << i : 0u;
       }
     }
     weigh<S, MT, true>(x, seen, a.c, z);
@@ -697,9 +690,19 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
       add_piece<S, T, MT>(piece, s, x, z);
     }
     __builtin_amdgcn_sched_barrier(0);
-    add_others(bad, seen, [&](int key, int d) {
+    add_others(bad, seen, [&](int key_at, int d) {
+      const uint32_t at = (uint32_t)min(key_at, last);
       Frag<T, S::CW> f;
-      load_values<T, S::CW>(vr.base + ((uint32_t)min(key, last) * vr.stride + (uint32_t)(d * kEs<T>)), f);
+      if constexpr (kQ) {
+        if (!own) {
+          uint32_t w[S::CW / 4];
+          load_codes<S::CW>(vr.base + (at * vr.stride + (uint32_t)d), w);
+          const float sc = scale_of(vr.scales[at * (uint32_t)a.nb + (uint32_t)((head + d) >> 7)]);
+          decode<T, S::CW>(w, &sc, f);
+          return f;
+        }
+      }
+      load_values<T, S::CW>(vr.base + (at * vr.stride + (uint32_t)(d * kEs<T>)), f);
       return f;
     });
   }
@@ -777,34 +780,44 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
   }
 }
 
-// The splits' results of a row: 64 lanes take its values, four each.
+// The splits' results of a row.  A wave's lanes first have the splits' references and sums, one each, then 16-byte
+// pieces of their results: as many splits at a time as a row's pieces leave lanes for.
 template <typename T>
 __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t rows, int rows_per_slot) {
-  const uint32_t row = blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
+  const uint32_t row = blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   if (row >= rows) return;
-  const int lane = threadIdx.x & (kWave - 1), d = lane * 4;
+  const int lane = threadIdx.x & (kWave - 1);
   const int m = (int)(row % (uint32_t)a.R);
   const uint32_t pair = row / (uint32_t)a.R;  // b * Hkv + h
   const int h = (int)(pair % (uint32_t)a.Hkv), b = (int)(pair / (uint32_t)a.Hkv);
   const int group = m / rows_per_slot, r = m % rows_per_slot;
-  auto at = [&](int s) { return (((size_t)pair * a.split + s) * a.groups + group) * rows_per_slot + r; };
+  const size_t slot0 = ((size_t)pair * a.split * a.groups + group) * rows_per_slot + r, step = (size_t)a.groups * rows_per_slot;
   float ref = kNinf;
   bool bad = false;
-  for (int s = 0; s < a.split; ++s) {
-    const float2 w = a.stats[at(s)];
+  for (int s = lane; s < a.split; s += kWave) {
+    const float2 w = a.stats[slot0 + s * step];
     bad |= w.y != w.y;
     if (w.y != 0.0f) ref = fmaxf(ref, w.x);
   }
+  ref = wave_max(ref);
+  bad = __any(bad);
+  const int pieces = a.D > 128 ? 64 : a.D > 64 ? 32 : 16, at_once = kWave / pieces;
+  const int d = (lane & (pieces - 1)) * 4;
   float l = 0.0f;
   f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.split; ++s) {
-    const float2 w = a.stats[at(s)];
-    if (w.y == 0.0f) continue;
-    const float f = w.x == kNinf ? 1.0f : exp2_of(w.x - ref);
+#pragma unroll 4
+  for (int s = lane / pieces; s < a.split; s += at_once) {
+    const float2 w = a.stats[slot0 + s * step];
+    const float f = w.y == 0.0f ? 0.0f : w.x == kNinf ? 1.0f : exp2_of(w.x - ref);
     l += w.y * f;
-    if (d < a.D && !bad) y += *reinterpret_cast<const f32x4*>(a.acc + at(s) * (size_t)a.D + d) * f;
+    if (d < a.D && w.y != 0.0f) y += *reinterpret_cast<const f32x4*>(a.acc + (slot0 + s * step) * (size_t)a.D + d) * f;
   }
-  if (d >= a.D) return;
+  for (int o = pieces; o < kWave; o *= 2) {
+    l += __shfl_xor(l, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += __shfl_xor(y[i], o);
+  }
+  if (lane >= pieces || d >= a.D) return;
   const float inv = 1.0f / l;
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = bad ? __builtin_nanf("") : l == 0.0f ? 0.0f : y[i] * inv;
@@ -821,7 +834,8 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t 
 
 template <typename T, bool kQ, int DP, int MT>
 void start(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  if (a.D == DP) hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, true>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  else hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, false>), dim3(p.grid), dim3(kBlock), 0, st, a);
 }
 
 template <typename T, bool kQ, int DP>
