@@ -30,6 +30,7 @@
 
 #include <type_traits>
 
+#include "sv_dma.h"
 #include "sv_internal.h"
 #include "sv_quant.h"
 #include "sv_tree.h"
@@ -56,6 +57,7 @@ struct AttnArgs {
   float c;
 };
 
+constexpr int kStage = kAttnStage;  // keys that the waves of a block share
 constexpr float kSlack = 8.0f;      // how far a weight's exponent may pass its reference
 constexpr float kNinf = -__builtin_inff();
 
@@ -187,56 +189,17 @@ __device__ __forceinline__ void load_rows(const Rows& r, int last, int D, int la
   }
 }
 
-// Keys as codes: 16 per piece, and a scale for each 8.
+// Keys as codes, KW per piece, and a scale for each 8.
 template <typename S>
 struct KeyCodes {
-  uint32_t w[S::U][S::KS][4];
-  uint32_t scale[S::U][S::KS][2];
+  uint32_t w[S::U][S::KS][S::KW / 4];
+  uint32_t scale[S::U][S::KS][S::KW / 8];
 };
 template <typename S>
 struct ValueCodes {
   uint32_t w[S::kSlots][S::VS][S::CW / 4];
   uint32_t scale[S::kSlots][S::VS];
 };
-
-// one: the head lies in whole blocks of 128, or inside one, so that a scale
-// serves 128 values (or all of them).
-template <typename S>
-__device__ __forceinline__ void load_key_codes(const Rows& r, int nb, int head, int last, int D, bool one, int lane,
-                                               KeyCodes<S>& c) {
-#pragma unroll
-  for (int u = 0; u < S::U; ++u) {
-    const uint32_t key = (uint32_t)min(u * 16 + (lane & 15), last);
-    const uint32_t row = key * r.stride;
-#pragma unroll
-    for (int s = 0; s < S::KS; ++s) {
-      const int d = s * 64 + (lane >> 4) * 16;
-      if (S::kAll || D % 16 == 0) {
-        const u32x4 v = *reinterpret_cast<const u32x4_any1*>(r.base + (row + (uint32_t)(S::kAll || d < D ? d : 0)));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) c.w[u][s][q] = v[q];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const u32x2_any v = *reinterpret_cast<const u32x2_any*>(r.base + (row + (uint32_t)(d + 8 * e < D ? d + 8 * e : 0)));
-          c.w[u][s][2 * e] = v[0];
-          c.w[u][s][2 * e + 1] = v[1];
-        }
-      }
-      if (one) {
-        if (s % 2 == 0) c.scale[u][s][0] = r.scales[key * (uint32_t)nb + (uint32_t)((head + s * 64) >> 7)];
-        else c.scale[u][s][0] = c.scale[u][s & ~1][0];
-        c.scale[u][s][1] = c.scale[u][s][0];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int at = d + 8 * e < D ? d + 8 * e : 0;
-          c.scale[u][s][e] = r.scales[key * (uint32_t)nb + (uint32_t)((head + at) >> 7)];
-        }
-      }
-    }
-  }
-}
 
 template <int n>
 __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[n / 4]) {
@@ -247,6 +210,47 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[n / 4
   } else {
     typedef uint32_t word __attribute__((aligned(1)));
     w[0] = *reinterpret_cast<const word*>(p);
+  }
+}
+
+// one: the head lies in whole blocks of 128, or inside one, so that a scale
+// serves 128 values (or all of them).
+template <typename S>
+__device__ __forceinline__ void load_key_codes(const Rows& r, int nb, int head, int last, int D, bool one, int lane,
+                                               KeyCodes<S>& c) {
+  constexpr int kPer128 = 128 / (4 * S::KW);  // pieces of 128 values
+#pragma unroll
+  for (int u = 0; u < S::U; ++u) {
+    const uint32_t key = (uint32_t)min(u * 16 + (lane & 15), last);
+    const uint32_t row = key * r.stride;
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s) {
+      const int d = (s * 4 + (lane >> 4)) * S::KW;
+      if (S::KW == 16 && (S::kAll || D % 16 == 0)) {
+        const u32x4 v = *reinterpret_cast<const u32x4_any1*>(r.base + (row + (uint32_t)(S::kAll || d < D ? d : 0)));
+#pragma unroll
+        for (int q = 0; q < S::KW / 4; ++q) c.w[u][s][q] = v[q];
+      } else {
+#pragma unroll
+        for (int e = 0; e < S::KW / 8; ++e) {
+          uint32_t v[2];
+          load_codes<8>(r.base + (row + (uint32_t)(S::kAll || d + 8 * e < D ? d + 8 * e : 0)), v);
+          c.w[u][s][2 * e] = v[0];
+          c.w[u][s][2 * e + 1] = v[1];
+        }
+      }
+      if (one) {
+        if (s % kPer128 == 0) c.scale[u][s][0] = r.scales[key * (uint32_t)nb + (uint32_t)((head + s * 4 * S::KW) >> 7)];
+        else c.scale[u][s][0] = c.scale[u][s - s % kPer128][0];
+        if constexpr (S::KW == 16) c.scale[u][s][1] = c.scale[u][s][0];
+      } else {
+#pragma unroll
+        for (int e = 0; e < S::KW / 8; ++e) {
+          const int at = d + 8 * e < D ? d + 8 * e : 0;
+          c.scale[u][s][e] = r.scales[key * (uint32_t)nb + (uint32_t)((head + at) >> 7)];
+        }
+      }
+    }
   }
 }
 
@@ -412,13 +416,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 template <int DP>
 constexpr int kPad = DP + 4;
 
-template <typename T, bool kQ, int DP, int MT, bool kWhole>
-__global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2) tree_attention_kernel(AttnArgs a) {
-  typedef Shape<T, kQ, DP, MT, kWhole> S;
+// kShared: every wave has 16 MT rows of its own, and all take the same keys, 64 at a time from shared memory.
+template <typename T, bool kQ, int DP, int MT, bool kWhole, bool kShared>
+__global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2)
+    tree_attention_kernel(AttnArgs a) {
+  typedef Shape<T, kQ && !kShared, DP, MT, kWhole> S;
   __shared__ uint64_t line_of[kMaxNodes];
   __shared__ int depth_of[kMaxNodes];
   __shared__ float2 stat[kWavesPerBlock][16 * MT];
-  __shared__ float part[kWavesPerBlock][16 * kPad<DP>];
+  __shared__ float part[kShared ? 1 : kWavesPerBlock][kShared ? 4 : 16 * kPad<DP>];
+  constexpr int kSpan = kShared ? kStage : S::kKeys;  // keys of a tile
+  __shared__ __align__(256) uint8_t stage[kShared ? 2 : 1][2][kShared ? kStage * DP * 2 : 16];  // keys, values
 
   // Blocks that share keys, one per group of rows, are eight apart: the same XCD.
   const uint32_t eight = blockIdx.x / (8u * a.groups), rest = blockIdx.x % (8u * a.groups);
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
   }
 
   // The rows' queries: row m is node m / G, head m % G of the KV head's G.
-  const int row0 = group * 16 * MT;
+  const int row0 = (kShared ? group * kWavesPerBlock + wave : group) * 16 * MT;
   Frag<T, S::KW> q[MT][S::KS];
   int node[MT];
 #pragma unroll
@@ -474,8 +482,8 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
     if (first == low) first = low = 0;
   }
   constexpr int kKeys = S::kKeys;
-  const int tiles_first = (first + kKeys - 1) / kKeys, tiles_cache = tiles_first + (n - low + kKeys - 1) / kKeys;
-  const int tiles = valid ? tiles_cache + (a.N + kKeys - 1) / kKeys : 0;
+  const int tiles_first = (first + kSpan - 1) / kSpan, tiles_cache = tiles_first + (n - low + kSpan - 1) / kSpan;
+  const int tiles = valid ? tiles_cache + (a.N + kSpan - 1) / kSpan : 0;
   const int from = (int)((long long)tiles * split / a.split), to = (int)((long long)tiles * (split + 1) / a.split);
   const int edge = a.window > 0 ? n + a.N - 1 - a.window : -1;  // no window hides a later entry from any node
   const size_t heads = (size_t)a.Hkv * a.D;                     // values per entry
@@ -494,8 +502,8 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
 
   // A tile of the cache: its first entry, and the tile's last key.
   auto place = [&](int tile, int& j0) {
-    j0 = tile < tiles_first ? tile * kKeys : low + (tile - tiles_first) * kKeys;
-    return min(kKeys, (tile < tiles_first ? first : n) - j0) - 1;
+    j0 = tile < tiles_first ? tile * kSpan : low + (tile - tiles_first) * kSpan;
+    return min(kSpan, (tile < tiles_first ? first : n) - j0) - 1;
   };
   auto rows_at = [&](const uint8_t* base, const uint8_t* scales, int j0) {
     const size_t row = (size_t)b * a.L + j0;
@@ -566,11 +574,131 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
   };
 
   // Tiles that every row sees whole: of the first entries, and behind the window's edge.
-  const int edge_tiles = edge >= low ? (edge - low) / kKeys + 1 : 0;
-  const int first_end = max(from, min(to, first / kKeys));
-  const int later = min(max(from, tiles_first + edge_tiles), to), later_end = max(later, min(to, tiles_first + (n - low) / kKeys));
+  const int edge_tiles = edge >= low ? (edge - low) / kSpan + 1 : 0;
+  const int first_end = max(from, min(to, first / kSpan));
+  const int later = min(max(from, tiles_first + edge_tiles), to), later_end = max(later, min(to, tiles_first + (n - low) / kSpan));
   const int count = first_end - from + later_end - later;
   auto whole_tile = [&](int i) { return i < first_end - from ? from + i : later + i - (first_end - from); };
+  if constexpr (kShared) {
+    // A row of shared memory has its 16-byte pieces in an order of its own, so that sixteen keys' pieces of one place
+    // lie in different banks.
+    constexpr int kRow = DP * 2, kPieces = kRow / 16;
+    auto turned = [](int row, int piece) { return piece ^ (kPieces == 16 ? row & 15 : row >> 1 & 7); };
+    // One stage: keys and values of 64 entries, a quarter by each wave.
+    constexpr int kRowsD = kWave / kPieces, kDmas = kStage / kRowsD / kWavesPerBlock;  // rows of a DMA
+    auto issue = [&](int i, int buffer) {
+      int j0;
+      place(whole_tile(i), j0);
+      const Rows kr = rows_at(a.k_cache, a.k_scales, j0), vr = rows_at(a.v_cache, a.v_scales, j0);
+#pragma unroll
+      for (int d = 0; d < kDmas; ++d) {
+        const int row0 = (wave * kDmas + d) * kRowsD, row = row0 + lane / kPieces, slot = lane % kPieces;
+        const int kd = turned(row, slot) * 8, vd = slot * 8;
+        dma16(kr.base + ((uint32_t)row * kr.stride + (uint32_t)((kWhole || kd < a.D ? kd : 0) * 2)), &stage[buffer][0][row0 * kRow]);
+        dma16(vr.base + ((uint32_t)row * vr.stride + (uint32_t)((kWhole || vd < a.D ? vd : 0) * 2)), &stage[buffer][1][row0 * kRow]);
+      }
+    };
+    // The same from codes, by way of registers: 16 per lane and load.
+    constexpr int kLanesC = DP / 16, kRowsC = kWave / kLanesC, kLoadsC = kStage / kRowsC / kWavesPerBlock;
+    uint32_t codes[2][kLoadsC][4], scales[2][kLoadsC][2];
+    auto fetch = [&](int i) {
+      int j0;
+      place(whole_tile(i), j0);
+      const Rows both[2] = {rows_at(a.k_cache, a.k_scales, j0), rows_at(a.v_cache, a.v_scales, j0)};
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int c = 0; c < kLoadsC; ++c) {
+          const uint32_t row = (uint32_t)((wave * kLoadsC + c) * kRowsC + lane / kLanesC);
+          const int d = lane % kLanesC * 16;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = kWhole || d + 8 * e < a.D ? d + 8 * e : 0;
+            if (!kWhole || e == 0) {
+              if constexpr (kWhole) {
+                const u32x4 w = *reinterpret_cast<const u32x4_any1*>(both[v].base + (row * both[v].stride + (uint32_t)at));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) codes[v][c][q] = w[q];
+              } else {
+                uint32_t w[2];
+                load_codes<8>(both[v].base + (row * both[v].stride + (uint32_t)at), w);
+                codes[v][c][2 * e] = w[0];
+                codes[v][c][2 * e + 1] = w[1];
+              }
+              scales[v][c][e] = both[v].scales[row * (uint32_t)a.nb + (uint32_t)((head + at) >> 7)];
+            }
+            if (kWhole && e == 1)  // 16 codes of a whole head are in one block where the head begins on 16
+              scales[v][c][1] = scales[v][c][0];
+          }
+        }
+    };
+    auto put = [&](int buffer) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int c = 0; c < kLoadsC; ++c) {
+          const int row = (wave * kLoadsC + c) * kRowsC + lane / kLanesC;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int piece = lane % kLanesC * 2 + e;
+            const float sc = scale_of(scales[v][c][e]);
+            const uint32_t w[2] = {codes[v][c][2 * e], codes[v][c][2 * e + 1]};
+            Frag<T, 8> f;
+            decode<T, 8>(w, &sc, f);
+            *reinterpret_cast<u32x4*>(&stage[buffer][v][row * kRow + (v == 0 ? turned(row, piece) : piece) * 16]) =
+                u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
+          }
+        }
+    };
+    if constexpr (kQ) {
+      if (count > 0) fetch(0);
+    } else {
+      if (count > 0) issue(0, 0);
+    }
+    for (int i = 0; i < count; ++i) {
+      const int buffer = i & 1;
+      // The stage is there, and every wave is done with the other buffer.
+      if constexpr (kQ) {
+        put(buffer);
+        if (i + 1 < count) fetch(i + 1);
+        block_barrier();
+      } else {
+        wait_vmcnt<0>();
+        block_barrier();
+        if (i + 1 < count) issue(i + 1, buffer ^ 1);
+      }
+#pragma unroll
+      for (int half = 0; half < kStage / kKeys; ++half) {
+        f32x4 x[MT][S::U];
+#pragma unroll
+        for (int u = 0; u < S::U; ++u)
+#pragma unroll
+          for (int s = 0; s < S::KS; ++s) {
+            const int row = half * kKeys + u * 16 + (lane & 15);
+            const u32x4 w = *reinterpret_cast<const u32x4*>(&stage[buffer][0][row * kRow + turned(row, 4 * s + g) * 16]);
+            Frag<T, S::KW> f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f.w[q] = w[q];
+            add_key(f, u, s, x);
+          }
+        const uint32_t none[MT] = {};
+        weigh<S, MT, false>(x, none, a.c, z);
+#pragma unroll
+        for (int s = 0; s < S::VS; ++s) {
+          Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+          for (int slot = 0; slot < S::kSlots; ++slot) {
+            typedef uint32_t words __attribute__((ext_vector_type(S::CW / 2)));
+            const words w = *reinterpret_cast<const words*>(
+                &stage[buffer][1][(half * kKeys + key_of(slot, lane)) * kRow + (s * 16 + (lane & 15)) * S::CW * 2]);
+#pragma unroll
+            for (int q = 0; q < S::CW / 2; ++q) piece[slot].w[q] = w[q];
+          }
+          add_piece<S, T, MT>(piece, s, x, z);
+        }
+      }
+    }
+  } else {
   if (wave < count) fetch_keys(whole_tile(wave));
   for (int i = wave; i < count; i += kWavesPerBlock) {
     int j0;
@@ -586,7 +714,7 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
 #pragma unroll
       for (int s = 0; s < S::KS; ++s) {
         if constexpr (kQ) {
-          const float sc[2] = {scale_of(k.scale[u][s][0]), scale_of(k.scale[u][s][1])};
+          const float sc[2] = {scale_of(k.scale[u][s][0]), scale_of(k.scale[u][s][S::KW / 8 - 1])};
           Frag<T, S::KW> f;
           decode<T, S::KW>(k.w[u][s], sc, f);
           add_key(f, u, s, x);
@@ -614,10 +742,12 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  }
 
   // The others: ends, entries at the window's edge, and the tree's own, of which a node sees its ancestors and itself.
 #pragma unroll 1
-  for (int tile = from + wave; tile < to; tile += kWavesPerBlock) {
+  for (int at = kShared ? from * (kSpan / kKeys) : from + wave; at < to * (kSpan / kKeys); at += kShared ? 1 : kWavesPerBlock) {
+    const int tile = at / (kSpan / kKeys), part_of = at % (kSpan / kKeys) * kKeys;  // a tile's 32 keys at a time
     if (tile < first_end || (tile >= later && tile < later_end)) continue;
     const bool own = tile >= tiles_cache;
     int j0, last;
@@ -626,15 +756,18 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
     f32x4 x[MT][S::U];
     Rows vr;
     if (own) {
-      j0 = (tile - tiles_cache) * kKeys;
+      j0 = (tile - tiles_cache) * kSpan + part_of;
       last = min(kKeys, a.N - j0) - 1;
+      if (last < 0) continue;
       const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
       const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
       vr = Rows{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
       load_keys<S, T>(kr, last, a.D, lane, key);
       load_rows<S, T>(vr, last, a.D, lane, v);
     } else {
-      last = place(tile, j0);
+      last = min(place(tile, j0) - part_of, kKeys - 1);
+      j0 += part_of;
+      if (last < 0) continue;
       const Rows kr = rows_at(a.k_cache, a.k_scales, j0);
       vr = rows_at(a.v_cache, a.v_scales, j0);
       if constexpr (kQ) {
@@ -646,7 +779,7 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
         for (int u = 0; u < S::U; ++u)
 #pragma unroll
           for (int s = 0; s < S::KS; ++s) {
-            const float sc[2] = {scale_of(kc.scale[u][s][0]), scale_of(kc.scale[u][s][1])};
+            const float sc[2] = {scale_of(kc.scale[u][s][0]), scale_of(kc.scale[u][s][S::KW / 8 - 1])};
             decode<T, S::KW>(kc.w[u][s], sc, key[u][s]);
           }
 #pragma unroll
@@ -705,6 +838,44 @@ __global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_sam
       load_values<T, S::CW>(vr.base + (at * vr.stride + (uint32_t)(d * kEs<T>)), f);
       return f;
     });
+  }
+
+  if constexpr (kShared) {
+    // A wave's rows are its own: lane (g, m) has values (4 g + r) CW .. of each piece of row m.
+    const size_t slot = ((size_t)item * a.groups + group) * (kWavesPerBlock * 16 * MT) + wave * 16 * MT;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float l = z.l[t] + __shfl_xor(z.l[t], 16);
+      l += __shfl_xor(l, 32);
+      const int r = t * 16 + (lane & 15), m = row0 + r;
+      if (m >= a.R) continue;
+      if (!valid) l = __builtin_nanf("");
+      if (line_of[node[t]] == 0) l = 0.0f;
+      const float inv = 1.0f / l;
+      const size_t to = (((size_t)b * a.N + node[t]) * a.Hq + h * a.G + (m - node[t] * a.G)) * (size_t)a.D;
+      if (a.split > 1 && g == 0) a.stats[slot + r] = float2{l == 0.0f ? kNinf : z.m[t], l};
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+          for (int j = 0; j < S::CW; j += 4) {
+            const int d = s * 16 * S::CW + (g * 4 + r4) * S::CW + j;
+            if (!kWhole && d >= a.D) continue;
+            f32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = z.o[t][s * S::CW + j + e][r4];
+            if (a.split > 1) {
+              if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + r) * (size_t)a.D + d) = y;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
+              typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
+              *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + to + d) = pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+            }
+          }
+    }
+    return;
   }
 
   // The waves' results, 16 rows at a time.
@@ -832,16 +1003,23 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t 
   }
 }
 
-template <typename T, bool kQ, int DP, int MT>
+template <typename T, bool kQ, int DP, int MT, bool kShared>
 void start(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (a.D == DP) hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, true>), dim3(p.grid), dim3(kBlock), 0, st, a);
-  else hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, false>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  if (a.D == DP) hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, true, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  else hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, false, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
 }
 
 template <typename T, bool kQ, int DP>
 void start_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (p.mt == 1) start<T, kQ, DP, 1>(a, p, st);
-  else if constexpr (DP <= 128) start<T, kQ, DP, 2>(a, p, st);
+  if constexpr (!std::is_same<T, float>::value && DP <= 128) {
+    if (p.shared) {
+      if (p.mt == 2) start<T, kQ, DP, 2, true>(a, p, st);
+      else start<T, kQ, DP, 4, true>(a, p, st);
+      return;
+    }
+  }
+  if (p.mt == 1) start<T, kQ, DP, 1, false>(a, p, st);
+  else if constexpr (DP <= 128) start<T, kQ, DP, 2, false>(a, p, st);
 }
 
 template <typename T, bool kQ>
@@ -853,7 +1031,7 @@ hipError_t run(const AttnArgs& a, const AttnPlan& p, int B, hipStream_t st) {
   if (e != hipSuccess || p.split == 1) return e;
   const uint32_t rows = (uint32_t)B * a.Hkv * a.R;
   hipLaunchKernelGGL((tree_join_kernel<T>), dim3((rows + kWavesPerBlock - 1) / kWavesPerBlock), dim3(kBlock), 0, st, a,
-                     rows, 16 * p.mt);
+                     rows, p.rows);
   return hipGetLastError();
 }
 

@@ -411,9 +411,8 @@ spec_status_t spec_tree_attention_quantized(const void* q, const void* k_codes, 
 
 size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
                                            spec_dtype_t dtype) {
-  sv::AttnPlan plan{};
-  bool empty = false;
-  return sv::check_attention(B, N, Hq, Hkv, D, L_max, dtype, &plan, &empty) == SPEC_OK && !empty ? plan.total : 0;
+  size_t bytes = 0;
+  return sv::attention_workspace(B, N, Hq, Hkv, D, L_max, dtype, &bytes) == SPEC_OK ? bytes : 0;
 }
 
 spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int32_t R, int32_t V, spec_dtype_t dtype,

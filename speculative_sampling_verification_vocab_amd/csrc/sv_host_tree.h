@@ -13,11 +13,13 @@ constexpr int32_t kMaxLength = 1 << 30;  // cache positions: sums with depths an
 
 // Launch plan of spec_tree_attention and its quantised form.  The rows of one
 // KV head are its G = Hq / Hkv query heads of every node, node by node; a block
-// takes 16 * mt of them against one split of the keys.
+// takes `rows` of them against one split of the keys.
 struct AttnPlan {
   int32_t R;       // rows per (sequence, KV head)
   int32_t dp;      // head size rounded up to 64, 128 or 256
-  int32_t mt;      // tiles of 16 rows per block
+  bool shared;     // the block's waves have rows of their own and share the keys; else keys of their own
+  int32_t mt;      // tiles of 16 rows per wave
+  int32_t rows;    // rows per block
   int32_t groups;  // blocks that share the rows of a KV head
   int32_t split;   // blocks that share the keys
   size_t slots;    // B * Hkv * groups * split: partial results, and blocks but for the round-up
@@ -25,11 +27,12 @@ struct AttnPlan {
   size_t stats, acc, total;  // workspace byte offsets (split > 1)
 };
 
-constexpr int kAttnBlocksWanted = 1024;  // 4 per CU
-constexpr int kAttnSplitKeys = 512;      // at least so many cache positions per split
+constexpr int kAttnStage = 64;         // keys that the waves of a block share at a time
+constexpr int kAttnBlocksWanted = 512; // 2 per CU
+constexpr int kAttnSplitKeys = 512;    // at least so many cache positions per split
 
 inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
-                                     spec_dtype_t dtype, AttnPlan* p, bool* empty) {
+                                     spec_dtype_t dtype, bool aligned, AttnPlan* p, bool* empty) {
   if (!valid_dtype(dtype) || B < 0 || N < 0 || Hq < 1 || Hkv < 1 || D < 1 || L_max < 0) return SPEC_ERR_INVALID_ARG;
   if (Hq % Hkv != 0 || N > kMaxNodes || D % 8 != 0 || D > 256 || L_max > kMaxLength) return SPEC_ERR_UNSUPPORTED;
   if ((long long)Hkv * D > (1 << 22) || Hq > (1 << 22)) return SPEC_ERR_UNSUPPORTED;  // 32 rows' offsets stay in uint32
@@ -40,11 +43,13 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
     return SPEC_ERR_UNSUPPORTED;
   p->R = N * (Hq / Hkv);
   p->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  p->mt = p->R <= 16 || p->dp == 256 ? 1 : 2;  // what the registers hold
-  p->groups = (p->R + 16 * p->mt - 1) / (16 * p->mt);
+  p->shared = aligned && dtype == SPEC_BF16 && p->dp <= 128 && p->R > 64;
+  p->mt = p->shared ? (p->R <= 128 ? 2 : 4) : p->R <= 16 || p->dp == 256 ? 1 : 2;
+  p->rows = 16 * p->mt * (p->shared ? kWavesPerBlock : 1);
+  p->groups = (p->R + p->rows - 1) / p->rows;
   const unsigned long long pairs = (unsigned long long)B * Hkv * p->groups;
   if (pairs > max_blocks(kBlock) / 64) return SPEC_ERR_UNSUPPORTED;
-  long long s = (kAttnBlocksWanted + pairs - 1) / pairs;
+  long long s = (p->shared && p->mt == 4 ? kAttnBlocksWanted / 2 : kAttnBlocksWanted) / pairs;
   const long long most_splits = ((long long)L_max + N + kAttnSplitKeys - 1) / kAttnSplitKeys;
   if (s > most_splits) s = most_splits;
   p->split = s < 1 ? 1 : (int32_t)s;
@@ -54,11 +59,26 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
   p->grid = (unsigned)eight;
   p->stats = p->acc = p->total = 0;
   if (p->split > 1) {
-    const size_t rows = p->slots * (size_t)(16 * p->mt);
+    const size_t rows = p->slots * (size_t)p->rows;
     if (rows > kMaxBytes / ((size_t)D * 4 + 8)) return SPEC_ERR_UNSUPPORTED;
     p->acc = align256(rows * 8);
     p->total = p->acc + align256(rows * (size_t)D * 4);
   }
+  return SPEC_OK;
+}
+
+// Workspace bytes of a call on any buffers.
+inline spec_status_t attention_workspace(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
+                                         spec_dtype_t dtype, size_t* bytes) {
+  AttnPlan p{};
+  bool empty = false;
+  size_t most = 0;
+  for (int aligned = 0; aligned < 2; ++aligned) {
+    const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, dtype, aligned != 0, &p, &empty);
+    if (sc != SPEC_OK) return sc;
+    if (!empty && p.total > most) most = p.total;
+  }
+  *bytes = most;
   return SPEC_OK;
 }
 
@@ -73,7 +93,12 @@ inline spec_status_t validate_attention(const AttnPointers& a, bool quantized, i
                                         int32_t Hkv, int32_t D, int32_t L_max, float scale, int32_t window,
                                         int32_t sinks, spec_dtype_t dtype, const void* workspace,
                                         size_t workspace_bytes, AttnPlan* p, bool* empty) {
-  const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, dtype, p, empty);
+  size_t need = 0;
+  const spec_status_t sw = attention_workspace(B, N, Hq, Hkv, D, L_max, dtype, &need);
+  if (sw != SPEC_OK) return sw;
+  // Values go to shared memory in whole 16-byte pieces.
+  const bool aligned = quantized || ((uintptr_t)a.k_cache % 16 == 0 && (uintptr_t)a.v_cache % 16 == 0);
+  const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, dtype, aligned, p, empty);
   if (sc != SPEC_OK) return sc;
   if (!(scale > 0.0f && isfinite(scale)) || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
   if (*empty) return SPEC_OK;
@@ -84,8 +109,7 @@ inline spec_status_t validate_attention(const AttnPointers& a, bool quantized, i
       (uintptr_t)a.parents % 4 || (uintptr_t)a.cache_len % 4)
     return SPEC_ERR_INVALID_ARG;
   if (!quantized && ((uintptr_t)a.k_cache % es || (uintptr_t)a.v_cache % es)) return SPEC_ERR_INVALID_ARG;
-  if (p->total > 0 && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < p->total))
-    return SPEC_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < need)) return SPEC_ERR_WORKSPACE;
   return SPEC_OK;
 }
 
