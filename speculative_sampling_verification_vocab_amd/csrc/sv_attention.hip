@@ -17,8 +17,23 @@
 //                 whole rows of V at a time; in bf16, value j of eight keys is
 //                 brought into one operand by byte permutes.
 // So keys and values are read once, with no shared memory and no barrier in
-// the loop.  The waves' results meet in shared memory, 16 rows at a time, and
-// those of blocks that share the keys in a second launch (tree_join_kernel).
+// the loop, and a tile's keys are asked for while the one before is worked on.
+// The waves' results meet in shared memory, 16 rows at a time, and those of
+// blocks that share the keys in a second launch (tree_join_kernel); sv_host_tree.h
+// says how the keys are shared out.
+//
+// More than 64 rows of a KV head are bound by the products and not by memory:
+// then each wave has 32 rows of its own and all four take the same keys,
+// 64 at a time from shared memory, in two buffers, bf16 values by direct loads
+// and codes decoded once for all waves.
+//
+// Measured (32 query heads on 8 KV heads of 128, half to all of L cached):
+//   B=64 N=1 L=8192 bf16      299 us  5.4 TB/s: the cache's bytes, of 6.0 to 6.4 that reads alone reach
+//   B=32 N=8 L=8192 bf16      184 us  4.4 TB/s, and 8-bit 122 us, 3.4 TB/s
+//   B=1 N=16 L=131072 bf16    119 us  4.5 TB/s, and 8-bit 80 us, 3.4 TB/s: the registers leave two waves per
+//                             SIMD, and the loads that those have in flight bound it
+//   B=64 N=64 L=8192 bf16     685 us  610 TFLOP/s of 1130 that a large product reaches: softmax and permutes
+//                             share the issue slots with the matrix instructions
 //
 // Sums, maxima and both products' accumulators are fp32.  The weights p are
 // rounded to bf16 for the bf16 product, half a step of 2^-8 each at random,
@@ -49,10 +64,10 @@ struct AttnArgs {
   const uint8_t *k_scales, *v_scales;         // [B][L][nb]
   const int32_t *parents, *cache_len;         // [B][N], [B]
   void* out;                                  // [B][N][Hq][D]
-  float2* stats;                              // [slots][16 mt] reference and sum
-  float* acc;                                 // [slots][16 mt][D]
-  int N, Hq, Hkv, G, D, L, nb, R, groups, split;
-  uint32_t items;                             // B * Hkv * split
+  float2* stats;                              // [slots][groups][rows] reference and sum
+  float* acc;                                 // [slots][groups][rows][D]
+  int B, N, Hq, Hkv, G, D, L, nb, R, groups;
+  int split, ranges, least, step, span;       // see AttnPlan
   int window, sinks;
   float c;
 };
@@ -274,7 +289,8 @@ __device__ __forceinline__ void load_row_codes(const Rows& r, int nb, int head, 
 
 __device__ __forceinline__ f32x4 mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4 c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+      0, 0, 0);
 #else
   return c;
 #endif
@@ -411,6 +427,75 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 
 // ---- the kernel -----------------------------------------------------------------
 
+// The keys of a sequence with `length` cached entries: those that every node sees before the window (none
+// without one), those from the first that the window of any node reaches, and the tree's own, each in tiles of
+// `span` keys.
+struct Keys {
+  int n, low, first;                   // cached entries; 0 .. first and low .. n are read
+  int tiles_first, tiles_cache, tiles; // ends of the three parts
+  bool valid;
+};
+
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int span, int length) {
+  Keys k;
+  k.valid = length >= 0 && length <= a.L;
+  k.n = k.valid ? length : 0;
+  k.low = k.first = 0;
+  if (a.window > 0) {
+    k.low = max(0, k.n - a.window + 1);
+    k.first = min(a.sinks, k.low);
+    if (k.first == k.low) k.first = k.low = 0;
+  }
+  k.tiles_first = (k.first + span - 1) / span;
+  k.tiles_cache = k.tiles_first + (k.n - k.low + span - 1) / span;
+  k.tiles = k.tiles_cache + (a.N + span - 1) / span;
+  return k;
+}
+
+// The batch's tiles are numbered through, sequence by sequence and KV head by KV head, and cut into a.ranges equal
+// ranges (a.least tiles at least), one per block: every block has the same to do, whatever the lengths.
+__device__ __forceinline__ int lanes_scan(int v) {  // inclusive, over the lanes
+  v += dpp::mov<dpp::kShr1, 0xf>(0, v);
+  v += dpp::mov<dpp::kShr2, 0xf>(0, v);
+  v += dpp::mov<dpp::kShr4, 0xf>(0, v);
+  v += dpp::mov<dpp::kShr8, 0xf>(0, v);
+  v += dpp::mov<dpp::kBcast15, 0xa>(0, v);
+  v += dpp::mov<dpp::kBcast31, 0xc>(0, v);
+  return v;
+}
+
+// Tiles of a range.  The whole batch has at most 2^31 - 1 tiles (checked on the host).
+__device__ __forceinline__ int range_of(const AttnArgs& a, int total) {
+  const int per = max((int)(((uint32_t)total + (uint32_t)a.ranges - 1) / (uint32_t)a.ranges), a.least);
+  return (per + a.step - 1) / a.step * a.step;
+}
+
+// Tiles of range i (0: there is no such range), and where it begins: sequence, KV head and the tile's number there.
+__device__ __forceinline__ int find_range(const AttnArgs& a, uint32_t range, int lane, int& b, int& h, int& tile) {
+  const int t0 = lane < a.B ? keys_of(a, a.span, a.cache_len[lane]).tiles : 0;
+  int all = t0;
+  for (int i = lane + kWave; i < a.B; i += kWave) all += keys_of(a, a.span, a.cache_len[i]).tiles;
+  const int total = dpp::lane63(lanes_scan(all)) * a.Hkv, per = range_of(a, total);
+  if (range >= (uint32_t)a.ranges || (uint64_t)range * (uint32_t)per >= (uint64_t)total) return 0;
+  const int p = (int)range * per;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kWave) {
+    const int t = b0 == 0 ? t0 : b0 + lane < a.B ? keys_of(a, a.span, a.cache_len[b0 + lane]).tiles : 0;
+    const int up_to = before + lanes_scan(t) * a.Hkv;
+    const uint64_t hit = __ballot(p < up_to);
+    if (hit != 0) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int of_b = __builtin_amdgcn_readlane(t, l), rem = p - (__builtin_amdgcn_readlane(up_to, l) - of_b * a.Hkv);
+      b = b0 + l;
+      h = rem / of_b;
+      tile = rem - h * of_b;
+      return min(per, total - p);
+    }
+    before = dpp::lane63(up_to);
+  }
+  return 0;
+}
+
 // Result of a row in shared memory: DP values, padded so that the sixteen rows
 // of a tile start in different banks.
 template <int DP>
@@ -432,563 +517,638 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
   const uint32_t eight = blockIdx.x / (8u * a.groups), rest = blockIdx.x % (8u * a.groups);
   const uint32_t item = eight * 8 + rest % 8;
   const int group = (int)(rest / 8);
-  if (item >= a.items) return;
-  const int split = (int)(item % (uint32_t)a.split);
-  const int h = (int)(item / (uint32_t)a.split % (uint32_t)a.Hkv);
-  const int b = (int)(item / (uint32_t)a.split / (uint32_t)a.Hkv);
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);  // scalar, and with it the tiles' addresses
-  const int length = a.cache_len[b];
-  const bool valid = length >= 0 && length <= a.L;
-  const int n = valid ? length : 0;
-
-  if (wave == 0) {
-    const TreeNode t = tree_node(lane < a.N ? a.parents[(size_t)b * a.N + lane] : -2, lane, a.N);
-    line_of[lane] = t.line;
-    depth_of[lane] = t.depth;
-  }
-
-  // The rows' queries: row m is node m / G, head m % G of the KV head's G.
-  const int row0 = (kShared ? group * kWavesPerBlock + wave : group) * 16 * MT;
-  Frag<T, S::KW> q[MT][S::KS];
-  int node[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = row0 + t * 16 + (lane & 15);
-    node[t] = m < a.R ? m / a.G : 0;
-    const int head = h * a.G + (m < a.R ? m - node[t] * a.G : 0);
-    const uint8_t* p = static_cast<const uint8_t*>(a.q) + (((size_t)b * a.N + node[t]) * a.Hq + head) * (size_t)a.D * kEs<T>;
-#pragma unroll
-    for (int s = 0; s < S::KS; ++s)
-#pragma unroll
-      for (int e = 0; e < S::KW; e += (S::KW > 8 ? 8 : S::KW)) {
-        constexpr int w = S::KW > 8 ? 8 : S::KW;
-        const int d = s * 4 * S::KW + g * S::KW + e;
-        Frag<T, w> f;
-        if (kWhole || d < a.D) load_values<T, w>(p + d * kEs<T>, f);
-        else clear(f);
-#pragma unroll
-        for (int i = 0; i < Frag<T, w>::kWords; ++i) q[t][s].w[e * kEs<T> / 4 + i] = f.w[i];
-      }
-  }
-
-  // The keys: cache entries that every node sees before the window (none without
-  // one), those from the first that the window of any node reaches, and the
-  // tree's own.
-  int low = 0, first = 0;
-  if (a.window > 0) {
-    low = max(0, n - a.window + 1);
-    first = min(a.sinks, low);
-    if (first == low) first = low = 0;
-  }
+  // scalar, and with it the tiles' addresses
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const size_t heads = (size_t)a.Hkv * a.D;                                   // values per entry
   constexpr int kKeys = S::kKeys;
-  const int tiles_first = (first + kSpan - 1) / kSpan, tiles_cache = tiles_first + (n - low + kSpan - 1) / kSpan;
-  const int tiles = valid ? tiles_cache + (a.N + kSpan - 1) / kSpan : 0;
-  const int from = (int)((long long)tiles * split / a.split), to = (int)((long long)tiles * (split + 1) / a.split);
-  const int edge = a.window > 0 ? n + a.N - 1 - a.window : -1;  // no window hides a later entry from any node
-  const size_t heads = (size_t)a.Hkv * a.D;                     // values per entry
-  const int head = h * a.D;
-  const bool one_scale = a.D % 128 == 0 ? head % 128 == 0 : head % 128 + a.D <= 128;
 
-  Sums<S, MT> z;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    z.m[t] = kNinf;
-    z.l[t] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < S::OT; ++i) z.o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int b = 0, h = 0, begin = 0;
+  int left = 0;  // tiles of the block's range
+  if (a.ranges == 0) {
+    const uint32_t pair = item / (uint32_t)a.split;
+    if (pair >= (uint32_t)a.B * (uint32_t)a.Hkv) return;
+    b = (int)(pair / (uint32_t)a.Hkv);
+    h = (int)(pair % (uint32_t)a.Hkv);
+    const uint32_t tiles = (uint32_t)keys_of(a, kSpan, a.cache_len[b]).tiles, piece = item - pair * (uint32_t)a.split;
+    const uint32_t each = tiles / (uint32_t)a.split, more = tiles - each * (uint32_t)a.split;
+    begin = (int)(piece * each + min(piece, more));
+    left = (int)(each + (piece < more ? 1 : 0));
+  } else {
+    left = find_range(a, item, threadIdx.x & (kWave - 1), b, h, begin);
+    if (left == 0) return;
   }
-  __syncthreads();
-
-  // A tile of the cache: its first entry, and the tile's last key.
-  auto place = [&](int tile, int& j0) {
-    j0 = tile < tiles_first ? tile * kSpan : low + (tile - tiles_first) * kSpan;
-    return min(kSpan, (tile < tiles_first ? first : n) - j0) - 1;
-  };
-  auto rows_at = [&](const uint8_t* base, const uint8_t* scales, int j0) {
-    const size_t row = (size_t)b * a.L + j0;
-    Rows r;
-    r.base = base + (row * heads + head) * (kQ ? 1 : kEs<T>);
-    r.scales = kQ ? scales + row * (size_t)a.nb : nullptr;
-    r.stride = (uint32_t)heads * (kQ ? 1 : kEs<T>);
-    return r;
-  };
-  typedef typename std::conditional<kQ, KeyCodes<S>, typename S::Keys>::type CacheKeys;
-  CacheKeys k;
-  auto fetch_keys = [&](int tile) {
-    int j0;
-    const int last = kWhole ? (place(tile, j0), kKeys - 1) : place(tile, j0);  // a constant leaves the offsets in registers
-    const Rows r = rows_at(a.k_cache, a.k_scales, j0);
-    if constexpr (kQ) load_key_codes<S>(r, a.nb, head, last, a.D, one_scale, lane, k);
-    else load_keys<S, T>(r, last, a.D, lane, k);
-  };
-  auto add_key = [&](Frag<T, S::KW>& f, int u, int s, f32x4 (&x)[MT][S::U]) {
-    if constexpr (!kWhole) cut_key<S, T>(a.D, s, lane, f);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) x[t][u] = product<T, S::KW>(f, q[t][s], s == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[t][u]);
-  };
-  // Tiles that some row does not see all of: values that are not finite are taken out of the product (bits of the slots
-  // that had some), and added to the rows that see them: an infinity or NaN outweighs whatever its weight is.
-  // value(key, d): the CW values from d on.
-  auto take_out = [&](typename S::Values& v) {
-    uint32_t bad = 0;
-#pragma unroll
-    for (int i = 0; i < S::kSlots; ++i)
-#pragma unroll
-      for (int s = 0; s < S::VS; ++s)
-#pragma unroll
-        for (int w = 0; w < Frag<T, S::CW>::kWords; ++w) {
-          const uint32_t f = not_finite<T>(v[i][s].w[w]);
-          v[i][s].w[w] &= ~f;
-          bad |= f != 0 ? 1u << i : 0u;
-        }
-    return bad;
-  };
-  auto add_others = [&](uint32_t bad, const uint32_t (&seen)[MT], auto value) {
-    if (!__any(bad != 0)) return;
+  // The pieces of the block's range, one pair's after the other.
 #pragma unroll 1
-    for (int key = 0; key < kKeys; ++key) {
-      const int group16 = (key >> 2) & 3, slot = (key >> 4) * 4 + (key & 3);
-      if (!__any((lane >> 4) == group16 && (bad >> slot & 1))) continue;
-#pragma unroll
-      for (int s = 0; s < S::VS; ++s)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int d = s * 16 * S::CW + (g * 4 + r) * S::CW;
-          const Frag<T, S::CW> f = value(key, d < a.D ? d : 0);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const bool sees = __shfl(seen[t], group16 * 16 + (lane & 15)) >> slot & 1;
-#pragma unroll
-            for (int j = 0; j < S::CW; ++j) {
-              uint32_t w;
-              if constexpr (S::kF32) w = f.w[j];
-              else w = j & 1 ? f.w[j / 2] & 0xffff0000u : f.w[j / 2] << 16;
-              const bool add = sees && (w & 0x7f800000u) == 0x7f800000u;
-              z.o[t][s * S::CW + j][r] += add ? __uint_as_float(w) : 0.0f;
-            }
-          }
-          __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers
-        }
-    }
-  };
+  for (int nth = 0;; ++nth) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // or the lane's offsets would be kept from one piece to the next, in scratch
+    const int lane = tid & (kWave - 1), g = lane >> 4;
+    b = __builtin_amdgcn_readfirstlane(b);
+    h = __builtin_amdgcn_readfirstlane(h);
+    const Keys keys = keys_of(a, kSpan, a.cache_len[b]);
+    const int n = keys.n, low = keys.low, first = keys.first;
+    const int tiles_first = keys.tiles_first, tiles_cache = keys.tiles_cache;
+    const bool valid = keys.valid;
+    const int from = __builtin_amdgcn_readfirstlane(begin);
+    const int to = __builtin_amdgcn_readfirstlane(min(keys.tiles, from + left));
+    const bool alone = from == 0 && to == keys.tiles && a.split == 1;  // no other block has keys of these rows
+    const size_t slot0 = a.ranges == 0 ? (size_t)item : 2 * (size_t)item + (nth > 0);
 
-  // Tiles that every row sees whole: of the first entries, and behind the window's edge.
-  const int edge_tiles = edge >= low ? (edge - low) / kSpan + 1 : 0;
-  const int first_end = max(from, min(to, first / kSpan));
-  const int later = min(max(from, tiles_first + edge_tiles), to), later_end = max(later, min(to, tiles_first + (n - low) / kSpan));
-  const int count = first_end - from + later_end - later;
-  auto whole_tile = [&](int i) { return i < first_end - from ? from + i : later + i - (first_end - from); };
-  if constexpr (kShared) {
-    // A row of shared memory has its 16-byte pieces in an order of its own, so that sixteen keys' pieces of one place
-    // lie in different banks.
-    constexpr int kRow = DP * 2, kPieces = kRow / 16;
-    auto turned = [](int row, int piece) { return piece ^ (kPieces == 16 ? row & 15 : row >> 1 & 7); };
-    // One stage: keys and values of 64 entries, a quarter by each wave.
-    constexpr int kRowsD = kWave / kPieces, kDmas = kStage / kRowsD / kWavesPerBlock;  // rows of a DMA
-    auto issue = [&](int i, int buffer) {
-      int j0;
-      place(whole_tile(i), j0);
-      const Rows kr = rows_at(a.k_cache, a.k_scales, j0), vr = rows_at(a.v_cache, a.v_scales, j0);
-#pragma unroll
-      for (int d = 0; d < kDmas; ++d) {
-        const int row0 = (wave * kDmas + d) * kRowsD, row = row0 + lane / kPieces, slot = lane % kPieces;
-        const int kd = turned(row, slot) * 8, vd = slot * 8;
-        dma16(kr.base + ((uint32_t)row * kr.stride + (uint32_t)((kWhole || kd < a.D ? kd : 0) * 2)), &stage[buffer][0][row0 * kRow]);
-        dma16(vr.base + ((uint32_t)row * vr.stride + (uint32_t)((kWhole || vd < a.D ? vd : 0) * 2)), &stage[buffer][1][row0 * kRow]);
-      }
-    };
-    // The same from codes, by way of registers: 16 per lane and load.
-    constexpr int kLanesC = DP / 16, kRowsC = kWave / kLanesC, kLoadsC = kStage / kRowsC / kWavesPerBlock;
-    uint32_t codes[2][kLoadsC][4], scales[2][kLoadsC][2];
-    auto fetch = [&](int i) {
-      int j0;
-      place(whole_tile(i), j0);
-      const Rows both[2] = {rows_at(a.k_cache, a.k_scales, j0), rows_at(a.v_cache, a.v_scales, j0)};
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int c = 0; c < kLoadsC; ++c) {
-          const uint32_t row = (uint32_t)((wave * kLoadsC + c) * kRowsC + lane / kLanesC);
-          const int d = lane % kLanesC * 16;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = kWhole || d + 8 * e < a.D ? d + 8 * e : 0;
-            if (!kWhole || e == 0) {
-              if constexpr (kWhole) {
-                const u32x4 w = *reinterpret_cast<const u32x4_any1*>(both[v].base + (row * both[v].stride + (uint32_t)at));
-#pragma unroll
-                for (int q = 0; q < 4; ++q) codes[v][c][q] = w[q];
-              } else {
-                uint32_t w[2];
-                load_codes<8>(both[v].base + (row * both[v].stride + (uint32_t)at), w);
-                codes[v][c][2 * e] = w[0];
-                codes[v][c][2 * e + 1] = w[1];
-              }
-              scales[v][c][e] = both[v].scales[row * (uint32_t)a.nb + (uint32_t)((head + at) >> 7)];
-            }
-            if (kWhole && e == 1)  // 16 codes of a whole head are in one block where the head begins on 16
-              scales[v][c][1] = scales[v][c][0];
-          }
-        }
-    };
-    auto put = [&](int buffer) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int c = 0; c < kLoadsC; ++c) {
-          const int row = (wave * kLoadsC + c) * kRowsC + lane / kLanesC;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int piece = lane % kLanesC * 2 + e;
-            const float sc = scale_of(scales[v][c][e]);
-            const uint32_t w[2] = {codes[v][c][2 * e], codes[v][c][2 * e + 1]};
-            Frag<T, 8> f;
-            decode<T, 8>(w, &sc, f);
-            *reinterpret_cast<u32x4*>(&stage[buffer][v][row * kRow + (v == 0 ? turned(row, piece) : piece) * 16]) =
-                u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
-          }
-        }
-    };
-    if constexpr (kQ) {
-      if (count > 0) fetch(0);
-    } else {
-      if (count > 0) issue(0, 0);
+    if (wave == 0) {
+      const TreeNode t = tree_node(lane < a.N ? a.parents[(size_t)b * a.N + lane] : -2, lane, a.N);
+      line_of[lane] = t.line;
+      depth_of[lane] = t.depth;
     }
-    for (int i = 0; i < count; ++i) {
-      const int buffer = i & 1;
-      // The stage is there, and every wave is done with the other buffer.
-      if constexpr (kQ) {
-        put(buffer);
-        if (i + 1 < count) fetch(i + 1);
-        block_barrier();
-      } else {
-        wait_vmcnt<0>();
-        block_barrier();
-        if (i + 1 < count) issue(i + 1, buffer ^ 1);
-      }
+
+    // The rows' queries: row m is node m / G, head m % G of the KV head's G.
+    const int row0 = (kShared ? group * kWavesPerBlock + wave : group) * 16 * MT;
+    Frag<T, S::KW> q[MT][S::KS];
+    int node[MT];
 #pragma unroll
-      for (int half = 0; half < kStage / kKeys; ++half) {
+    for (int t = 0; t < MT; ++t) {
+      const int m = row0 + t * 16 + (lane & 15);
+      node[t] = m < a.R ? m / a.G : 0;
+      const int head = h * a.G + (m < a.R ? m - node[t] * a.G : 0);
+      const size_t row = ((size_t)b * a.N + node[t]) * a.Hq + head;
+      const uint8_t* p = static_cast<const uint8_t*>(a.q) + row * (size_t)a.D * kEs<T>;
+#pragma unroll
+      for (int s = 0; s < S::KS; ++s)
+#pragma unroll
+        for (int e = 0; e < S::KW; e += (S::KW > 8 ? 8 : S::KW)) {
+          constexpr int w = S::KW > 8 ? 8 : S::KW;
+          const int d = s * 4 * S::KW + g * S::KW + e;
+          Frag<T, w> f;
+          if (kWhole || d < a.D) load_values<T, w>(p + d * kEs<T>, f);
+          else clear(f);
+#pragma unroll
+          for (int i = 0; i < Frag<T, w>::kWords; ++i) q[t][s].w[e * kEs<T> / 4 + i] = f.w[i];
+        }
+    }
+
+    const int edge = a.window > 0 ? n + a.N - 1 - a.window : -1;  // no window hides a later entry from any node
+    const int head = h * a.D;
+    const bool one_scale = a.D % 128 == 0 ? head % 128 == 0 : head % 128 + a.D <= 128;
+
+    Sums<S, MT> z;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      z.m[t] = kNinf;
+      z.l[t] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::OT; ++i) z.o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __syncthreads();
+
+    // A tile of the cache: its first entry, and the tile's last key.
+    auto place = [&](int tile, int& j0) {
+      j0 = tile < tiles_first ? tile * kSpan : low + (tile - tiles_first) * kSpan;
+      return min(kSpan, (tile < tiles_first ? first : n) - j0) - 1;
+    };
+    auto rows_at = [&](const uint8_t* base, const uint8_t* scales, int j0) {
+      const size_t row = (size_t)b * a.L + j0;
+      Rows r;
+      r.base = base + (row * heads + head) * (kQ ? 1 : kEs<T>);
+      r.scales = kQ ? scales + row * (size_t)a.nb : nullptr;
+      r.stride = (uint32_t)heads * (kQ ? 1 : kEs<T>);
+      return r;
+    };
+    typedef typename std::conditional<kQ, KeyCodes<S>, typename S::Keys>::type CacheKeys;
+    CacheKeys k;
+    auto fetch_keys = [&](int tile) {
+      int j0;
+      // a constant leaves the offsets in registers
+      const int last = kWhole ? (place(tile, j0), kKeys - 1) : place(tile, j0);
+      const Rows r = rows_at(a.k_cache, a.k_scales, j0);
+      if constexpr (kQ) load_key_codes<S>(r, a.nb, head, last, a.D, one_scale, lane, k);
+      else load_keys<S, T>(r, last, a.D, lane, k);
+    };
+    auto add_key = [&](Frag<T, S::KW>& f, int u, int s, f32x4 (&x)[MT][S::U], int lane) {
+      if constexpr (!kWhole) cut_key<S, T>(a.D, s, lane, f);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        x[t][u] = product<T, S::KW>(f, q[t][s], s == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[t][u]);
+    };
+    // Tiles that some row does not see all of: values that are not finite are taken out of the product (bits of the
+    // slots that had some), and added to the rows that see them: an infinity or NaN outweighs whatever its weight is.
+    // value(key, d): the CW values from d on.
+    auto take_out = [&](typename S::Values& v) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < S::kSlots; ++i)
+#pragma unroll
+        for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+          for (int w = 0; w < Frag<T, S::CW>::kWords; ++w) {
+            const uint32_t f = not_finite<T>(v[i][s].w[w]);
+            v[i][s].w[w] &= ~f;
+            bad |= f != 0 ? 1u << i : 0u;
+          }
+      return bad;
+    };
+    auto add_others = [&](uint32_t bad, const uint32_t (&seen)[MT], int lane, auto value) {
+      const int g = lane >> 4;
+      if (!__any(bad != 0)) return;
+#pragma unroll 1
+      for (int key = 0; key < kKeys; ++key) {
+        const int group16 = (key >> 2) & 3, slot = (key >> 4) * 4 + (key & 3);
+        if (!__any((lane >> 4) == group16 && (bad >> slot & 1))) continue;
+#pragma unroll
+        for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int d = s * 16 * S::CW + (g * 4 + r) * S::CW;
+            const Frag<T, S::CW> f = value(key, d < a.D ? d : 0);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              const bool sees = __shfl(seen[t], group16 * 16 + (lane & 15)) >> slot & 1;
+#pragma unroll
+              for (int j = 0; j < S::CW; ++j) {
+                uint32_t w;
+                if constexpr (S::kF32) w = f.w[j];
+                else w = j & 1 ? f.w[j / 2] & 0xffff0000u : f.w[j / 2] << 16;
+                const bool add = sees && (w & 0x7f800000u) == 0x7f800000u;
+                z.o[t][s * S::CW + j][r] += add ? __uint_as_float(w) : 0.0f;
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers
+          }
+      }
+    };
+
+    // Tiles that every row sees whole: of the first entries, and behind the window's edge.
+    const int edge_tiles = edge >= low ? (edge - low) / kSpan + 1 : 0;
+    const int first_end = max(from, min(to, first / kSpan));
+    const int later = min(max(from, tiles_first + edge_tiles), to);
+    const int later_end = max(later, min(to, tiles_first + (n - low) / kSpan));
+    const int count = first_end - from + later_end - later;
+    auto whole_tile = [&](int i) { return i < first_end - from ? from + i : later + i - (first_end - from); };
+    if constexpr (kShared) {
+      // A row of shared memory has its 16-byte pieces in an order of its own, so that sixteen keys' pieces of one place
+      // lie in different banks.
+      constexpr int kRow = DP * 2, kPieces = kRow / 16;
+      auto turned = [](int row, int piece) { return piece ^ (kPieces == 16 ? row & 15 : row >> 1 & 7); };
+      // One stage: keys and values of 64 entries, a quarter by each wave.
+      constexpr int kRowsD = kWave / kPieces, kDmas = kStage / kRowsD / kWavesPerBlock;  // rows of a DMA
+      auto issue = [&](int i, int buffer) {
+        int j0;
+        place(whole_tile(i), j0);
+        const Rows kr = rows_at(a.k_cache, a.k_scales, j0), vr = rows_at(a.v_cache, a.v_scales, j0);
+#pragma unroll
+        for (int d = 0; d < kDmas; ++d) {
+          const int row0 = (wave * kDmas + d) * kRowsD, row = row0 + lane / kPieces, slot = lane % kPieces;
+          const int kd = turned(row, slot) * 8, vd = slot * 8;
+          const uint32_t k_at = (uint32_t)row * kr.stride + (uint32_t)((kWhole || kd < a.D ? kd : 0) * 2);
+          const uint32_t v_at = (uint32_t)row * vr.stride + (uint32_t)((kWhole || vd < a.D ? vd : 0) * 2);
+          dma16(kr.base + k_at, &stage[buffer][0][row0 * kRow]);
+          dma16(vr.base + v_at, &stage[buffer][1][row0 * kRow]);
+        }
+      };
+      // The same from codes, by way of registers: 16 per lane and load.
+      constexpr int kLanesC = DP / 16, kRowsC = kWave / kLanesC, kLoadsC = kStage / kRowsC / kWavesPerBlock;
+      uint32_t codes[2][kLoadsC][4], scales[2][kLoadsC][2];
+      auto fetch = [&](int i) {
+        int j0;
+        place(whole_tile(i), j0);
+        const Rows both[2] = {rows_at(a.k_cache, a.k_scales, j0), rows_at(a.v_cache, a.v_scales, j0)};
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int c = 0; c < kLoadsC; ++c) {
+            const uint32_t row = (uint32_t)((wave * kLoadsC + c) * kRowsC + lane / kLanesC);
+            const int d = lane % kLanesC * 16;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = kWhole || d + 8 * e < a.D ? d + 8 * e : 0;
+              if (!kWhole || e == 0) {
+                if constexpr (kWhole) {
+                  const uint8_t* p = both[v].base + (row * both[v].stride + (uint32_t)at);
+                  const u32x4 w = *reinterpret_cast<const u32x4_any1*>(p);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) codes[v][c][q] = w[q];
+                } else {
+                  uint32_t w[2];
+                  load_codes<8>(both[v].base + (row * both[v].stride + (uint32_t)at), w);
+                  codes[v][c][2 * e] = w[0];
+                  codes[v][c][2 * e + 1] = w[1];
+                }
+                scales[v][c][e] = both[v].scales[row * (uint32_t)a.nb + (uint32_t)((head + at) >> 7)];
+              }
+              if (kWhole && e == 1)  // 16 codes of a whole head are in one block where the head begins on 16
+                scales[v][c][1] = scales[v][c][0];
+            }
+          }
+      };
+      auto put = [&](int buffer) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int c = 0; c < kLoadsC; ++c) {
+            const int row = (wave * kLoadsC + c) * kRowsC + lane / kLanesC;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int piece = lane % kLanesC * 2 + e;
+              const float sc = scale_of(scales[v][c][e]);
+              const uint32_t w[2] = {codes[v][c][2 * e], codes[v][c][2 * e + 1]};
+              Frag<T, 8> f;
+              decode<T, 8>(w, &sc, f);
+              *reinterpret_cast<u32x4*>(&stage[buffer][v][row * kRow + (v == 0 ? turned(row, piece) : piece) * 16]) =
+                  u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
+            }
+          }
+      };
+      if constexpr (kQ) {
+        if (count > 0) fetch(0);
+      } else {
+        if (count > 0) issue(0, 0);
+      }
+      for (int i = 0; i < count; ++i) {
+        const int buffer = i & 1;
+        // The stage is there, and every wave is done with the other buffer.
+        if constexpr (kQ) {
+          put(buffer);
+          if (i + 1 < count) fetch(i + 1);
+          block_barrier();
+        } else {
+          wait_vmcnt<0>();
+          block_barrier();
+          if (i + 1 < count) issue(i + 1, buffer ^ 1);
+        }
+#pragma unroll
+        for (int half = 0; half < kStage / kKeys; ++half) {
+          f32x4 x[MT][S::U];
+#pragma unroll
+          for (int u = 0; u < S::U; ++u)
+#pragma unroll
+            for (int s = 0; s < S::KS; ++s) {
+              const int row = half * kKeys + u * 16 + (lane & 15);
+              const uint8_t* p = &stage[buffer][0][row * kRow + turned(row, 4 * s + g) * 16];
+              const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+              Frag<T, S::KW> f;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) f.w[q] = w[q];
+              add_key(f, u, s, x, lane);
+            }
+          const uint32_t none[MT] = {};
+          weigh<S, MT, false>(x, none, a.c, z);
+#pragma unroll
+          for (int s = 0; s < S::VS; ++s) {
+            Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+            for (int slot = 0; slot < S::kSlots; ++slot) {
+              typedef uint32_t words __attribute__((ext_vector_type(S::CW / 2)));
+              const words w = *reinterpret_cast<const words*>(
+                  &stage[buffer][1][(half * kKeys + key_of(slot, lane)) * kRow + (s * 16 + (lane & 15)) * S::CW * 2]);
+#pragma unroll
+              for (int q = 0; q < S::CW / 2; ++q) piece[slot].w[q] = w[q];
+            }
+            add_piece<S, T, MT>(piece, s, x, z);
+          }
+        }
+      }
+    } else {
+      if (wave < count) fetch_keys(whole_tile(wave));
+      for (int i = wave; i < count; i += kWavesPerBlock) {
+        int j0;
+        const int last = kWhole ? (place(whole_tile(i), j0), kKeys - 1) : place(whole_tile(i), j0);
+        const Rows rows = rows_at(a.v_cache, a.v_scales, j0);
+        typedef typename std::conditional<kQ, ValueCodes<S>, typename S::Values>::type CacheValues;
+        CacheValues raw;
+        if constexpr (kQ) load_row_codes<S>(rows, a.nb, head, last, a.D, lane, raw);
+        else load_rows<S, T>(rows, last, a.D, lane, raw);
         f32x4 x[MT][S::U];
 #pragma unroll
         for (int u = 0; u < S::U; ++u)
 #pragma unroll
           for (int s = 0; s < S::KS; ++s) {
-            const int row = half * kKeys + u * 16 + (lane & 15);
-            const u32x4 w = *reinterpret_cast<const u32x4*>(&stage[buffer][0][row * kRow + turned(row, 4 * s + g) * 16]);
-            Frag<T, S::KW> f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) f.w[q] = w[q];
-            add_key(f, u, s, x);
+            if constexpr (kQ) {
+              const float sc[2] = {scale_of(k.scale[u][s][0]), scale_of(k.scale[u][s][S::KW / 8 - 1])};
+              Frag<T, S::KW> f;
+              decode<T, S::KW>(k.w[u][s], sc, f);
+              add_key(f, u, s, x, lane);
+            } else {
+              add_key(k[u][s], u, s, x, lane);
+            }
           }
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + kWavesPerBlock < count) fetch_keys(whole_tile(i + kWavesPerBlock));
         const uint32_t none[MT] = {};
         weigh<S, MT, false>(x, none, a.c, z);
 #pragma unroll
         for (int s = 0; s < S::VS; ++s) {
           Frag<T, S::CW> piece[S::kSlots];
 #pragma unroll
-          for (int slot = 0; slot < S::kSlots; ++slot) {
-            typedef uint32_t words __attribute__((ext_vector_type(S::CW / 2)));
-            const words w = *reinterpret_cast<const words*>(
-                &stage[buffer][1][(half * kKeys + key_of(slot, lane)) * kRow + (s * 16 + (lane & 15)) * S::CW * 2]);
-#pragma unroll
-            for (int q = 0; q < S::CW / 2; ++q) piece[slot].w[q] = w[q];
+          for (int i8 = 0; i8 < S::kSlots; ++i8) {
+            if constexpr (kQ) {
+              const float sc = scale_of(raw.scale[i8][s]);
+              decode<T, S::CW>(raw.w[i8][s], &sc, piece[i8]);
+            } else {
+              piece[i8] = raw[i8][s];
+            }
           }
           add_piece<S, T, MT>(piece, s, x, z);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  } else {
-  if (wave < count) fetch_keys(whole_tile(wave));
-  for (int i = wave; i < count; i += kWavesPerBlock) {
-    int j0;
-    const int last = kWhole ? (place(whole_tile(i), j0), kKeys - 1) : place(whole_tile(i), j0);
-    const Rows rows = rows_at(a.v_cache, a.v_scales, j0);
-    typedef typename std::conditional<kQ, ValueCodes<S>, typename S::Values>::type CacheValues;
-    CacheValues raw;
-    if constexpr (kQ) load_row_codes<S>(rows, a.nb, head, last, a.D, lane, raw);
-    else load_rows<S, T>(rows, last, a.D, lane, raw);
-    f32x4 x[MT][S::U];
-#pragma unroll
-    for (int u = 0; u < S::U; ++u)
-#pragma unroll
-      for (int s = 0; s < S::KS; ++s) {
-        if constexpr (kQ) {
-          const float sc[2] = {scale_of(k.scale[u][s][0]), scale_of(k.scale[u][s][S::KW / 8 - 1])};
-          Frag<T, S::KW> f;
-          decode<T, S::KW>(k.w[u][s], sc, f);
-          add_key(f, u, s, x);
-        } else {
-          add_key(k[u][s], u, s, x);
-        }
-      }
-    __builtin_amdgcn_sched_barrier(0);
-    if (i + kWavesPerBlock < count) fetch_keys(whole_tile(i + kWavesPerBlock));
-    const uint32_t none[MT] = {};
-    weigh<S, MT, false>(x, none, a.c, z);
-#pragma unroll
-    for (int s = 0; s < S::VS; ++s) {
-      Frag<T, S::CW> piece[S::kSlots];
-#pragma unroll
-      for (int i8 = 0; i8 < S::kSlots; ++i8) {
-        if constexpr (kQ) {
-          const float sc = scale_of(raw.scale[i8][s]);
-          decode<T, S::CW>(raw.w[i8][s], &sc, piece[i8]);
-        } else {
-          piece[i8] = raw[i8][s];
-        }
-      }
-      add_piece<S, T, MT>(piece, s, x, z);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  }
 
-  // The others: ends, entries at the window's edge, and the tree's own, of which a node sees its ancestors and itself.
+    // The others: ends, entries at the window's edge, and the tree's own, of which a node sees its ancestors and
+    // itself.  A tile's 32 keys at a time.
+    constexpr int kParts = kSpan / kKeys;
+    const int before = later - first_end, careful = before + to - later_end;
 #pragma unroll 1
-  for (int at = kShared ? from * (kSpan / kKeys) : from + wave; at < to * (kSpan / kKeys); at += kShared ? 1 : kWavesPerBlock) {
-    const int tile = at / (kSpan / kKeys), part_of = at % (kSpan / kKeys) * kKeys;  // a tile's 32 keys at a time
-    if (tile < first_end || (tile >= later && tile < later_end)) continue;
-    const bool own = tile >= tiles_cache;
-    int j0, last;
-    typename S::Keys key;
-    typename S::Values v;
-    f32x4 x[MT][S::U];
-    Rows vr;
-    if (own) {
-      j0 = (tile - tiles_cache) * kSpan + part_of;
-      last = min(kKeys, a.N - j0) - 1;
-      if (last < 0) continue;
-      const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
-      const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
-      vr = Rows{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
-      load_keys<S, T>(kr, last, a.D, lane, key);
-      load_rows<S, T>(vr, last, a.D, lane, v);
-    } else {
-      last = min(place(tile, j0) - part_of, kKeys - 1);
-      j0 += part_of;
-      if (last < 0) continue;
-      const Rows kr = rows_at(a.k_cache, a.k_scales, j0);
-      vr = rows_at(a.v_cache, a.v_scales, j0);
-      if constexpr (kQ) {
-        KeyCodes<S> kc;
-        ValueCodes<S> vc;
-        load_key_codes<S>(kr, a.nb, head, last, a.D, one_scale, lane, kc);
-        load_row_codes<S>(vr, a.nb, head, last, a.D, lane, vc);
-#pragma unroll
-        for (int u = 0; u < S::U; ++u)
-#pragma unroll
-          for (int s = 0; s < S::KS; ++s) {
-            const float sc[2] = {scale_of(kc.scale[u][s][0]), scale_of(kc.scale[u][s][S::KW / 8 - 1])};
-            decode<T, S::KW>(kc.w[u][s], sc, key[u][s]);
-          }
-#pragma unroll
-        for (int i = 0; i < S::kSlots; ++i)
-#pragma unroll
-          for (int s = 0; s < S::VS; ++s) {
-            const float sc = scale_of(vc.scale[i][s]);
-            decode<T, S::CW>(vc.w[i][s], &sc, v[i][s]);
-          }
-      } else {
+    for (int i = kShared ? 0 : wave; i < careful * kParts; i += kShared ? 1 : kWavesPerBlock) {
+      const int part_of = i % kParts * kKeys, at = i / kParts;
+      const int tile = at < before ? first_end + at : later_end + at - before;
+      int my = tid;
+      asm volatile("" : "+v"(my));  // these few tiles' offsets are not kept through the loop above
+      const int lane = my & (kWave - 1);
+      const bool own = tile >= tiles_cache;
+      int j0, last;
+      typename S::Keys key;
+      typename S::Values v;
+      f32x4 x[MT][S::U];
+      Rows vr;
+      if (own) {
+        j0 = (tile - tiles_cache) * kSpan + part_of;
+        last = min(kKeys, a.N - j0) - 1;
+        if (last < 0) continue;
+        const size_t at = (((size_t)b * a.N + j0) * heads + head) * kEs<T>;
+        const Rows kr{static_cast<const uint8_t*>(a.k_new) + at, nullptr, (uint32_t)heads * kEs<T>};
+        vr = Rows{static_cast<const uint8_t*>(a.v_new) + at, nullptr, (uint32_t)heads * kEs<T>};
         load_keys<S, T>(kr, last, a.D, lane, key);
-        load_rows<S, T>(vr, last, a.D, lane, v);
-      }
-    }
+        if constexpr (!kQ) load_rows<S, T>(vr, last, a.D, lane, v);
+      } else {
+        last = min(place(tile, j0) - part_of, kKeys - 1);
+        j0 += part_of;
+        if (last < 0) continue;
+        const Rows kr = rows_at(a.k_cache, a.k_scales, j0);
+        vr = rows_at(a.v_cache, a.v_scales, j0);
+        if constexpr (kQ) {
+          KeyCodes<S> kc;
+          load_key_codes<S>(kr, a.nb, head, last, a.D, one_scale, lane, kc);
 #pragma unroll
-    for (int u = 0; u < S::U; ++u)
+          for (int u = 0; u < S::U; ++u)
 #pragma unroll
-      for (int s = 0; s < S::KS; ++s) add_key(key[u][s], u, s, x);
-    __builtin_amdgcn_sched_barrier(0);
-    uint32_t seen[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint64_t line = line_of[node[t]];
-      const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;  // up to here, but for the first
-      seen[t] = 0;
-#pragma unroll
-      for (int i = 0; i < S::kSlots; ++i) {
-        const int off = key_of(i, lane), j = min(j0 + off, own ? kMaxNodes - 1 : n);
-        const int position = own ? n + depth_of[j & (kMaxNodes - 1)] : j;
-        const bool sees = off <= last && (!own || (line >> (j & 63) & 1)) && (position > hidden || position < a.sinks);
-        seen[t] |= sees ? 1u << i : 0u;
-      }
-    }
-    weigh<S, MT, true>(x, seen, a.c, z);
-    const uint32_t bad = take_out(v);
-#pragma unroll
-    for (int s = 0; s < S::VS; ++s) {
-      Frag<T, S::CW> piece[S::kSlots];
-#pragma unroll
-      for (int i = 0; i < S::kSlots; ++i) piece[i] = v[i][s];
-      add_piece<S, T, MT>(piece, s, x, z);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    add_others(bad, seen, [&](int key_at, int d) {
-      const uint32_t at = (uint32_t)min(key_at, last);
-      Frag<T, S::CW> f;
-      if constexpr (kQ) {
-        if (!own) {
-          uint32_t w[S::CW / 4];
-          load_codes<S::CW>(vr.base + (at * vr.stride + (uint32_t)d), w);
-          const float sc = scale_of(vr.scales[at * (uint32_t)a.nb + (uint32_t)((head + d) >> 7)]);
-          decode<T, S::CW>(w, &sc, f);
-          return f;
+            for (int s = 0; s < S::KS; ++s) {
+              const float sc[2] = {scale_of(kc.scale[u][s][0]), scale_of(kc.scale[u][s][S::KW / 8 - 1])};
+              decode<T, S::KW>(kc.w[u][s], sc, key[u][s]);
+            }
+        } else {
+          load_keys<S, T>(kr, last, a.D, lane, key);
+          load_rows<S, T>(vr, last, a.D, lane, v);
         }
       }
-      load_values<T, S::CW>(vr.base + (at * vr.stride + (uint32_t)(d * kEs<T>)), f);
-      return f;
-    });
-  }
-
-  if constexpr (kShared) {
-    // A wave's rows are its own: lane (g, m) has values (4 g + r) CW .. of each piece of row m.
-    const size_t slot = ((size_t)item * a.groups + group) * (kWavesPerBlock * 16 * MT) + wave * 16 * MT;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      float l = z.l[t] + __shfl_xor(z.l[t], 16);
-      l += __shfl_xor(l, 32);
-      const int r = t * 16 + (lane & 15), m = row0 + r;
-      if (m >= a.R) continue;
-      if (!valid) l = __builtin_nanf("");
-      if (line_of[node[t]] == 0) l = 0.0f;
-      const float inv = 1.0f / l;
-      const size_t to = (((size_t)b * a.N + node[t]) * a.Hq + h * a.G + (m - node[t] * a.G)) * (size_t)a.D;
-      if (a.split > 1 && g == 0) a.stats[slot + r] = float2{l == 0.0f ? kNinf : z.m[t], l};
+      for (int u = 0; u < S::U; ++u)
 #pragma unroll
-      for (int s = 0; s < S::VS; ++s)
+        for (int s = 0; s < S::KS; ++s) add_key(key[u][s], u, s, x, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t seen[MT];
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4)
+      for (int t = 0; t < MT; ++t) {
+        const uint64_t line = line_of[node[t]];
+        const int hidden = a.window > 0 ? n + depth_of[node[t]] - a.window : -1;  // up to here, but for the first
+        seen[t] = 0;
 #pragma unroll
-          for (int j = 0; j < S::CW; j += 4) {
-            const int d = s * 16 * S::CW + (g * 4 + r4) * S::CW + j;
-            if (!kWhole && d >= a.D) continue;
-            f32x4 y;
+        for (int i = 0; i < S::kSlots; ++i) {
+          const int off = key_of(i, lane), j = min(j0 + off, own ? kMaxNodes - 1 : n);
+          const int position = own ? n + depth_of[j & (kMaxNodes - 1)] : j;
+          const bool sees = off <= last && (!own || (line >> (j & 63) & 1)) &&
+              (position > hidden || position < a.sinks);
+          seen[t] |= sees ? 1u << i : 0u;
+        }
+      }
+      weigh<S, MT, true>(x, seen, a.c, z);
+      if constexpr (kQ) {
+        if (!own) {  // now, when the keys' registers are free
+          ValueCodes<S> vc;
+          load_row_codes<S>(vr, a.nb, head, last, a.D, lane, vc);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = z.o[t][s * S::CW + j + e][r4];
-            if (a.split > 1) {
-              if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + r) * (size_t)a.D + d) = y;
-            } else {
+          for (int i = 0; i < S::kSlots; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
-              typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
-              *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + to + d) = pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+            for (int s = 0; s < S::VS; ++s) {
+              const float sc = scale_of(vc.scale[i][s]);
+              decode<T, S::CW>(vc.w[i][s], &sc, v[i][s]);
             }
+        } else {
+          load_rows<S, T>(vr, last, a.D, lane, v);
+        }
+      }
+      const uint32_t bad = take_out(v);
+#pragma unroll
+      for (int s = 0; s < S::VS; ++s) {
+        Frag<T, S::CW> piece[S::kSlots];
+#pragma unroll
+        for (int i = 0; i < S::kSlots; ++i) piece[i] = v[i][s];
+        add_piece<S, T, MT>(piece, s, x, z);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      add_others(bad, seen, lane, [&](int key_at, int d) {
+        const uint32_t at = (uint32_t)min(key_at, last);
+        Frag<T, S::CW> f;
+        if constexpr (kQ) {
+          if (!own) {
+            uint32_t w[S::CW / 4];
+            load_codes<S::CW>(vr.base + (at * vr.stride + (uint32_t)d), w);
+            const float sc = scale_of(vr.scales[at * (uint32_t)a.nb + (uint32_t)((head + d) >> 7)]);
+            decode<T, S::CW>(w, &sc, f);
+            return f;
           }
+        }
+        load_values<T, S::CW>(vr.base + (at * vr.stride + (uint32_t)(d * kEs<T>)), f);
+        return f;
+      });
     }
-    return;
-  }
 
-  // The waves' results, 16 rows at a time.
+    if constexpr (kShared) {
+      // A wave's rows are its own: lane (g, m) has values (4 g + r) CW .. of each piece of row m.
+      const size_t slot = (slot0 * a.groups + group) * (kWavesPerBlock * 16 * MT) + wave * 16 * MT;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    z.l[t] += __shfl_xor(z.l[t], 16);
-    z.l[t] += __shfl_xor(z.l[t], 32);
-    if (g == 0) stat[wave][t * 16 + (lane & 15)] = float2{z.m[t], z.l[t]};
-  }
-  __syncthreads();
-  const size_t slot = ((size_t)item * a.groups + group) * (16 * MT);
+      for (int t = 0; t < MT; ++t) {
+        float l = z.l[t] + __shfl_xor(z.l[t], 16);
+        l += __shfl_xor(l, 32);
+        const int r = t * 16 + (lane & 15), m = row0 + r;
+        if (m >= a.R) continue;
+        if (!valid) l = __builtin_nanf("");
+        if (line_of[node[t]] == 0) l = 0.0f;
+        const float inv = 1.0f / l;
+        const size_t to = (((size_t)b * a.N + node[t]) * a.Hq + h * a.G + (m - node[t] * a.G)) * (size_t)a.D;
+        if (!alone && g == 0) a.stats[slot + r] = float2{l == 0.0f ? kNinf : z.m[t], l};
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    {
-      const int r = t * 16 + (lane & 15);
-      float m = stat[0][r].x;
+        for (int s = 0; s < S::VS; ++s)
 #pragma unroll
-      for (int w = 1; w < kWavesPerBlock; ++w) m = fmaxf(m, stat[w][r].x);
-      const float f = z.m[t] == kNinf ? 0.0f : exp2_of(z.m[t] - m);
-      float* to = &part[wave][(lane & 15) * kPad<DP>];
+          for (int r4 = 0; r4 < 4; ++r4)
 #pragma unroll
-      for (int s = 0; s < S::VS; ++s)
+            for (int j = 0; j < S::CW; j += 4) {
+              const int d = s * 16 * S::CW + (g * 4 + r4) * S::CW + j;
+              if (!kWhole && d >= a.D) continue;
+              f32x4 y;
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4)
+              for (int e = 0; e < 4; ++e) y[e] = z.o[t][s * S::CW + j + e][r4];
+              if (!alone) {
+                if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + r) * (size_t)a.D + d) = y;
+              } else {
 #pragma unroll
-          for (int j = 0; j < S::CW; j += 4) {
-            f32x4 y;
+                for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
+                typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
+                *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + to + d) =
+                    pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+              }
+            }
+      }
+    } else {
+      // The waves' results, 16 rows at a time.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = z.l[t] == 0.0f ? 0.0f : z.o[t][s * S::CW + j + i][r4] * f;
-            *reinterpret_cast<f32x4*>(to + s * 16 * S::CW + (g * 4 + r4) * S::CW + j) = y;
+      for (int t = 0; t < MT; ++t) {
+        z.l[t] += __shfl_xor(z.l[t], 16);
+        z.l[t] += __shfl_xor(z.l[t], 32);
+        if (g == 0) stat[wave][t * 16 + (lane & 15)] = float2{z.m[t], z.l[t]};
+      }
+      __syncthreads();
+      const size_t slot = (slot0 * a.groups + group) * (16 * MT);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        {
+          const int r = t * 16 + (lane & 15);
+          float m = stat[0][r].x;
+#pragma unroll
+          for (int w = 1; w < kWavesPerBlock; ++w) m = fmaxf(m, stat[w][r].x);
+          const float f = z.m[t] == kNinf ? 0.0f : exp2_of(z.m[t] - m);
+          float* to = &part[wave][(lane & 15) * kPad<DP>];
+#pragma unroll
+          for (int s = 0; s < S::VS; ++s)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+              for (int j = 0; j < S::CW; j += 4) {
+                f32x4 y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = z.l[t] == 0.0f ? 0.0f : z.o[t][s * S::CW + j + i][r4] * f;
+                *reinterpret_cast<f32x4*>(to + s * 16 * S::CW + (g * 4 + r4) * S::CW + j) = y;
+              }
+        }
+        __syncthreads();
+        constexpr int kQuads = DP / 4;
+#pragma unroll
+        for (int k = 0; k < 16 * kQuads / kBlock; ++k) {
+          const int at = k * kBlock + tid, r = at / kQuads, d = at % kQuads * 4;
+          const int m = row0 + t * 16 + r;
+          if (m >= a.R || d >= a.D) continue;
+          f32x4 y = *reinterpret_cast<const f32x4*>(&part[0][r * kPad<DP> + d]);
+#pragma unroll
+          for (int w = 1; w < kWavesPerBlock; ++w) y += *reinterpret_cast<const f32x4*>(&part[w][r * kPad<DP> + d]);
+          float ref = stat[0][t * 16 + r].x;
+#pragma unroll
+          for (int w = 1; w < kWavesPerBlock; ++w) ref = fmaxf(ref, stat[w][t * 16 + r].x);
+          float l = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWavesPerBlock; ++w) {
+            const float2 s = stat[w][t * 16 + r];
+            l += s.x == kNinf ? s.y : s.y * exp2_of(s.x - ref);
           }
-    }
-    __syncthreads();
-    constexpr int kQuads = DP / 4;
+          const int nd = m / a.G;
+          if (!valid) l = __builtin_nanf("");
+          if (line_of[nd] == 0) l = 0.0f;
+          if (!alone) {
+            if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
+            if (d == 0) a.stats[slot + t * 16 + r] = float2{l == 0.0f ? kNinf : ref, l};
+            continue;
+          }
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int k = 0; k < 16 * kQuads / kBlock; ++k) {
-      const int at = k * kBlock + threadIdx.x, r = at / kQuads, d = at % kQuads * 4;
-      const int m = row0 + t * 16 + r;
-      if (m >= a.R || d >= a.D) continue;
-      f32x4 y = *reinterpret_cast<const f32x4*>(&part[0][r * kPad<DP> + d]);
-#pragma unroll
-      for (int w = 1; w < kWavesPerBlock; ++w) y += *reinterpret_cast<const f32x4*>(&part[w][r * kPad<DP> + d]);
-      float ref = stat[0][t * 16 + r].x;
-#pragma unroll
-      for (int w = 1; w < kWavesPerBlock; ++w) ref = fmaxf(ref, stat[w][t * 16 + r].x);
-      float l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWavesPerBlock; ++w) {
-        const float2 s = stat[w][t * 16 + r];
-        l += s.x == kNinf ? s.y : s.y * exp2_of(s.x - ref);
-      }
-      const int nd = m / a.G;
-      if (!valid) l = __builtin_nanf("");
-      if (line_of[nd] == 0) l = 0.0f;
-      if (a.split > 1) {
-        if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
-        if (d == 0) a.stats[slot + t * 16 + r] = float2{l == 0.0f ? kNinf : ref, l};
-        continue;
-      }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = l == 0.0f ? 0.0f : y[i] * inv;
-      const size_t at_out = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
-      if constexpr (S::kF32) {
-        typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
-        *reinterpret_cast<quad*>(static_cast<float*>(a.out) + at_out) = quad{y[0], y[1], y[2], y[3]};
-      } else {
-        typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
-        *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + at_out) = pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+          for (int i = 0; i < 4; ++i) y[i] = l == 0.0f ? 0.0f : y[i] * inv;
+          const size_t at_out = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
+          if constexpr (S::kF32) {
+            typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
+            *reinterpret_cast<quad*>(static_cast<float*>(a.out) + at_out) = quad{y[0], y[1], y[2], y[3]};
+          } else {
+            typedef uint32_t pair __attribute__((ext_vector_type(2), aligned(2)));
+            *reinterpret_cast<pair*>(static_cast<uint16_t*>(a.out) + at_out) =
+                pair{pack2(y[0], y[1]), pack2(y[2], y[3])};
+          }
+        }
+        __syncthreads();
       }
     }
-    __syncthreads();
+    left -= to - from;
+    if (left <= 0) return;
+    begin = 0;
+    if (++h == a.Hkv) h = 0, ++b;
+    __syncthreads();  // the tree's lines and the waves' results give way to the next ones
   }
 }
 
-// The splits' results of a row.  A wave's lanes first have the splits' references and sums, one each, then 16-byte
-// pieces of their results: as many splits at a time as a row's pieces leave lanes for.
+// The rows of a KV head whose keys several blocks have: a range's first piece is in its first slot, another in its
+// second.  A wave has a row.  Its lanes first have the pieces' references and sums, one each, then 16-byte parts of
+// their results: as many pieces at a time as a row's parts leave lanes for, and several such loads in flight.
 template <typename T>
-__global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t rows, int rows_per_slot) {
-  const uint32_t row = blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  if (row >= rows) return;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int m = (int)(row % (uint32_t)a.R);
-  const uint32_t pair = row / (uint32_t)a.R;  // b * Hkv + h
-  const int h = (int)(pair % (uint32_t)a.Hkv), b = (int)(pair / (uint32_t)a.Hkv);
-  const int group = m / rows_per_slot, r = m % rows_per_slot;
-  const size_t slot0 = ((size_t)pair * a.split * a.groups + group) * rows_per_slot + r, step = (size_t)a.groups * rows_per_slot;
+__global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_per_block) {
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int m = (int)blockIdx.x * kWavesPerBlock + wave, b = (int)blockIdx.y / a.Hkv, h = (int)blockIdx.y % a.Hkv;
+  if (m >= a.R) return;
+  int first = (int)blockIdx.y * a.split, next = first + 1, count = a.split, step = 1;  // the pieces' slots
+  if (a.ranges > 0) {
+    int before = 0, all = 0;
+    for (int i = lane; i < a.B; i += kWave) {
+      const int t = keys_of(a, a.span, a.cache_len[i]).tiles;
+      all += t;
+      before += i < b ? t : 0;
+    }
+    const int per = range_of(a, dpp::lane63(lanes_scan(all)) * a.Hkv);
+    const int tiles = keys_of(a, a.span, a.cache_len[b]).tiles;
+    const int begin = dpp::lane63(lanes_scan(before)) * a.Hkv + h * tiles;
+    const int range = begin / per;
+    count = (begin + tiles - 1) / per - range + 1;
+    if (count == 1) return;
+    first = 2 * range + (begin != range * per ? 1 : 0);  // not its range's first piece?
+    next = 2 * range + 2;
+    step = 2;
+  }
+  const int group = m / rows_per_block, r = m % rows_per_block;
+  auto at = [&](int i) {
+    return ((size_t)(i == 0 ? first : next + (i - 1) * step) * a.groups + group) * rows_per_block + r;
+  };
   float ref = kNinf;
   bool bad = false;
-  for (int s = lane; s < a.split; s += kWave) {
-    const float2 w = a.stats[slot0 + s * step];
+  for (int i = lane; i < count; i += kWave) {
+    const float2 w = a.stats[at(i)];
     bad |= w.y != w.y;
     if (w.y != 0.0f) ref = fmaxf(ref, w.x);
   }
   ref = wave_max(ref);
   bad = __any(bad);
-  const int pieces = a.D > 128 ? 64 : a.D > 64 ? 32 : 16, at_once = kWave / pieces;
-  const int d = (lane & (pieces - 1)) * 4;
+  const int parts = a.D > 128 ? 64 : a.D > 64 ? 32 : 16, at_once = kWave / parts;
+  const int d = (lane & (parts - 1)) * 4;
   float l = 0.0f;
   f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int s = lane / pieces; s < a.split; s += at_once) {
-    const float2 w = a.stats[slot0 + s * step];
-    const float f = w.y == 0.0f ? 0.0f : w.x == kNinf ? 1.0f : exp2_of(w.x - ref);
-    l += w.y * f;
-    if (d < a.D && w.y != 0.0f) y += *reinterpret_cast<const f32x4*>(a.acc + (slot0 + s * step) * (size_t)a.D + d) * f;
-  }
-  for (int o = pieces; o < kWave; o *= 2) {
+  auto add = [&](auto loads) {
+    constexpr int kLoads = decltype(loads)::value;
+    for (int i = lane / parts; i < count; i += at_once * kLoads) {
+      float2 w[kLoads];
+      f32x4 v[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const size_t x = at(min(i + j * at_once, count - 1));
+        w[j] = a.stats[x];
+        v[j] = *reinterpret_cast<const f32x4*>(a.acc + x * (size_t)a.D + (d < a.D ? d : 0));
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        if (i + j * at_once >= count || w[j].y == 0.0f) continue;
+        const float f = w[j].x == kNinf ? 1.0f : exp2_of(w[j].x - ref);
+        l += w[j].y * f;
+        y += v[j] * f;
+      }
+    }
+  };
+  if (count > 4 * at_once) add(std::integral_constant<int, 8>{});
+  else add(std::integral_constant<int, 2>{});
+  for (int o = parts; o < kWave; o *= 2) {
     l += __shfl_xor(l, o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] += __shfl_xor(y[i], o);
   }
-  if (lane >= pieces || d >= a.D) return;
+  if (lane >= parts || d >= a.D) return;
   const float inv = 1.0f / l;
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = bad ? __builtin_nanf("") : l == 0.0f ? 0.0f : y[i] * inv;
@@ -1005,16 +1165,17 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, uint32_t 
 
 template <typename T, bool kQ, int DP, int MT, bool kShared>
 void start(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (a.D == DP) hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, true, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
-  else hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, false, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  if (a.D == DP)
+    hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, true, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
+  else
+    hipLaunchKernelGGL((tree_attention_kernel<T, kQ, DP, MT, false, kShared>), dim3(p.grid), dim3(kBlock), 0, st, a);
 }
 
 template <typename T, bool kQ, int DP>
 void start_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   if constexpr (!std::is_same<T, float>::value && DP <= 128) {
     if (p.shared) {
-      if (p.mt == 2) start<T, kQ, DP, 2, true>(a, p, st);
-      else start<T, kQ, DP, 4, true>(a, p, st);
+      start<T, kQ, DP, 2, true>(a, p, st);
       return;
     }
   }
@@ -1023,15 +1184,14 @@ void start_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 }
 
 template <typename T, bool kQ>
-hipError_t run(const AttnArgs& a, const AttnPlan& p, int B, hipStream_t st) {
+hipError_t run(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   if (p.dp == 64) start_rows<T, kQ, 64>(a, p, st);
   else if (p.dp == 128) start_rows<T, kQ, 128>(a, p, st);
   else start_rows<T, kQ, 256>(a, p, st);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.split == 1) return e;
-  const uint32_t rows = (uint32_t)B * a.Hkv * a.R;
-  hipLaunchKernelGGL((tree_join_kernel<T>), dim3((rows + kWavesPerBlock - 1) / kWavesPerBlock), dim3(kBlock), 0, st, a,
-                     rows, p.rows);
+  if (e != hipSuccess || (p.ranges == 0 && p.split == 1)) return e;
+  const dim3 grid((unsigned)((a.R + kWavesPerBlock - 1) / kWavesPerBlock), (unsigned)(a.B * a.Hkv));
+  hipLaunchKernelGGL((tree_join_kernel<T>), grid, dim3(kBlock), 0, st, a, p.rows);
   return hipGetLastError();
 }
 
@@ -1051,10 +1211,11 @@ hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, 
   a.parents = io.parents;
   a.cache_len = io.cache_len;
   a.out = const_cast<void*>(io.out);
-  if (plan.split > 1) {
+  if (plan.slots > 0) {
     a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.stats);
     a.acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.acc);
   }
+  a.B = B;
   a.N = N;
   a.Hq = Hq;
   a.Hkv = Hkv;
@@ -1065,12 +1226,15 @@ hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, 
   a.R = plan.R;
   a.groups = plan.groups;
   a.split = plan.split;
-  a.items = (uint32_t)B * Hkv * plan.split;
+  a.ranges = plan.ranges;
+  a.least = plan.least;
+  a.step = plan.step;
+  a.span = plan.span;
   a.window = window;
   a.sinks = sinks;
   a.c = scale * 1.44269504088896340736f;
-  if (dtype == 1) return quantized ? run<uint16_t, true>(a, plan, B, st) : run<uint16_t, false>(a, plan, B, st);
-  return quantized ? run<float, true>(a, plan, B, st) : run<float, false>(a, plan, B, st);
+  if (dtype == 1) return quantized ? run<uint16_t, true>(a, plan, st) : run<uint16_t, false>(a, plan, st);
+  return quantized ? run<float, true>(a, plan, st) : run<float, false>(a, plan, st);
 }
 
 }  // namespace sv

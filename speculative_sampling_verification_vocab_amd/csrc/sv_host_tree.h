@@ -13,7 +13,8 @@ constexpr int32_t kMaxLength = 1 << 30;  // cache positions: sums with depths an
 
 // Launch plan of spec_tree_attention and its quantised form.  The rows of one
 // KV head are its G = Hq / Hkv query heads of every node, node by node; a block
-// takes `rows` of them against one split of the keys.
+// takes `rows` of them against some of their keys: one of `split` equal pieces,
+// or one of `ranges` equal parts of the keys of the whole batch.
 struct AttnPlan {
   int32_t R;       // rows per (sequence, KV head)
   int32_t dp;      // head size rounded up to 64, 128 or 256
@@ -21,18 +22,41 @@ struct AttnPlan {
   int32_t mt;      // tiles of 16 rows per wave
   int32_t rows;    // rows per block
   int32_t groups;  // blocks that share the rows of a KV head
-  int32_t split;   // blocks that share the keys
-  size_t slots;    // B * Hkv * groups * split: partial results, and blocks but for the round-up
+  int32_t split;   // blocks (per group) that share the keys of a sequence's KV head
+  int32_t ranges;  // blocks (per group) that share those of the whole batch, or 0
+  int32_t least;   // tiles that a range has at least
+  int32_t step;    // and whose multiple it has: a tile per wave, where these have keys of their own
+  int32_t span;    // keys of a tile
   unsigned grid;
-  size_t stats, acc, total;  // workspace byte offsets (split > 1)
+  size_t slots;              // partial results of a group
+  size_t stats, acc, total;  // workspace byte offsets
 };
 
-constexpr int kAttnStage = 64;         // keys that the waves of a block share at a time
-constexpr int kAttnBlocksWanted = 512; // 2 per CU
-constexpr int kAttnSplitKeys = 512;    // at least so many cache positions per split
+constexpr int kAttnStage = 64;          // keys that the waves of a block share at a time
+constexpr int kAttnBlocksWanted = 512;  // 2 per CU
+constexpr int kAttnLeastKeys = 256;     // keys of a piece or range at least
+constexpr int kAttnMostKeys = 2048;     // keys of a piece at most, where sequences differ in length
+
+// How the keys are shared out, with times at 32 query heads on 8 KV heads of 128:
+//  - a block per pair of sequence and KV head up to 1024 keys (B=1 N=4 L=1000: 15.7 us, in pieces 20.3), and from
+//    4096 pairs on;
+//  - pieces of each pair's own keys, all found from the block's number, while the longest piece is short: a batch of
+//    sequences of half to all of L takes 35 us in pieces and 40 in ranges at B=8 N=16 L=4096, 8-bit B=4 N=32 L=16384
+//    59 and 66 us;
+//  - ranges of the batch's keys from there on, which every length fills alike: 8-bit B=64 N=1 L=8192 takes 185 us, a
+//    block per pair 214; bf16 B=64 N=64 L=8192 12 % less.  A block has to find its range first (2 to 3 us), and most
+//    have parts of two pairs.
+// 384 or 768 blocks in place of 512 are slower by 7 to 30 %.
+//
+// Which rows a block has, in the same terms:
+//  - up to 64 rows: the waves have keys of their own (B=8 N=16 L=4096 35 us, shared 39; 8-bit B=1 N=16 L=131072 80 and
+//    92; bf16 there 119 and 113), 16 rows of them where there are no more;
+//  - from there on shared keys (8-bit B=4 N=32 L=16384 58 us, own 84), 32 rows a wave: with 64 one wave per SIMD is left
+//    and B=64 N=64 L=8192 takes 815 us, not 685.
 
 inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
-                                     spec_dtype_t dtype, bool aligned, AttnPlan* p, bool* empty) {
+                                     int32_t window, int32_t sinks, spec_dtype_t dtype, bool aligned, AttnPlan* p,
+                                     bool* empty) {
   if (!valid_dtype(dtype) || B < 0 || N < 0 || Hq < 1 || Hkv < 1 || D < 1 || L_max < 0) return SPEC_ERR_INVALID_ARG;
   if (Hq % Hkv != 0 || N > kMaxNodes || D % 8 != 0 || D > 256 || L_max > kMaxLength) return SPEC_ERR_UNSUPPORTED;
   if ((long long)Hkv * D > (1 << 22) || Hq > (1 << 22)) return SPEC_ERR_UNSUPPORTED;  // 32 rows' offsets stay in uint32
@@ -44,22 +68,36 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
   p->R = N * (Hq / Hkv);
   p->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   p->shared = aligned && dtype == SPEC_BF16 && p->dp <= 128 && p->R > 64;
-  p->mt = p->shared ? (p->R <= 128 ? 2 : 4) : p->R <= 16 || p->dp == 256 ? 1 : 2;
+  p->mt = !p->shared && (p->R <= 16 || p->dp == 256) ? 1 : 2;
   p->rows = 16 * p->mt * (p->shared ? kWavesPerBlock : 1);
   p->groups = (p->R + p->rows - 1) / p->rows;
-  const unsigned long long pairs = (unsigned long long)B * Hkv * p->groups;
-  if (pairs > max_blocks(kBlock) / 64) return SPEC_ERR_UNSUPPORTED;
-  long long s = (p->shared && p->mt == 4 ? kAttnBlocksWanted / 2 : kAttnBlocksWanted) / pairs;
-  const long long most_splits = ((long long)L_max + N + kAttnSplitKeys - 1) / kAttnSplitKeys;
-  if (s > most_splits) s = most_splits;
-  p->split = s < 1 ? 1 : (int32_t)s;
-  p->slots = (size_t)pairs * p->split;
-  const size_t eight = ((size_t)B * Hkv * p->split + 7) / 8 * 8 * p->groups;
-  if (eight > max_blocks(kBlock)) return SPEC_ERR_UNSUPPORTED;
-  p->grid = (unsigned)eight;
+  p->span = p->shared ? kAttnStage : dtype == SPEC_F32 && p->dp == 256 ? 16 : 32;
+  const size_t pairs = (size_t)B * (size_t)Hkv;
+  if (pairs * (size_t)p->groups > max_blocks(kBlock) / 8) return SPEC_ERR_UNSUPPORTED;
+  const size_t wanted = kAttnBlocksWanted > p->groups ? (size_t)(kAttnBlocksWanted / p->groups) : 1;
+  const size_t keys = (size_t)L_max + (size_t)N;  // of a pair at most
+  p->least = kAttnLeastKeys / p->span;
+  p->step = p->shared ? 1 : kWavesPerBlock;
+  p->split = 1;
+  p->ranges = 0;
+  p->slots = 0;
+  if (pairs < 8 * wanted && keys > 4 * kAttnLeastKeys) {
+    const size_t most = pairs * (keys / kAttnLeastKeys);
+    const size_t ranges = wanted < most ? wanted : most;
+    if (pairs * (keys / p->span + 4) > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+    p->slots = 2 * ranges;  // whatever the window
+    const size_t seen = window > 0 && (size_t)window + (size_t)sinks < (size_t)L_max ? (size_t)window + sinks + N : keys;
+    size_t split = wanted / pairs;
+    if (split > (seen + kAttnLeastKeys - 1) / kAttnLeastKeys) split = (seen + kAttnLeastKeys - 1) / kAttnLeastKeys;
+    if (split < 1) split = 1;
+    if (B == 1 || seen - (size_t)N <= split * kAttnMostKeys) p->split = (int32_t)split;
+    else p->ranges = (int32_t)ranges;
+  }
+  const size_t items = p->ranges > 0 ? (size_t)p->ranges : pairs * (size_t)p->split;
+  p->grid = (unsigned)((items + 7) / 8 * 8 * p->groups);
   p->stats = p->acc = p->total = 0;
-  if (p->split > 1) {
-    const size_t rows = p->slots * (size_t)p->rows;
+  if (p->slots > 0) {
+    const size_t rows = p->slots * (size_t)p->groups * (size_t)p->rows;
     if (rows > kMaxBytes / ((size_t)D * 4 + 8)) return SPEC_ERR_UNSUPPORTED;
     p->acc = align256(rows * 8);
     p->total = p->acc + align256(rows * (size_t)D * 4);
@@ -67,14 +105,14 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
   return SPEC_OK;
 }
 
-// Workspace bytes of a call on any buffers.
+// Workspace bytes of a call on any buffers, with any window.
 inline spec_status_t attention_workspace(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
                                          spec_dtype_t dtype, size_t* bytes) {
   AttnPlan p{};
   bool empty = false;
   size_t most = 0;
   for (int aligned = 0; aligned < 2; ++aligned) {
-    const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, dtype, aligned != 0, &p, &empty);
+    const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, 0, 0, dtype, aligned != 0, &p, &empty);
     if (sc != SPEC_OK) return sc;
     if (!empty && p.total > most) most = p.total;
   }
@@ -98,9 +136,9 @@ inline spec_status_t validate_attention(const AttnPointers& a, bool quantized, i
   if (sw != SPEC_OK) return sw;
   // Values go to shared memory in whole 16-byte pieces.
   const bool aligned = quantized || ((uintptr_t)a.k_cache % 16 == 0 && (uintptr_t)a.v_cache % 16 == 0);
-  const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, dtype, aligned, p, empty);
-  if (sc != SPEC_OK) return sc;
   if (!(scale > 0.0f && isfinite(scale)) || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
+  const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, window, sinks, dtype, aligned, p, empty);
+  if (sc != SPEC_OK) return sc;
   if (*empty) return SPEC_OK;
   if (!a.q || !a.k_new || !a.v_new || !a.parents || !a.cache_len || !a.out) return SPEC_ERR_INVALID_ARG;
   if (L_max > 0 && (!a.k_cache || !a.v_cache || (quantized && (!a.k_scales || !a.v_scales)))) return SPEC_ERR_INVALID_ARG;
