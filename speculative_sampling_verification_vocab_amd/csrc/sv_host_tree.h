@@ -66,6 +66,7 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
   if (!mul_fits((size_t)B * (size_t)(L_max > N ? L_max : N), (size_t)Hq * (size_t)D * elem_size(dtype), kMaxBytes, &n))
     return SPEC_ERR_UNSUPPORTED;
   p->R = N * (Hq / Hkv);
+  if ((size_t)p->R > max_blocks(kBlock) * kWavesPerBlock) return SPEC_ERR_UNSUPPORTED;  // the join's waves have one each
   p->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   p->shared = aligned && dtype == SPEC_BF16 && p->dp <= 128 && p->R > 64;
   p->mt = !p->shared && (p->R <= 16 || p->dp == 256) ? 1 : 2;
@@ -163,7 +164,7 @@ inline spec_status_t check_tree_commit(const TreeCommitIO& io, int32_t P, int32_
                                        int32_t E, spec_dtype_t dtype, bool* empty) {
   if (!valid_dtype(dtype)) return SPEC_ERR_INVALID_ARG;
   if (P < 0 || B < 0 || N < 1 || L_max < 0 || E < 0) return SPEC_ERR_INVALID_ARG;
-  if (N > kMaxNodes) return SPEC_ERR_UNSUPPORTED;
+  if (N > kMaxNodes || (size_t)B > max_blocks(kBlock) * kWavesPerBlock) return SPEC_ERR_UNSUPPORTED;  // a wave each
   *empty = B == 0;
   if (*empty) return SPEC_OK;
   const int32_t* in[] = {io.tokens, io.parents, io.sampled, io.cache_len};
