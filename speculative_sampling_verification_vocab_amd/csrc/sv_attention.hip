@@ -32,7 +32,7 @@
 //   B=32 N=8 L=8192 bf16      184 us  4.4 TB/s, and 8-bit 122 us, 3.4 TB/s
 //   B=1 N=16 L=131072 bf16    119 us  4.5 TB/s, and 8-bit 80 us, 3.4 TB/s: the registers leave two waves per
 //                             SIMD, and the loads that those have in flight bound it
-//   B=64 N=64 L=8192 bf16     685 us  610 TFLOP/s of 1130 that a large product reaches: softmax and permutes
+//   B=64 N=64 L=8192 bf16     636 us  655 TFLOP/s of 1130 that a large product reaches: softmax and permutes
 //                             share the issue slots with the matrix instructions
 //
 // Sums, maxima and both products' accumulators are fp32.  The weights p are
@@ -1079,13 +1079,15 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
 }
 
 // The rows of a KV head whose keys several blocks have: a range's first piece is in its first slot, another in its
-// second.  A wave has a row.  Its lanes first have the pieces' references and sums, one each, then 16-byte parts of
-// their results: as many pieces at a time as a row's parts leave lanes for, and several such loads in flight.
+// second.  A wave has `rows` rows, one after the other.  Its lanes have 16-byte parts of the pieces' results: as many
+// pieces at a time as a row's parts leave lanes for, and several such loads in flight.  A wave per row spends more on
+// finding the pieces than on joining them where rows are many: B=64 N=64 L=8192 85 us, 38 with eight rows a wave.
 template <typename T>
-__global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_per_block) {
+__global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_per_block, int rows) {
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const int m = (int)blockIdx.x * kWavesPerBlock + wave, b = (int)blockIdx.y / a.Hkv, h = (int)blockIdx.y % a.Hkv;
-  if (m >= a.R) return;
+  const int m0 = ((int)blockIdx.x * kWavesPerBlock + wave) * rows;
+  const int b = (int)blockIdx.y / a.Hkv, h = (int)blockIdx.y % a.Hkv;
+  if (m0 >= a.R) return;
   int first = (int)blockIdx.y * a.split, next = first + 1, count = a.split, step = 1;  // the pieces' slots
   if (a.ranges > 0) {
     int before = 0, all = 0;
@@ -1104,62 +1106,72 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_
     next = 2 * range + 2;
     step = 2;
   }
-  const int group = m / rows_per_block, r = m % rows_per_block;
-  auto at = [&](int i) {
-    return ((size_t)(i == 0 ? first : next + (i - 1) * step) * a.groups + group) * rows_per_block + r;
-  };
-  float ref = kNinf;
-  bool bad = false;
-  for (int i = lane; i < count; i += kWave) {
-    const float2 w = a.stats[at(i)];
-    bad |= w.y != w.y;
-    if (w.y != 0.0f) ref = fmaxf(ref, w.x);
-  }
-  ref = wave_max(ref);
-  bad = __any(bad);
   const int parts = a.D > 128 ? 64 : a.D > 64 ? 32 : 16, at_once = kWave / parts;
   const int d = (lane & (parts - 1)) * 4;
-  float l = 0.0f;
-  f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](auto loads) {
+  auto join = [&](int m, auto loads) {
     constexpr int kLoads = decltype(loads)::value;
-    for (int i = lane / parts; i < count; i += at_once * kLoads) {
+    const int group = m / rows_per_block, r = m % rows_per_block;
+    float ref = kNinf, l = 0.0f;
+    f32x4 y{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = lane / parts; i0 < count; i0 += at_once * kLoads) {
       float2 w[kLoads];
       f32x4 v[kLoads];
+      bool in[kLoads];
+      float top = ref;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const size_t x = at(min(i + j * at_once, count - 1));
-        w[j] = a.stats[x];
-        v[j] = *reinterpret_cast<const f32x4*>(a.acc + x * (size_t)a.D + (d < a.D ? d : 0));
+        const int i = min(i0 + j * at_once, count - 1);
+        const size_t at = ((size_t)(i == 0 ? first : next + (i - 1) * step) * a.groups + group) * rows_per_block + r;
+        w[j] = a.stats[at];
+        v[j] = *reinterpret_cast<const f32x4*>(a.acc + at * (size_t)a.D + (d < a.D ? d : 0));
       }
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        if (i + j * at_once >= count || w[j].y == 0.0f) continue;
+        in[j] = i0 + j * at_once < count && w[j].y != 0.0f;  // with a sum of 0 no results were written
+        if (in[j]) top = fmaxf(top, w[j].x);
+      }
+      const float old = ref == kNinf ? 0.0f : exp2_of(ref - top);
+      ref = top;
+      l *= old;
+      y *= old;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
         const float f = w[j].x == kNinf ? 1.0f : exp2_of(w[j].x - ref);
-        l += w[j].y * f;
-        y += v[j] * f;
+        l += in[j] ? w[j].y * f : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += in[j] ? v[j][e] * f : 0.0f;
       }
     }
+    float top = ref;
+    for (int o = parts; o < kWave; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+    const float f = ref == kNinf ? 1.0f : exp2_of(ref - top);  // -inf: nothing, or a sum that is NaN
+    l *= f;
+    y *= f;
+    for (int o = parts; o < kWave; o *= 2) {
+      l += __shfl_xor(l, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] += __shfl_xor(y[i], o);
+    }
+    if (lane >= parts || d >= a.D) return;
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = l == 0.0f ? 0.0f : l != l ? l : y[i] * inv;
+    const int nd = m / a.G;
+    const size_t to = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
+    if constexpr (std::is_same<T, float>::value) {
+      typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
+      *reinterpret_cast<quad*>(static_cast<float*>(a.out) + to) = quad{y[0], y[1], y[2], y[3]};
+    } else {
+      typedef uint32_t pair2 __attribute__((ext_vector_type(2), aligned(2)));
+      *reinterpret_cast<pair2*>(static_cast<uint16_t*>(a.out) + to) = pair2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+    }
   };
-  if (count > 4 * at_once) add(std::integral_constant<int, 8>{});
-  else add(std::integral_constant<int, 2>{});
-  for (int o = parts; o < kWave; o *= 2) {
-    l += __shfl_xor(l, o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] += __shfl_xor(y[i], o);
-  }
-  if (lane >= parts || d >= a.D) return;
-  const float inv = 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = bad ? __builtin_nanf("") : l == 0.0f ? 0.0f : y[i] * inv;
-  const int nd = m / a.G;
-  const size_t to = (((size_t)b * a.N + nd) * a.Hq + h * a.G + (m - nd * a.G)) * (size_t)a.D + d;
-  if constexpr (std::is_same<T, float>::value) {
-    typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
-    *reinterpret_cast<quad*>(static_cast<float*>(a.out) + to) = quad{y[0], y[1], y[2], y[3]};
+  const int m1 = min(a.R, m0 + rows);
+  if (count > 4 * at_once) {
+    for (int m = m0; m < m1; ++m) join(m, std::integral_constant<int, 8>{});
   } else {
-    typedef uint32_t pair2 __attribute__((ext_vector_type(2), aligned(2)));
-    *reinterpret_cast<pair2*>(static_cast<uint16_t*>(a.out) + to) = pair2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+#pragma unroll 2
+    for (int m = m0; m < m1; ++m) join(m, std::integral_constant<int, 2>{});
   }
 }
 
@@ -1190,8 +1202,9 @@ hipError_t run(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   else start_rows<T, kQ, 256>(a, p, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.ranges == 0 && p.split == 1)) return e;
-  const dim3 grid((unsigned)((a.R + kWavesPerBlock - 1) / kWavesPerBlock), (unsigned)(a.B * a.Hkv));
-  hipLaunchKernelGGL((tree_join_kernel<T>), grid, dim3(kBlock), 0, st, a, p.rows);
+  const int per_block = p.join_rows * kWavesPerBlock;
+  const dim3 grid((unsigned)((a.R + per_block - 1) / per_block), (unsigned)(a.B * a.Hkv));
+  hipLaunchKernelGGL((tree_join_kernel<T>), grid, dim3(kBlock), 0, st, a, p.rows, p.join_rows);
   return hipGetLastError();
 }
 

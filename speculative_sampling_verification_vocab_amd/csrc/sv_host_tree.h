@@ -28,6 +28,7 @@ struct AttnPlan {
   int32_t step;    // and whose multiple it has: a tile per wave, where these have keys of their own
   int32_t span;    // keys of a tile
   unsigned grid;
+  int32_t join_rows;         // rows that a wave joins
   size_t slots;              // partial results of a group
   size_t stats, acc, total;  // workspace byte offsets
 };
@@ -37,6 +38,8 @@ constexpr int kAttnBlocksWanted = 512;  // 2 per CU
 constexpr int kAttnLeastKeys = 256;     // keys of a piece or range at least
 constexpr int kAttnMostKeys = 2048;     // keys of a piece at most, where sequences differ in length
 
+constexpr size_t kAttnJoinWaves = 16384;  // of the launch that joins partial results, where there are so many rows
+
 // How the keys are shared out, with times at 32 query heads on 8 KV heads of 128:
 //  - a block per pair of sequence and KV head up to 1024 keys (B=1 N=4 L=1000: 15.7 us, in pieces 20.3), and from
 //    4096 pairs on;
@@ -44,7 +47,7 @@ constexpr int kAttnMostKeys = 2048;     // keys of a piece at most, where sequen
 //    sequences of half to all of L takes 35 us in pieces and 40 in ranges at B=8 N=16 L=4096, 8-bit B=4 N=32 L=16384
 //    59 and 66 us;
 //  - ranges of the batch's keys from there on, which every length fills alike: 8-bit B=64 N=1 L=8192 takes 185 us, a
-//    block per pair 214; bf16 B=64 N=64 L=8192 12 % less.  A block has to find its range first (2 to 3 us), and most
+//    block per pair 214; bf16 B=64 N=64 L=8192 636 and 680.  A block has to find its range first (2 to 3 us), and most
 //    have parts of two pairs.
 // 384 or 768 blocks in place of 512 are slower by 7 to 30 %.
 //
@@ -52,7 +55,7 @@ constexpr int kAttnMostKeys = 2048;     // keys of a piece at most, where sequen
 //  - up to 64 rows: the waves have keys of their own (B=8 N=16 L=4096 35 us, shared 39; 8-bit B=1 N=16 L=131072 80 and
 //    92; bf16 there 119 and 113), 16 rows of them where there are no more;
 //  - from there on shared keys (8-bit B=4 N=32 L=16384 58 us, own 84), 32 rows a wave: with 64 one wave per SIMD is left
-//    and B=64 N=64 L=8192 takes 815 us, not 685.
+//    and B=64 N=64 L=8192 takes 815 us, not 685 (both with a slower join).
 
 inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t L_max,
                                      int32_t window, int32_t sinks, spec_dtype_t dtype, bool aligned, AttnPlan* p,
@@ -94,6 +97,8 @@ inline spec_status_t check_attention(int32_t B, int32_t N, int32_t Hq, int32_t H
     if (B == 1 || seen - (size_t)N <= split * kAttnMostKeys) p->split = (int32_t)split;
     else p->ranges = (int32_t)ranges;
   }
+  const size_t rows_wave = pairs * (size_t)p->R / kAttnJoinWaves;
+  p->join_rows = (int32_t)(rows_wave < 1 ? 1 : rows_wave > 8 ? 8 : rows_wave);
   const size_t items = p->ranges > 0 ? (size_t)p->ranges : pairs * (size_t)p->split;
   p->grid = (unsigned)((items + 7) / 8 * 8 * p->groups);
   p->stats = p->acc = p->total = 0;
