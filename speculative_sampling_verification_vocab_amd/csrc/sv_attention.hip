@@ -1170,7 +1170,6 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_
   if (count > 4 * at_once) {
     for (int m = m0; m < m1; ++m) join(m, std::integral_constant<int, 8>{});
   } else {
-#pragma unroll 2
     for (int m = m0; m < m1; ++m) join(m, std::integral_constant<int, 2>{});
   }
 }
