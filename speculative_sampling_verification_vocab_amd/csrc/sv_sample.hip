@@ -12,8 +12,30 @@
 // the largest weight for each token, is far below the distance of a uniform
 // from its nearest border but for one row in millions.
 //
-// A block of 16 waves does a row.  The cuts are found digit by digit in the
-// ordered bits of the logits, a histogram of counts and weights per pass.
+// A block does a row, in one launch.  Its first pass over the row has the largest
+// logit and what the settings ask for:
+//  - top-k, or min-p alone: the tokens above a bound that at least k of them
+//    reach (the k-th largest of disjoint sets of tokens), as a list in shared
+//    memory, which is then ranked and cut;
+//  - top-p over the whole row: bf16 logits as counts per value, in a table of 30
+//    octaves of both signs, so that exact sums per value give the cut with no
+//    second pass; fp32 ones as weights per upper half, and then those tokens
+//    alone that share the cut's half;
+//  - what neither holds (ties past the list, logits outside the octaves): the
+//    cut digit by digit in the ordered bits, a histogram of counts and weights
+//    per pass over the row.
+// A last pass over the row (out of the L2 or the last level of cache, where a
+// row fits) sums the kept weights in chunks, and the chunk that the uniform
+// falls into is scanned for its token.  A list needs no such pass.
+//
+// Measured (event times of calls one after the other; floor: the logits' bytes
+// at 6.4 TB/s):
+//   2048 x 262144 bf16    greedy 178 us, top 50 195, top-p 430 to 455, all kept 373; floor 168.  The first pass runs at
+//                         6 TB/s where nothing is counted; counting costs an LDS atomic per kept token, and the
+//                         draw's pass reads the row again from memory
+//   64 x 128256 bf16      greedy 9.6 us, top 50 21, top-p 42, all kept 29: a row per CU on a quarter of the CUs, bound
+//                         by what one CU reads and by the barriers of the scans
+//   1 x 32000 fp32        12 us for top 50: latency of a chain of 4 to 6 barriers and two reads
 
 #include "sv_internal.h"
 #include "sv_quant.h"
@@ -27,8 +49,12 @@ constexpr int kChunk = 2048;   // tokens of a chunk, times a factor for rows of 
 constexpr int kChunks = 512;   // chunks
 constexpr int kLoadsT = 4;     // 16-byte vectors of a thread's piece of a segment
 constexpr int kList = 4096;    // candidates
-constexpr int kRanked = 512;   // so many are ranked by counting
-// Where less than one token in so many is kept, weights are computed for those alone.
+// So many are ranked by counting, with every thread of a block of 16 waves, and the others sorted: top 200 with
+// top-p on 64 rows of 128256 35 us and 41 sorted, top 50 21 and 28.  With eight waves counting pays for fewer: top
+// 100 on 300 rows 43 us and 48 sorted, top 200 with top-p 70 counted and 57 sorted.
+constexpr int kRanked = 512, kRankedFewer = 256;
+// Where less than one token in so many is kept, weights are computed for those alone, and else taken from a table of
+// the bf16 values' weights: 64 rows of 128256, all kept 29 us and 40 computed; top-p of 0.9 at T = 0.5 34 and 39.
 constexpr int kSparse = 256;
 // Values by sign and magnitude, in their upper 16 bits (a bf16 value itself): 30
 // octaves, a bin for zero and what is smaller, and one for what is larger.
@@ -944,7 +970,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   const int n = sh.count;
   if (listed && n <= kList) {
     // Ranked: the bits' complements ascend where the logits descend.  Few are ranked by counting, more are sorted.
-    const bool few = n <= kRanked;
+    const bool few = n <= (kT == kSampleThreads ? kRanked : kRankedFewer);
     int size = n;
     uint64_t own_entry = 0;
     uint32_t own_ranks = 0;
