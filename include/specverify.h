@@ -566,13 +566,13 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                cache_len is outside [0, L_max].  What a node does not see has
  *                no effect on it, infinities and NaN included.
  *   workspace    spec_tree_attention_workspace_bytes(), 256-byte aligned (may be
- *                NULL where that is 0): partial results where few rows share
- *                long caches.  The contents need no initialisation.
+ *                NULL where that is 0): partial results where several blocks
+ *                share the keys of a row.  The contents need no initialisation.
  * D is a multiple of 8 up to 256, Hq a multiple of Hkv.  Scores, the softmax's
  * sums and the output are accumulated in fp32; with bf16 the weights are
  * rounded to bf16 for their product with the values.  Results are the same on
- * every call.  One launch, two where the workspace is used.  Any alignment of
- * whole elements works.
+ * every call.  One launch, or two where blocks share keys (the workspace is then
+ * used).  Any alignment of whole elements works.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, negative sizes,
  * a scale, window or sinks out of range, an unknown dtype; SPEC_ERR_UNSUPPORTED
  * for N > SPEC_MAX_NODES, a D or Hq other than said, L_max > 2^30, Hkv * D or Hq
