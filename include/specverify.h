@@ -564,7 +564,8 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                window lets it see them.  Zeros for an absent node, and for
  *                one whose scores are all -inf; NaN for a sequence whose
  *                cache_len is outside [0, L_max].  What a node does not see has
- *                no effect on it, infinities and NaN included.
+ *                no effect on it, infinities and NaN included.  out may be q
+ *                itself; it overlaps no other buffer.
  *   workspace    spec_tree_attention_workspace_bytes(), 256-byte aligned (may be
  *                NULL where that is 0): partial results where several blocks
  *                share the keys of a row.  The contents need no initialisation.
@@ -623,7 +624,8 @@ size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int
  *   tokens       [R] int32 out: the smallest kept id at which the kept weights,
  *                summed in id order, exceed uniforms[r] of their total.  -1 where
  *                the row's largest logit is not finite, the row holds a NaN, or a
- *                setting or the uniform is NaN or out of range.
+ *                setting or the uniform is NaN or out of range.  Overlaps no
+ *                input.
  * Weights are computed in 64 bits and held as whole multiples of 2^-F of the
  * largest one, F = 62 - ceil(log2 V) (at most 50): the result does not depend on
  * the order of any sum, and differs from the exact law's only where a uniform

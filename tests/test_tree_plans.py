@@ -158,6 +158,19 @@ def test_values_that_begin_between_whole_pieces():
         c.check(sv().spec_tree_attention(t[0], k, v, *t[1:]))
 
 
+# ---- in place -------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,L,lens", [(2, 5, 90, None), (2, 40, 300, None), (1, 40, 5000, [4990]), (260, 3, 2100, None)])
+def test_the_output_may_be_the_queries(B, N, L, lens):
+    lens = lengths(B, L, {B - 1: L}) if lens is None else lens
+    c = Case(B, B=B, N=N, Hq=2, Hkv=1, D=64, L=L, lens=lens)
+    want = c.call()
+    t = [x.to(DEV) for x in (c.q, *c.cache, c.k_new, c.v_new, c.parents, c.lens)]
+    got = sv().spec_tree_attention(*t, out=t[0])
+    assert got is t[0] and torch.equal(got, want)
+
+
 # ---- planes ---------------------------------------------------------------------
 
 @pytest.mark.gpu
