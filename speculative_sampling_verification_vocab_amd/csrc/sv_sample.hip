@@ -30,7 +30,7 @@
 //
 // Measured (event times of calls one after the other; floor: the logits' bytes
 // at 6.4 TB/s):
-//   2048 x 262144 bf16    greedy 178 us, top 50 195, top-p 430 to 455, all kept 373; floor 168.  The first pass runs at
+//   2048 x 262144 bf16    greedy 178 us, top 50 195, top-p 430 to 490, all kept 373; floor 168.  The first pass runs at
 //                         6 TB/s where nothing is counted; counting costs an LDS atomic per kept token, and the
 //                         draw's pass reads the row again from memory
 //   64 x 128256 bf16      greedy 9.6 us, top 50 21, top-p 42, all kept 29: a row per CU on a quarter of the CUs, bound

@@ -9,10 +9,11 @@
 // copy needs no launch before it; the entries of a path are scattered in
 // staging and contiguous in the cache.
 //
-// Measured (64 planes, entries of 1024 bf16 values): 256 trees of 16 28.5 us,
-// 4.7 TB/s read and written as a large copy's 4.9, and 29.7 us in 8 bits, 3.5 TB/s,
-// where the walk's chain of loads and the codes' arithmetic show; one tree of 8
-// 3.8 and 4.7 us, two dependent loads and a launch.
+// Measured (64 planes, entries of 1024 bf16 values, staging from memory): 256
+// trees of 16 34 us, 3.9 TB/s read and written of a large copy's 4.9, and in 8 bits
+// 34 us too, 3.0 TB/s, where the walk's chain of loads and the codes' arithmetic
+// show (28 and 29 us where the memory-side cache has the staging); one tree of 8
+// 3.5 and 4.5 us, two dependent loads and a launch.
 
 #include <type_traits>
 
@@ -144,7 +145,11 @@ __global__ void __launch_bounds__(kBlock) tree_commit_kernel(TreeCommitArgs a, i
         int p, r;
         const int u = pieces.place(i, p, r);
         const size_t pb = (size_t)(plane0 + p) * a.B + b;
-        d[(pb * a.L + head[1] + r) * a.units + u] = v[k];
+        U* to = d + (pb * a.L + head[1] + r) * a.units + u;
+        // Nontemporal whole vectors: 512 and 256 trees whose staging comes from memory 60 and 34 us, else 72 and 40; 64
+        // trees and fewer the same.
+        if constexpr (kUnit == 16) __builtin_nontemporal_store(v[k], to);
+        else *to = v[k];
       }
     }
   }
