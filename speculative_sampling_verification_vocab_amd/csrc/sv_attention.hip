@@ -560,15 +560,17 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
       depth_of[lane] = t.depth;
     }
 
-    // The rows' queries: row m is node m / G, head m % G of the KV head's G.
+    // The rows' queries: row m is node m / G, head m % G of the KV head's G.  Rows past the last have zeros: any query
+    // read in their place would be another block's row, which that block may be writing (out is q).
     const int row0 = (kShared ? group * kWavesPerBlock + wave : group) * 16 * MT;
     Frag<T, S::KW> q[MT][S::KS];
     int node[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int m = row0 + t * 16 + (lane & 15);
-      node[t] = m < a.R ? m / a.G : 0;
-      const int head = h * a.G + (m < a.R ? m - node[t] * a.G : 0);
+      const bool is_row = m < a.R;
+      node[t] = is_row ? m / a.G : 0;
+      const int head = h * a.G + (is_row ? m - node[t] * a.G : 0);
       const size_t row = ((size_t)b * a.N + node[t]) * a.Hq + head;
       const uint8_t* p = static_cast<const uint8_t*>(a.q) + row * (size_t)a.D * kEs<T>;
 #pragma unroll
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
           constexpr int w = S::KW > 8 ? 8 : S::KW;
           const int d = s * 4 * S::KW + g * S::KW + e;
           Frag<T, w> f;
-          if (kWhole || d < a.D) load_values<T, w>(p + d * kEs<T>, f);
+          if (is_row && (kWhole || d < a.D)) load_values<T, w>(p + d * kEs<T>, f);
           else clear(f);
 #pragma unroll
           for (int i = 0; i < Frag<T, w>::kWords; ++i) q[t][s].w[e * kEs<T> / 4 + i] = f.w[i];
