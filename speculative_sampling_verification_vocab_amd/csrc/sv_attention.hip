@@ -1,9 +1,9 @@
 // Attention of a tree of drafted tokens over a KV cache and the tree's own
 // entries (gfx950, wave64).  For node i and query head h of KV head k:
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(c q.k_j - m),  c = scale * log2(e),
-// over the entries j that node i sees, with m a running reference: when a
-// tile's largest c q.k_j passes m by more than 8, m becomes that maximum and
-// what was summed is scaled down; otherwise p_j <= 2^8 and nothing is.
+// over the entries j that node i sees, with m a running reference, each row's
+// own: when a tile's largest c q.k_j passes m by more than 8, m becomes that
+// maximum and what was summed is scaled down; otherwise p_j <= 2^8 and nothing is.
 //
 // The rows of a KV head are its G query heads of every node.  Four waves of a
 // block take 16 MT rows each against keys of their own, 32 at a time, and a
@@ -348,8 +348,8 @@ __device__ __forceinline__ void cut_key(int D, int s, int lane, Frag<T, S::KW>& 
 }
 
 // Scores to weights: x[t][u][r] is row t * 16 + lane % 16's product with key 16 u + 4 g + r.  seen: null, or
-// bit i says whether the row sees the lane's slot i.  The references move where a row's largest score passes its own
-// by more than the slack.
+// bit i says whether the row sees the lane's slot i.  A row's reference moves where its largest score passes it by
+// more than the slack.
 template <typename S, int MT, bool kMasked>
 __device__ __forceinline__ void weigh(f32x4 (&x)[MT][S::U], const uint32_t (&seen)[MT], float c, Sums<S, MT>& z) {
   float top[MT];
@@ -370,8 +370,8 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[MT][S::U], const uint32_t (&see
     for (int t = 0; t < MT; ++t) {
       float w = fmaxf(top[t], __shfl_xor(top[t], 16));
       w = fmaxf(w, __shfl_xor(w, 32));
-      const float m = fmaxf(z.m[t], w);
-      const float f = m == kNinf ? 1.0f : exp2_of(z.m[t] - m);
+      const float m = w > z.m[t] + kSlack ? w : z.m[t];  // each row by its own scores: others' are not seen
+      const float f = m == z.m[t] ? 1.0f : exp2_of(z.m[t] - m);
       z.m[t] = m;
       z.l[t] *= f;
 #pragma unroll
