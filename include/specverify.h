@@ -564,8 +564,10 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                window lets it see them.  Zeros for an absent node, and for
  *                one whose scores are all -inf; NaN for a sequence whose
  *                cache_len is outside [0, L_max].  What a node does not see has
- *                no effect on it, infinities and NaN included.  out may be q
- *                itself; it overlaps no other buffer.
+ *                no effect on it, infinities and NaN included.  An infinite value
+ *                that it sees gives infinity, and NaN where its score is -inf (one or
+ *                the other with a weight below fp32's range, 2^-126 of the largest).
+ *                out may be q itself; it overlaps no other buffer.
  *   workspace    spec_tree_attention_workspace_bytes(), 256-byte aligned (may be
  *                NULL where that is 0): partial results where several blocks
  *                share the keys of a row.  The contents need no initialisation.

@@ -41,7 +41,9 @@
 //
 // Entries that a row does not see weigh exactly 0 whatever they hold: their
 // score is replaced, and where a tile with such entries has a value that is not
-// finite, that value is left out of the product and added to the rows that see it.
+// finite, that value is left out of the product and its own product with the
+// weight added to the rows that see it: an infinity or a NaN, and NaN for an
+// infinity of weight 0, as the matrix product has it for tiles seen whole.
 
 #include <type_traits>
 
@@ -631,8 +633,9 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
         x[t][u] = product<T, S::KW>(f, q[t][s], s == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[t][u]);
     };
     // Tiles that some row does not see all of: values that are not finite are taken out of the product (bits of the
-    // slots that had some), and added to the rows that see them: an infinity or NaN outweighs whatever its weight is.
-    // value(key, d): the CW values from d on.
+    // slots that had some), and their products with the weights added to the rows that see them: an infinity or NaN
+    // itself, but NaN for an infinity whose weight is 0.  marks: bit i where the row sees slot i, bit 16 + i where its
+    // weight is 0.  value(key, d): the CW values from d on.
     auto take_out = [&](typename S::Values& v) {
       uint32_t bad = 0;
 #pragma unroll
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
           }
       return bad;
     };
-    auto add_others = [&](uint32_t bad, const uint32_t (&seen)[MT], int lane, auto value) {
+    auto add_others = [&](uint32_t bad, const uint32_t (&marks)[MT], int lane, auto value) {
       const int g = lane >> 4;
       if (!__any(bad != 0)) return;
 #pragma unroll 1
@@ -662,14 +665,15 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
             const Frag<T, S::CW> f = value(key, d < a.D ? d : 0);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-              const bool sees = __shfl(seen[t], group16 * 16 + (lane & 15)) >> slot & 1;
+              const uint32_t mark = __shfl(marks[t], group16 * 16 + (lane & 15)) >> slot;
 #pragma unroll
               for (int j = 0; j < S::CW; ++j) {
                 uint32_t w;
                 if constexpr (S::kF32) w = f.w[j];
                 else w = j & 1 ? f.w[j / 2] & 0xffff0000u : f.w[j / 2] << 16;
-                const bool add = sees && (w & 0x7f800000u) == 0x7f800000u;
-                z.o[t][s * S::CW + j][r] += add ? __uint_as_float(w) : 0.0f;
+                const bool add = (mark & 1) && (w & 0x7f800000u) == 0x7f800000u;
+                w |= mark >> 16 & 1 ? 0x7fc00000u : 0u;  // 0 times an infinity
+                z.o[t][s * S::CW + j][r] += add ? __uint_as_float(w) : -0.0f;  // -0 leaves every sum as it is
               }
             }
             __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers
@@ -937,6 +941,18 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
         }
       }
       const uint32_t bad = take_out(v);
+      if (__any(bad != 0)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t zero = 0;
+#pragma unroll
+          for (int i = S::kSlots - 1; i >= 0; --i) {
+            zero = zero << 1 | (x[t][i / 4][i % 4] == 0.0f ? 1u : 0u);
+            asm("" : "+v"(zero));  // as shifts: a constant for each bit would be kept in a register through the loop
+          }
+          seen[t] |= zero << 16;
+        }
+      }
 #pragma unroll
       for (int s = 0; s < S::VS; ++s) {
         Frag<T, S::CW> piece[S::kSlots];
@@ -988,7 +1004,7 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[e] = z.o[t][s * S::CW + j + e][r4];
               if (!alone) {
-                if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + r) * (size_t)a.D + d) = y;
+                *reinterpret_cast<f32x4*>(a.acc + (slot + r) * (size_t)a.D + d) = y;
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
@@ -1025,7 +1041,7 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
               for (int j = 0; j < S::CW; j += 4) {
                 f32x4 y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = z.l[t] == 0.0f ? 0.0f : z.o[t][s * S::CW + j + i][r4] * f;
+                for (int i = 0; i < 4; ++i) y[i] = z.o[t][s * S::CW + j + i][r4] * f;
                 *reinterpret_cast<f32x4*>(to + s * 16 * S::CW + (g * 4 + r4) * S::CW + j) = y;
               }
         }
@@ -1052,7 +1068,7 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
           if (!valid) l = __builtin_nanf("");
           if (line_of[nd] == 0) l = 0.0f;
           if (!alone) {
-            if (l != 0.0f) *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
+            *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
             if (d == 0) a.stats[slot + t * 16 + r] = float2{l == 0.0f ? kNinf : ref, l};
             continue;
           }
@@ -1129,7 +1145,7 @@ __global__ void __launch_bounds__(kBlock) tree_join_kernel(AttnArgs a, int rows_
       }
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        in[j] = i0 + j * at_once < count && w[j].y != 0.0f;  // with a sum of 0 no results were written
+        in[j] = i0 + j * at_once < count;  // with a sum of 0 too: its results are zeros, or NaN by 0 times an infinity
         if (in[j]) top = fmaxf(top, w[j].x);
       }
       const float old = ref == kNinf ? 0.0f : exp2_of(ref - top);
