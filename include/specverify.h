@@ -572,7 +572,9 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                NULL where that is 0): partial results where several blocks
  *                share the keys of a row.  The contents need no initialisation.
  * D is a multiple of 8 up to 256, Hq a multiple of Hkv.  Scores, the softmax's
- * sums and the output are accumulated in fp32; with bf16 the weights are
+ * sums and the output are accumulated in fp32: a score times log2(e) beyond its
+ * range is infinite (a row with +inf is NaN), and values of which L_max + N times
+ * 2^8 pass it may sum to infinity; with bf16 the weights are
  * rounded to bf16 for their product with the values.  Results are the same on
  * every call.  One launch, or two where blocks share keys (the workspace is then
  * used).  Any alignment of whole elements works.

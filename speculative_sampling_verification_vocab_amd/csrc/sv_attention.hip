@@ -76,7 +76,7 @@ struct AttnArgs {
 
 constexpr int kStage = kAttnStage;  // keys that the waves of a block share
 constexpr float kSlack = 8.0f;      // how far a weight's exponent may pass its reference
-constexpr float kNinf = -__builtin_inff();
+constexpr float kNinf = -__builtin_inff(), kMost = 3.402823466e38f;  // the largest float
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -372,7 +372,9 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[MT][S::U], const uint32_t (&see
     for (int t = 0; t < MT; ++t) {
       float w = fmaxf(top[t], __shfl_xor(top[t], 16));
       w = fmaxf(w, __shfl_xor(w, 32));
-      const float m = w > z.m[t] + kSlack ? w : z.m[t];  // each row by its own scores: others' are not seen
+      // Each row by its own scores: others' are not seen.  A score that c takes out of range leaves a finite reference,
+      // so that its weight is infinite and the row NaN; with an infinite one its weight would be 0.
+      const float m = w > z.m[t] + kSlack ? fminf(w, kMost) : z.m[t];
       const float f = m == z.m[t] ? 1.0f : exp2_of(z.m[t] - m);
       z.m[t] = m;
       z.l[t] *= f;

@@ -132,3 +132,17 @@ def test_infinities_at_a_windows_edge_and_in_the_tree(dtype, own):
     k[0, at, :, 0] = 0.0
     got = c.call(window=9)
     assert (got[0, sees][..., 3] == float("inf")).all() and torch.isfinite(got[0, blind]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 40, 9000])
+@pytest.mark.parametrize("N", [1, 40])
+def test_scores_beyond_fp32_are_nan_not_a_finite_answer(dtype, N, n):
+    """scale * q.k * log2(e) that overflows counts as +inf, whose softmax is NaN."""
+    c = Case(44, B=1, N=N, Hq=2, Hkv=1, D=8, L=n, lens=[n], parents=[[-1] * N], dtype=dtype)
+    c.q[..., 0] = 1.6e19
+    c.cache[0][..., 0] = 0.0
+    c.k_new[..., 0] = 0.0
+    c.cache[0][0, n // 2, 0, 0] = 1.6e19
+    assert torch.isnan(c.call(scale=1.0)).all()
