@@ -553,7 +553,7 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                the commit's staging).
  *   parents      [B, N] int32.
  *   cache_len    [B] int32: the sequences' cached entries.
- *   scale        finite, > 0 (usually D^-0.5).
+ *   scale        > 0 (usually D^-0.5), and finite times log2(e).
  *   window       0: none.  W > 0: a node sees positions above its own - W only,
  *                and the first `sinks`.  Node i's position is cache_len[b] + its
  *                number of ancestors; cache entry j's is j.

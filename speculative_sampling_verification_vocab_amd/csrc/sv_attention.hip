@@ -1264,7 +1264,7 @@ hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, 
   a.span = plan.span;
   a.window = window;
   a.sinks = sinks;
-  a.c = scale * 1.44269504088896340736f;
+  a.c = scale * kLog2e;
   if (dtype == 1) return quantized ? run<uint16_t, true>(a, plan, st) : run<uint16_t, false>(a, plan, st);
   return quantized ? run<float, true>(a, plan, st) : run<float, false>(a, plan, st);
 }

@@ -7,6 +7,7 @@
 namespace sv {
 
 constexpr int kMaxNodes = SPEC_MAX_NODES;
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int32_t kMaxLength = 1 << 30;  // cache positions: sums with depths and windows stay in int32
 
 // ---- attention ------------------------------------------------------------------
@@ -142,7 +143,7 @@ inline spec_status_t validate_attention(const AttnPointers& a, bool quantized, i
   if (sw != SPEC_OK) return sw;
   // Values go to shared memory in whole 16-byte pieces.
   const bool aligned = quantized || ((uintptr_t)a.k_cache % 16 == 0 && (uintptr_t)a.v_cache % 16 == 0);
-  if (!(scale > 0.0f && isfinite(scale)) || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
+  if (!(scale > 0.0f && isfinite(scale * kLog2e)) || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
   const spec_status_t sc = check_attention(B, N, Hq, Hkv, D, L_max, window, sinks, dtype, aligned, p, empty);
   if (sc != SPEC_OK) return sc;
   if (*empty) return SPEC_OK;
