@@ -393,8 +393,10 @@ __device__ __forceinline__ int draw(const T* row, int V, int factor, const Weigh
       __syncthreads();
     }
   }
-  // Ties' place in the table; a cut at no bf16 value (min-p's) has none.
-  const uint32_t tie_at = all || (__float_as_uint(value) & 0xffffu) ? ~0u : 8u * (uint32_t)table_bin(__float_as_uint(value) >> 16);
+  // Ties' place in the table.  A min-p cut at no bf16 value has none, nor one beyond the octaves, whose bin is that of
+  // zeros or of all that is larger.
+  const uint32_t bits = __float_as_uint(value), octave = (bits >> 16 & 0x7fffu) - (uint32_t)kLeast;
+  const uint32_t tie_at = all || (bits & 0xffffu) || octave >= kOctaves * 128u ? ~0u : 8u * (uint32_t)table_bin(bits >> 16);
   // A wave's chunks, two vectors at a time, the next ones on their way.
   constexpr int kGroup = 2;
   const int steps = (size + kWave * n * kGroup - 1) / (kWave * n * kGroup);  // of a chunk
