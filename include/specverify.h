@@ -567,7 +567,7 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                no effect on it, infinities and NaN included.  An infinite value
  *                that it sees gives infinity, and NaN where its score is -inf (one or
  *                the other with a weight below fp32's range, 2^-126 of the largest).
- *                out may be q itself; it overlaps no other buffer.
+ *                out may be q itself; it overlaps no other buffer, nor does the workspace.
  *   workspace    spec_tree_attention_workspace_bytes(), 256-byte aligned (may be
  *                NULL where that is 0): partial results where several blocks
  *                share the keys of a row.  The contents need no initialisation.
@@ -578,8 +578,8 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  * rounded to bf16 for their product with the values.  Results are the same on
  * every call.  One launch, or two where blocks share keys (the workspace is then
  * used).  Any alignment of whole elements works.
- * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, negative sizes,
- * a scale, window or sinks out of range, an unknown dtype; SPEC_ERR_UNSUPPORTED
+ * Errors: SPEC_ERR_INVALID_ARG for NULL, misaligned or overlapping buffers,
+ * negative sizes, a scale, window or sinks out of range, an unknown dtype; SPEC_ERR_UNSUPPORTED
  * for N > SPEC_MAX_NODES, a D or Hq other than said, L_max > 2^30, Hkv * D or Hq
  * > 2^22, or sizes too large for one launch; SPEC_ERR_WORKSPACE.
  */

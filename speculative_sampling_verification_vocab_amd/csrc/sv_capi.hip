@@ -379,6 +379,8 @@ spec_status_t tree_attention(const sv::AttnPointers& io, bool quantized, int32_t
   const spec_status_t sc = sv::validate_attention(io, quantized, B, N, Hq, Hkv, D, L_max, scale, window, sinks, dtype,
                                                   workspace, workspace_bytes, &plan, &empty);
   if (sc != SPEC_OK || empty) return sc;
+  if (sv::attention_overlaps(io, quantized, B, N, Hq, Hkv, D, L_max, dtype, plan, workspace))
+    return SPEC_ERR_INVALID_ARG;
   (void)hipGetLastError();
   const hipError_t e = sv::launch_tree_attention(io, quantized, B, N, Hq, Hkv, D, L_max, scale, window, sinks,
                                                  dtype == SPEC_BF16 ? 1 : 0, plan, workspace,

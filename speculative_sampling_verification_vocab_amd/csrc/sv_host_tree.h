@@ -158,6 +158,24 @@ inline spec_status_t validate_attention(const AttnPointers& a, bool quantized, i
   return SPEC_OK;
 }
 
+// What a call writes (its output, and its workspace where it has one) is apart from what it reads and from each other;
+// the output may be the queries themselves.  Of a call that validate_attention took.
+inline bool attention_overlaps(const AttnPointers& a, bool quantized, int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                               int32_t D, int32_t L_max, spec_dtype_t dtype, const AttnPlan& p, const void* workspace) {
+  const size_t es = elem_size(dtype), rows = (size_t)B * N, entries = (size_t)B * L_max, heads = (size_t)Hkv * D;
+  const size_t out = rows * Hq * D * es, own = rows * heads * es, cache = entries * heads * (quantized ? 1 : es);
+  const size_t scales = quantized ? entries * quant_blocks((int32_t)heads) : 0;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } in[] = {{a.k_cache, cache}, {a.v_cache, cache}, {a.k_scales, scales}, {a.v_scales, scales}, {a.k_new, own},
+            {a.v_new, own}, {a.parents, rows * 4}, {a.cache_len, (size_t)B * 4}};
+  for (const auto& i : in)
+    if (overlap(a.out, out, i.at, i.bytes) || overlap(workspace, p.total, i.at, i.bytes)) return true;
+  return (a.out != a.q && overlap(a.out, out, a.q, out)) || overlap(workspace, p.total, a.q, out) ||
+         overlap(workspace, p.total, a.out, out);
+}
+
 // ---- commit of a tree's path ----------------------------------------------------
 
 // What both commits check; the buffers of the cache are the callers'.

@@ -12,3 +12,50 @@ def test_scales_that_overflow_in_the_exponents_base(quantized):
     assert attention.c_call(quantized, scale=2.35e38) == WORKSPACE   # valid, but for the workspace
     for scale in (2.37e38, 3.4e38):
         assert attention.c_call(quantized, scale=scale) == INVALID
+
+
+# ---- outputs that overlap other buffers ------------------------------------------
+# Calls are refused before anything is launched, so that made-up addresses do; those that are taken run on a GPU.
+
+def spans(sizes, start=1 << 40):
+    """Addresses, 256 bytes apart at least, of buffers of these sizes."""
+    at = {}
+    for name, size in sizes.items():
+        at[name] = start
+        start += (size + 511) // 256 * 256
+    return at
+
+
+def attention_sizes(quantized, dt, B=2, N=3, Hq=4, Hkv=2, D=64, L=5000):
+    es = 2 if dt == 1 else 4
+    cache = B * L * Hkv * D * (1 if quantized else es)
+    sizes = dict(q=B * N * Hq * D * es, k=cache, v=cache, kn=B * N * Hkv * D * es, vn=B * N * Hkv * D * es,
+                 par=B * N * 4, n=B * 4, out=B * N * Hq * D * es,
+                 ws=attention.sv()._native.load().spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, L, dt))
+    if quantized:
+        sizes.update(ks=B * L, vs=B * L)
+    return sizes
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_attention_refuses_outputs_over_other_buffers(quantized, dt):
+    """The output's first and last byte in another buffer, and the workspace's."""
+    sizes = attention_sizes(quantized, dt)
+    at = spans(sizes)
+    es = 2 if dt == 1 else 4
+
+    def call(**over):
+        return attention.c_call(quantized, dt=dt, wsb=sizes["ws"], **{**at, **over})
+    for name in at:
+        if name in ("out", "ws"):
+            continue
+        end = at[name] + sizes[name]
+        assert call(out=end - 4) == INVALID, name                                    # the output's beginning
+        assert call(out=at[name] - sizes["out"] + 4) == INVALID, name                # its end
+        ws = (end - 1) // 256 * 256
+        assert call(ws=ws) == INVALID, name
+        assert call(ws=(at[name] - sizes["ws"]) // 256 * 256 + 256) == INVALID, name
+    assert call(out=at["q"] + es) == INVALID and call(out=at["q"] - es) == INVALID   # not the queries themselves
+    assert call(out=at["q"], kn=at["q"]) == INVALID                                  # those alone
+    assert call(out=at["ws"]) == INVALID
