@@ -579,9 +579,10 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  * every call.  One launch, or two where blocks share keys (the workspace is then
  * used).  Any alignment of whole elements works.
  * Errors: SPEC_ERR_INVALID_ARG for NULL, misaligned or overlapping buffers,
- * negative sizes, a scale, window or sinks out of range, an unknown dtype; SPEC_ERR_UNSUPPORTED
- * for N > SPEC_MAX_NODES, a D or Hq other than said, L_max > 2^30, Hkv * D or Hq
- * > 2^22, or sizes too large for one launch; SPEC_ERR_WORKSPACE.
+ * negative sizes, a scale, window or sinks out of range, an unknown dtype;
+ * SPEC_ERR_UNSUPPORTED for N > SPEC_MAX_NODES, a D or Hq other than said, L_max >
+ * 2^30, Hkv * D or Hq > 2^22, or sizes too large for one launch;
+ * SPEC_ERR_WORKSPACE.
  */
 spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache, const void* k_new,
                                   const void* v_new, const int32_t* parents, const int32_t* cache_len, int32_t B,
@@ -635,9 +636,10 @@ size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int
  * the order of any sum, and differs from the exact law's only where a uniform
  * or a cut is nearer than about V * 2^-F to a border.  Results are the same on
  * every call.  One launch.
- * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, R < 0, V < 1, a
- * value for every row that is NaN or out of range, an unknown dtype;
- * SPEC_ERR_UNSUPPORTED for V > 2^30 or a grid too large for one launch.
+ * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, tokens that overlap
+ * an input, R < 0, V < 1, a value for every row that is NaN or out of range, an
+ * unknown dtype; SPEC_ERR_UNSUPPORTED for V > 2^30 or a grid too large for one
+ * launch.
  */
 spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int32_t R, int32_t V, spec_dtype_t dtype,
                                  const float* temperature, float all_temperature, const int32_t* top_k,

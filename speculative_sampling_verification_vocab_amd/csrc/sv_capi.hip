@@ -426,6 +426,7 @@ spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int3
   bool empty = false;
   const spec_status_t sc = sv::validate_sample(logits, uniforms, R, V, dtype, set, tokens, &empty);
   if (sc != SPEC_OK || empty) return sc;
+  if (sv::sample_overlaps(logits, uniforms, R, V, dtype, set, tokens)) return SPEC_ERR_INVALID_ARG;
   (void)hipGetLastError();
   const hipError_t e = sv::launch_sample_tokens(logits, uniforms, R, V, dtype == SPEC_BF16 ? 1 : 0, set, tokens,
                                                 static_cast<hipStream_t>(stream));

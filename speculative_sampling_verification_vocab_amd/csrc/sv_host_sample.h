@@ -43,4 +43,15 @@ inline spec_status_t validate_sample(const void* logits, const float* uniforms, 
   return SPEC_OK;
 }
 
+// The tokens share a byte with what the call reads: a row's block would write where another reads its logits or settings.
+// Of a call that validate_sample took.
+inline bool sample_overlaps(const void* logits, const float* uniforms, int32_t R, int32_t V, spec_dtype_t dtype,
+                            const SampleSettings& set, const int32_t* tokens) {
+  const size_t rows = (size_t)R * 4;
+  const void* const per_row[] = {uniforms, set.temperature.rows, set.top_k.rows, set.top_p.rows, set.min_p.rows};
+  for (const void* p : per_row)
+    if (p && overlap(tokens, rows, p, rows)) return true;
+  return overlap(tokens, rows, logits, (size_t)R * (size_t)V * elem_size(dtype));
+}
+
 }  // namespace sv

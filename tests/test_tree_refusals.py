@@ -1,6 +1,7 @@
 """What the operators of a step with a tree of drafts refuse, beside their own tests (CPU)."""
 import pytest
 
+from tests import test_sample_tokens as sample
 from tests import test_tree_attention as attention
 
 OK, INVALID, WORKSPACE = 0, 1, 3
@@ -59,3 +60,13 @@ def test_attention_refuses_outputs_over_other_buffers(quantized, dt):
     assert call(out=at["q"] + es) == INVALID and call(out=at["q"] - es) == INVALID   # not the queries themselves
     assert call(out=at["q"], kn=at["q"]) == INVALID                                  # those alone
     assert call(out=at["ws"]) == INVALID
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+def test_sampling_refuses_tokens_over_its_inputs(dt):
+    R, V = 5, 130
+    sizes = dict(x=R * V * (2 if dt == 1 else 4), u=R * 4, T=R * 4, k=R * 4, p=R * 4, m=R * 4, out=R * 4)
+    at = spans(sizes)
+    for name in ("x", "u", "T", "k", "p", "m"):
+        for out in (at[name], at[name] + sizes[name] - 4, at[name] - sizes["out"] + 4):
+            assert sample.c_call(R=R, V=V, dt=dt, **{**at, "out": out}) == INVALID, name
