@@ -676,9 +676,9 @@ spec_status_t spec_sample_tokens(const void* logits, const float* uniforms, int3
  * Any alignment of whole elements works; rows of 16-byte multiples in aligned
  * buffers take vectors.
  * Errors: SPEC_ERR_INVALID_ARG for NULL or misaligned buffers, sizes out of
- * range, an unknown dtype, or outputs that overlap each other or an input (but
- * for new_len == cache_len); SPEC_ERR_UNSUPPORTED for N > SPEC_MAX_NODES or a
- * grid too large for one launch.
+ * range, an unknown dtype, or outputs, the cache among them, that overlap each
+ * other or an input (but for new_len == cache_len); SPEC_ERR_UNSUPPORTED for N >
+ * SPEC_MAX_NODES or a grid too large for one launch.
  */
 spec_status_t spec_tree_commit(void* cache, const void* staging, const int32_t* tokens, const int32_t* parents,
                                const int32_t* sampled, const int32_t* cache_len, int32_t* new_len,

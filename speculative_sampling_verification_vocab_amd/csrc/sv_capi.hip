@@ -442,6 +442,10 @@ spec_status_t spec_tree_commit(void* cache, const void* staging, const int32_t* 
   bool empty = false;
   const spec_status_t sc = sv::validate_tree_commit(cache, staging, io, P, B, N, L_max, E, dtype, &plan, &empty);
   if (sc != SPEC_OK || empty) return sc;
+  const size_t es = sv::elem_size(dtype), planes = (size_t)P * (size_t)B;
+  if (plan.chunks > 0 && sv::tree_commit_overlaps(cache, planes * L_max * E * es, nullptr, 0, staging,
+                                                  planes * N * E * es, io, B, N))
+    return SPEC_ERR_INVALID_ARG;
   (void)hipGetLastError();
   const hipError_t e = sv::launch_tree_commit(cache, staging, io, P, B, N, L_max, E, dtype == SPEC_BF16 ? 2 : 4, plan,
                                               static_cast<hipStream_t>(stream));
@@ -459,6 +463,10 @@ spec_status_t spec_tree_commit_quantized(void* codes, void* scales, const void* 
   const spec_status_t sc =
       sv::validate_tree_commit_quantized(codes, scales, staging, io, P, B, N, L_max, E, dtype, &plan, &empty);
   if (sc != SPEC_OK || empty) return sc;
+  const size_t planes = (size_t)P * (size_t)B;
+  if (plan.copies && sv::tree_commit_overlaps(codes, planes * L_max * E, scales, planes * L_max * plan.nb, staging,
+                                              planes * N * E * sv::elem_size(dtype), io, B, N))
+    return SPEC_ERR_INVALID_ARG;
   (void)hipGetLastError();
   const hipError_t e = sv::launch_tree_commit_quantized(codes, scales, staging, io, P, B, N, L_max, E,
                                                         dtype == SPEC_BF16 ? 1 : 0, plan,

@@ -214,6 +214,28 @@ inline spec_status_t check_tree_commit(const TreeCommitIO& io, int32_t P, int32_
   return SPEC_OK;
 }
 
+// The cache shares a byte with the staging, an input or an output, or the staging with an output: blocks would move
+// what others have written already.  Of a call that a validate_tree_commit took and that has entries to move.
+inline bool tree_commit_overlaps(const void* cache, size_t cache_bytes, const void* scales, size_t scale_bytes,
+                                 const void* staging, size_t staging_bytes, const TreeCommitIO& io, int32_t B,
+                                 int32_t N) {
+  const struct {
+    const void* at;
+    size_t bytes;
+  } lists[] = {{io.new_len, (size_t)B * 4}, {io.accepted_len, (size_t)B * 4}, {io.out_tokens, (size_t)B * N * 4},
+               {io.path, io.path ? (size_t)B * N * 4 : 0}, {io.status, io.status ? (size_t)B * 4 : 0},
+               {io.cache_len, (size_t)B * 4}, {io.tokens, (size_t)B * N * 4}, {io.parents, (size_t)B * N * 4},
+               {io.sampled, (size_t)B * N * 4}};
+  constexpr int kOutputs = 5;
+  for (int i = 0; i < (int)(sizeof(lists) / sizeof(lists[0])); ++i) {
+    if (overlap(cache, cache_bytes, lists[i].at, lists[i].bytes) || overlap(scales, scale_bytes, lists[i].at, lists[i].bytes))
+      return true;
+    if (i < kOutputs && overlap(staging, staging_bytes, lists[i].at, lists[i].bytes)) return true;
+  }
+  return overlap(cache, cache_bytes, staging, staging_bytes) || overlap(scales, scale_bytes, staging, staging_bytes) ||
+         overlap(cache, cache_bytes, scales, scale_bytes);
+}
+
 // Units (16-byte vectors or elements) of a path's entries, in chunks of one
 // block; chunks is 0 where there is nothing to move.
 struct TreeCopyPlan {

@@ -3,6 +3,7 @@ import pytest
 
 from tests import test_sample_tokens as sample
 from tests import test_tree_attention as attention
+from tests import test_tree_commit as commit
 
 OK, INVALID, WORKSPACE = 0, 1, 3
 
@@ -70,3 +71,27 @@ def test_sampling_refuses_tokens_over_its_inputs(dt):
     for name in ("x", "u", "T", "k", "p", "m"):
         for out in (at[name], at[name] + sizes[name] - 4, at[name] - sizes["out"] + 4):
             assert sample.c_call(R=R, V=V, dt=dt, **{**at, "out": out}) == INVALID, name
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_commits_refuse_a_cache_or_staging_over_other_buffers(quantized, dt):
+    P, B, N, L, E = 2, 3, 4, 16, 64
+    es = 2 if dt == 1 else 4
+    sizes = dict(cache=P * B * L * E * (1 if quantized else es), scales=P * B * L, staging=P * B * N * E * es,
+                 tok=B * N * 4, par=B * N * 4, sam=B * N * 4, n=B * 4, new=B * 4, acc=B * 4, out=B * N * 4, path=B * N * 4,
+                 st=B * 4)
+    assert set(sizes) == set(commit.FAR)
+    at = spans(sizes)
+
+    def call(**over):
+        return commit.c_call(quantized, dt=dt, P=P, B=B, N=N, L=L, E=E, **{**at, **over})
+    lists = [n for n in sizes if n not in ("cache", "scales", "staging")]
+    for buf in ["cache", "staging"] + ["scales"] * quantized:
+        for name in lists:
+            if buf == "staging" and name in ("tok", "par", "sam", "n"):
+                continue                                                       # it is read alone, as they are
+            for x in (at[name] + sizes[name] - 4, at[name] - sizes[buf] + 4):
+                assert call(**{buf: x}) == INVALID, (buf, name)
+    for a, b in [("cache", "staging")] + [("scales", "staging"), ("cache", "scales")] * quantized:
+        assert call(**{a: at[b] + sizes[b] - 4}) == INVALID and call(**{a: at[b] - sizes[a] + 4}) == INVALID
