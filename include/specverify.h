@@ -562,8 +562,8 @@ spec_status_t spec_kv_read_quantized(const void* codes, const void* scales, cons
  *                h / (Hq / Hkv), sum_j softmax_j(scale * q.k_j) v_j over the cache
  *                entries j and the node's ancestors and itself, as far as the
  *                window lets it see them.  Zeros for an absent node, and for
- *                one whose scores are all -inf; NaN for a sequence whose
- *                cache_len is outside [0, L_max].  What a node does not see has
+ *                one whose scores are all -inf; NaN for all nodes of a sequence
+ *                whose cache_len is outside [0, L_max].  What a node does not see has
  *                no effect on it, infinities and NaN included.  An infinite value
  *                that it sees gives infinity, and NaN where its score is -inf (one or
  *                the other with a weight below fp32's range, 2^-126 of the largest).

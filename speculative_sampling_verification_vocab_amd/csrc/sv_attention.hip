@@ -989,8 +989,8 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
         l += __shfl_xor(l, 32);
         const int r = t * 16 + (lane & 15), m = row0 + r;
         if (m >= a.R) continue;
-        if (!valid) l = __builtin_nanf("");
         if (line_of[node[t]] == 0) l = 0.0f;
+        if (!valid) l = __builtin_nanf("");
         const float inv = 1.0f / l;
         const size_t to = (((size_t)b * a.N + node[t]) * a.Hq + h * a.G + (m - node[t] * a.G)) * (size_t)a.D;
         if (!alone && g == 0) a.stats[slot + r] = float2{l == 0.0f ? kNinf : z.m[t], l};
@@ -1067,8 +1067,8 @@ __global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && 
             l += s.x == kNinf ? s.y : s.y * exp2_of(s.x - ref);
           }
           const int nd = m / a.G;
-          if (!valid) l = __builtin_nanf("");
           if (line_of[nd] == 0) l = 0.0f;
+          if (!valid) l = __builtin_nanf("");
           if (!alone) {
             *reinterpret_cast<f32x4*>(a.acc + (slot + t * 16 + r) * (size_t)a.D + d) = y;
             if (d == 0) a.stats[slot + t * 16 + r] = float2{l == 0.0f ? kNinf : ref, l};

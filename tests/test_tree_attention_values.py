@@ -146,3 +146,15 @@ def test_scores_beyond_fp32_are_nan_not_a_finite_answer(dtype, N, n):
     c.k_new[..., 0] = 0.0
     c.cache[0][0, n // 2, 0, 0] = 1.6e19
     assert torch.isnan(c.call(scale=1.0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [5, 40])
+@pytest.mark.parametrize("L", [30, 4000])
+def test_a_bad_length_makes_absent_nodes_nan_too(N, L):
+    """A sequence whose length cannot be is NaN as a whole, as in the plain form; another's absent nodes are zeros."""
+    parents = [[-1, 0, -2, 2] + [0] * (N - 4)] * 3
+    c = Case(45, B=3, N=N, Hq=4, Hkv=2, L=L, lens=[L + 1, L, -1], parents=parents)
+    got = c.call()
+    assert torch.isnan(got[[0, 2]]).all() and torch.isfinite(got[1]).all() and not got[1, 2:4].any()
+    c.check(got)
