@@ -30,8 +30,8 @@
 // Measured (32 query heads on 8 KV heads of 128, half to all of L cached):
 //   B=64 N=1 L=8192 bf16      299 us  5.4 TB/s: the cache's bytes, of 6.0 to 6.4 that reads alone reach
 //   B=32 N=8 L=8192 bf16      184 us  4.4 TB/s, and 8-bit 122 us, 3.4 TB/s
-//   B=1 N=16 L=131072 bf16    119 us  4.5 TB/s, and 8-bit 80 us, 3.4 TB/s: the registers leave two waves per
-//                             SIMD, and the loads that those have in flight bound it
+//   B=1 N=16 L=131072 bf16    119 us  4.5 TB/s, and 8-bit 78 to 92 us by machine, 2.9 to 3.5 TB/s: the registers leave
+//                             two waves per SIMD, and the loads that those have in flight bound it
 //   B=64 N=64 L=8192 bf16     636 us  655 TFLOP/s of 1130 that a large product reaches: softmax and permutes
 //                             share the issue slots with the matrix instructions
 //
@@ -507,7 +507,7 @@ constexpr int kPad = DP + 4;
 
 // kShared: every wave has 16 MT rows of its own, and all take the same keys, 64 at a time from shared memory.
 template <typename T, bool kQ, int DP, int MT, bool kWhole, bool kShared>
-__global__ void __launch_bounds__(kBlock, MT == 4 || DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2)
+__global__ void __launch_bounds__(kBlock, DP == 256 || (DP == 128 && std::is_same<T, float>::value) ? 1 : 2)
     tree_attention_kernel(AttnArgs a) {
   typedef Shape<T, kQ && !kShared, DP, MT, kWhole> S;
   __shared__ uint64_t line_of[kMaxNodes];

@@ -447,8 +447,7 @@ spec_status_t spec_tree_commit(void* cache, const void* staging, const int32_t* 
                                                   planes * N * E * es, io, B, N))
     return SPEC_ERR_INVALID_ARG;
   (void)hipGetLastError();
-  const hipError_t e = sv::launch_tree_commit(cache, staging, io, P, B, N, L_max, E, dtype == SPEC_BF16 ? 2 : 4, plan,
-                                              static_cast<hipStream_t>(stream));
+  const hipError_t e = sv::launch_tree_commit(cache, staging, io, P, B, N, L_max, plan, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 

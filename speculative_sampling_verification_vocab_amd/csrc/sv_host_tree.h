@@ -54,7 +54,8 @@ constexpr size_t kAttnJoinWaves = 16384;  // of the launch that joins partial re
 //
 // Which rows a block has, in the same terms:
 //  - up to 64 rows: the waves have keys of their own (B=8 N=16 L=4096 35 us, shared 39; 8-bit B=1 N=16 L=131072 80 and
-//    92; bf16 there 119 and 113), 16 rows of them where there are no more;
+//    92 on one machine), 16 rows of them where there are no more.  One rule for both types, which the 8-bit cache's
+//    figure decides: bf16 values at that length would gain 5 % by sharing (119 and 113 us);
 //  - from there on shared keys (8-bit B=4 N=32 L=16384 58 us, own 84), 32 rows a wave: with 64 one wave per SIMD is left
 //    and B=64 N=64 L=8192 takes 815 us, not 685 (both with a slower join).
 

@@ -75,15 +75,15 @@ hipError_t launch_logprobs(const LogprobsShape& s, const LogprobsWorkspace& w, c
                            const int32_t* tokens, int dtype, float temperature, float* logprobs, float* entropy,
                            int32_t* top_ids, float* top_logprobs, void* workspace, hipStream_t st);
 
-// Attention of a tree over the cache: one launch, and with plan.split > 1 the
-// join of the splits.
+// Attention of a tree over the cache: one launch, and a second one where blocks
+// share the keys of a row (plan.split > 1 or plan.ranges > 0), which joins them.
 hipError_t launch_tree_attention(const AttnPointers& io, bool quantized, int B, int N, int Hq, int Hkv, int D, int L,
                                  float scale, int window, int sinks, int dtype, const AttnPlan& plan, void* workspace,
                                  hipStream_t st);
 
 // Walk along a tree and commit of its path: one launch, or two when new_len is cache_len.
 hipError_t launch_tree_commit(void* cache, const void* staging, const TreeCommitIO& io, int P, int B, int N, int L,
-                              int E, int elem_bytes, const TreeCopyPlan& plan, hipStream_t st);
+                              const TreeCopyPlan& plan, hipStream_t st);
 hipError_t launch_tree_commit_quantized(void* codes, void* scales, const void* staging, const TreeCommitIO& io, int P,
                                         int B, int N, int L, int E, int dtype, const KvQPlan& plan, hipStream_t st);
 

@@ -23,7 +23,12 @@
 //    alone that share the cut's half;
 //  - what neither holds (ties past the list, logits outside the octaves): the
 //    cut digit by digit in the ordered bits, a histogram of counts and weights
-//    per pass over the row.
+//    per pass over the row.  One logit other than 0 but nearer to it than 2^-20
+//    sends a row there, which costs bf16 rows several times the table's time
+//    (below); logits of deviation 2.5 around 0 have one in 4 % of rows of 128256
+//    and 8 % of 262144.  So does a temperature at which -2^10 has weight (from
+//    about 30 on) where the row has values of -2^10 or below, or the last
+//    vectors of its read are filled up with -inf behind its end.
 // A last pass over the row (out of the L2 or the last level of cache, where a
 // row fits) sums the kept weights in chunks, and the chunk that the uniform
 // falls into is scanned for its token.  A list needs no such pass.
@@ -36,6 +41,8 @@
 //   64 x 128256 bf16      greedy 9.6 us, top 50 21, top-p 42, all kept 29: a row per CU on a quarter of the CUs, bound
 //                         by what one CU reads and by the barriers of the scans
 //   1 x 32000 fp32        12 us for top 50: latency of a chain of 4 to 6 barriers and two reads
+//   digit by digit        64 x 128256 bf16, top-p, 151 us if one row goes so and 157 if all do, where the table takes 40;
+//                         2048 x 262144 460 us and 2260, by table 426.  fp32 top-p takes 160 to 165 us either way
 
 #include "sv_internal.h"
 #include "sv_quant.h"
@@ -797,7 +804,7 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
                                    : smallest < ((uint32_t)kLeast << 16) - 1;
   if (tables && tiny) sh.tiny = 1;
   if (tables && (sizeof(T) == 2 ? (largest & 0xffffu) >= 0x4480u || largest >> 16 >= 0x4480u : largest >= 0x44800000u))
-    sh.low = 1;  // a magnitude of 2^10 or more; of the largest, or below
+    sh.low = 1;  // a magnitude of 2^10 or more: of the largest, of one below, or of the fill behind the row's end
   if (counts) {
     __syncthreads();
     if (threadIdx.x == 0) sh.table[0] += sh.table[kHalf], sh.table[kHalf] = 0;
@@ -840,7 +847,8 @@ __global__ void __launch_bounds__(kT, 4) sample_tokens_kernel(SampleArgs a) {
   if (tables) {
     // Values outside the table that have weight, or that a cut may meet, leave the row to its digits.
     const bool weightless = top > -1024.0f && weight(-1024.0f) == 0;
-    const int low = counts ? (int)sh.table[kTable - 1] : sh.low;  // values of -2^10 and below, masked ones among them
+    // Values of -2^10 and below: masked ones, and what fills the last vector behind the row's end.
+    const int low = counts ? (int)sh.table[kTable - 1] : sh.low;
     const bool plain = top < 1024.0f && !sh.tiny && (low == 0 || weightless) && (!by_k || k <= V - low);
     uint64_t kept = (uint64_t)V;  // at most
     if (plain && sizeof(T) == 2 && !done) {

@@ -31,10 +31,9 @@ struct TreeCommitArgs {
   uint32_t chunks;
   int planes;  // of a block
   // values
-  uint8_t* cache;          // [P][B][L][row_bytes]
-  const uint8_t* staging;  // [P][B][N][row_bytes]
-  int64_t row_bytes;
-  int units;
+  uint8_t* cache;          // [P][B][L][units]
+  const uint8_t* staging;  // [P][B][N][units]
+  int units;               // vectors or elements of an entry
   // 8-bit
   uint8_t *codes, *scales;  // [P][B][L][E], [P][B][L][nb]
   const void* in;           // [P][B][N][E]
@@ -219,7 +218,7 @@ hipError_t finish(const TreeCommitArgs& a, bool copied, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_tree_commit(void* cache, const void* staging, const TreeCommitIO& io, int P, int B, int N, int L,
-                              int E, int elem_bytes, const TreeCopyPlan& plan, hipStream_t st) {
+                              const TreeCopyPlan& plan, hipStream_t st) {
   TreeCommitArgs a{};
   a.io = io;
   a.P = P;
@@ -230,7 +229,6 @@ hipError_t launch_tree_commit(void* cache, const void* staging, const TreeCommit
   a.planes = tree_planes(P, B, plan.chunks);
   a.cache = static_cast<uint8_t*>(cache);
   a.staging = static_cast<const uint8_t*>(staging);
-  a.row_bytes = (int64_t)E * elem_bytes;
   a.units = plan.units;
   const bool copies = plan.chunks > 0;
   if (copies) {
